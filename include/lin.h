@@ -453,6 +453,89 @@ LIN_API int lin_forward_fp32_static(int M, int N, int K, const float* X, const f
 LIN_API int lin_attention_forward(lin_ctx* ctx, int B, int T, int H, int D, const void* qkv, void* out, float* lse,
                                   int causal, float scale, void* stream);
 
+/* ---- Operators on the LM head's logits ----
+ * R rows of V logits, row r at logits + r * ld elements (ld >= V: a padded
+ * vocabulary's columns are neither read nor written), z_rj below. Element
+ * types are named by lin_dtype. tau > 0 is a temperature: probabilities are
+ * softmax(z / tau). Maxima, sums and statistics are held in fp32, the
+ * differences from a row's maximum are formed before they are scaled, and
+ * results do not depend on the order in which blocks run (identical inputs
+ * give identical bits). A NaN or +inf among a row's logits makes that row's
+ * results NaN; -inf is a token that cannot occur (probability 0).
+ * Pointers are DEVICE pointers aligned to their elements (LIN_ERR_ALIGN).
+ * LIN_ERR_ARG: a NULL that is not allowed, a negative size, ld < V, an
+ * unknown type, tau not positive and finite, or an output that overlaps an
+ * input or another output (except as said). LIN_ERR_UNSUPPORTED: V > 2^30 or
+ * R > 2^27. R == 0 does nothing; V == 0 with rows is LIN_ERR_ARG. No
+ * workspace. Launched like lin_forward, as a programmatic dependent that reads
+ * and writes only after the previous kernel on the stream has finished. */
+typedef enum {
+    LIN_TYPE_FP32 = 0,
+    LIN_TYPE_BF16 = 1,
+    LIN_TYPE_INT32 = 2,
+    LIN_TYPE_INT64 = 3
+} lin_dtype;
+
+/* Log probabilities of given tokens, with the distribution's entropy and its
+ * top alternatives:
+ *   lse_r     = log sum_j exp(z_rj / tau)
+ *   logprob_r = z_r,token_r / tau - lse_r
+ *   entropy_r = - sum_j p_rj log p_rj          (nats, p = exp(z / tau - lse))
+ *   top_ids[r * top + i]     : the i-th largest logit's index; equal values
+ *                              (zeros of either sign are equal) by the lowest
+ *                              index, NaN ranked with -inf
+ *   top_logprob[r * top + i] : its log probability
+ *   logits_type : LIN_TYPE_FP32 or LIN_TYPE_BF16.
+ *   tokens : R of LIN_TYPE_INT32 or LIN_TYPE_INT64 (tokens_type), or NULL
+ *            (with logprob NULL). A negative token gives logprob 0 (no token
+ *            here), one >= V gives NaN.
+ *   logprob, entropy, lse : R fp32 each; entropy and lse may be NULL, logprob
+ *            if and only if tokens is.
+ *   top    : 0 to 64, at most V; with 0 both top outputs are ignored.
+ * A row whose logits are all -inf: lse and log probabilities -inf, entropy 0. */
+LIN_API int lin_token_logprobs(lin_ctx* ctx, int R, int V, const void* logits, long long ld, int logits_type,
+                               const void* tokens, int tokens_type, float tau, int top, float* logprob,
+                               float* entropy, float* lse, float* top_logprob, int* top_ids, void* stream);
+
+/* Distillation towards a teacher's top logits. Row r has K entries: token
+ * ids[r * K + i] with the teacher's logit (or log probability: a constant
+ * added to a row changes nothing) teacher[r * K + i]. Entries with a negative
+ * id are padding. With
+ *   q = softmax(teacher / tau) over the row's entries,
+ *   p = softmax(z / tau) over the row's V logits,
+ *   loss_r = tau^2 sum_i q_i (log q_i - log p_id(i)),
+ *   dz_rj  = g_r tau (p_rj - sum of the q_i with id(i) = j),
+ * g_r being the gradient that reaches loss_r. Entries may repeat a token. A
+ * row without entries (or whose teacher logits are all -inf) has loss 0 and
+ * gradient 0, and so has the gradient where g_r = 0, whatever the logits are.
+ * An id >= V makes its row's loss and gradient NaN.
+ *   ids     : R x K, LIN_TYPE_INT32 or LIN_TYPE_INT64 (ids_type), 0 <= K <= 1024.
+ *   teacher : R x K, LIN_TYPE_FP32 or LIN_TYPE_BF16 (teacher_type). */
+
+/* loss (R fp32) and, if not NULL, lse (R fp32, log sum exp(z / tau): what
+ * lin_distill_backward needs). */
+LIN_API int lin_distill_forward(lin_ctx* ctx, int R, int V, int K, const void* logits, long long ld, int logits_type,
+                                const void* ids, int ids_type, const void* teacher, int teacher_type, float tau,
+                                float* loss, float* lse, void* stream);
+
+/* dlogits (R rows of V, ldd apart, in the logits' type, one rounding) from the
+ * forward's lse and grad_loss (R fp32: g). dlogits may be the logits
+ * themselves (in place, with ldd == ld). Fast when dlogits and logits start
+ * at the same offset within 16 bytes and (ld - ldd) * element size is a
+ * multiple of 16; right for any. */
+LIN_API int lin_distill_backward(lin_ctx* ctx, int R, int V, int K, const void* logits, long long ld, int logits_type,
+                                 const void* ids, int ids_type, const void* teacher, int teacher_type, float tau,
+                                 const float* lse, const float* grad_loss, void* dlogits, long long ldd,
+                                 void* stream);
+
+/* Both in one pass over the logits, for a loss whose weights are known before
+ * it is computed: weight (R fp32, NULL = 1) is g, loss (not weighted) may be
+ * NULL. dlogits as above. */
+LIN_API int lin_distill_forward_backward(lin_ctx* ctx, int R, int V, int K, const void* logits, long long ld,
+                                         int logits_type, const void* ids, int ids_type, const void* teacher,
+                                         int teacher_type, float tau, const float* weight, float* loss,
+                                         void* dlogits, long long ldd, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 from .build import LIB as _LIB_PATH
 from .build import TIMELINE_LIB as _TIMELINE_LIB_PATH
@@ -22,6 +23,7 @@ from .build import build
 __all__ = [
     "LinError", "Context", "Plan", "forward", "forward_plan", "plan_query", "plan_make", "build",
     "backward_data", "backward_weight", "gelu_backward", "attention_forward",
+    "TokenLogprobs", "token_logprobs", "distill_forward", "distill_backward", "distill_forward_backward",
     "library", "PREC_FP32", "PREC_TF32", "PREC_BF16", "EPI_NONE", "EPI_GELU_TANH",
     "KERNEL_NONE", "KERNEL_FILL", "KERNEL_SKINNY", "KERNEL_FFMA", "KERNEL_TC", "KERNEL_GEMV",
 ]
@@ -38,6 +40,8 @@ OPT_PROGRAMMATIC_LAUNCH = 3
 # stream writes a call's inputs between library calls).
 EARLY_NONE, EARLY_WEIGHTS, EARLY_ALL = 0, 1, 2
 OK, ERR_ARG, ERR_ALIGN, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_TIMEOUT, ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
+# lin_dtype
+TYPE_FP32, TYPE_BF16, TYPE_INT32, TYPE_INT64 = 0, 1, 2, 3
 # LIN_STATIC_SCRATCH_BYTES: the fixed device array behind lin_forward_fp32_static.
 STATIC_SCRATCH_BYTES = 8 << 20
 
@@ -87,6 +91,7 @@ def library() -> ctypes.CDLL:
             lib = ctypes.CDLL(_LIB_PATH)
             P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
             PP = ctypes.POINTER(Plan)
+            L, F = ctypes.c_longlong, ctypes.c_float
             sig = {
                 "lin_create": ([ctypes.POINTER(P), I, Z], I),
                 "lin_destroy": ([P], I),
@@ -111,6 +116,10 @@ def library() -> ctypes.CDLL:
                 "lin_probe_ffma": ([P, I, P, ctypes.POINTER(ctypes.c_double), P], I),
                 "lin_timeline": ([I, P, Z, I], I),
                 "lin_attention_forward": ([P, I, I, I, I, P, P, P, I, ctypes.c_float, P], I),
+                "lin_token_logprobs": ([P, I, I, P, L, I, P, I, F, I, P, P, P, P, P, P], I),
+                "lin_distill_forward": ([P, I, I, I, P, L, I, P, I, P, I, F, P, P, P], I),
+                "lin_distill_backward": ([P, I, I, I, P, L, I, P, I, P, I, F, P, P, P, L, P], I),
+                "lin_distill_forward_backward": ([P, I, I, I, P, L, I, P, I, P, I, F, P, P, P, L, P], I),
                 "lin_strerror": ([I], ctypes.c_char_p),
                 "lin_abi_version": ([], I),
             }
@@ -548,3 +557,178 @@ def attention_forward(qkv, B: int, T: int, H: int, causal: bool = True, scale: f
     if rc != OK:
         raise LinError(rc, "lin_attention_forward")
     return (out, lse) if lse is not None else out
+
+
+# ---------------------------------------------------------------- logits
+
+class TokenLogprobs(NamedTuple):
+    """Result of :func:`token_logprobs` (fp32, ids int32)."""
+
+    logprob: object       # R, or None without tokens
+    entropy: object       # R
+    lse: object           # R
+    top_logprob: object   # R x top
+    top_ids: object       # R x top
+
+
+def _float_type(t, what):
+    import torch
+
+    if t.dtype == torch.float32:
+        return TYPE_FP32
+    if t.dtype == torch.bfloat16:
+        return TYPE_BF16
+    raise TypeError(f"{what} must be fp32 or bf16, got {t.dtype}")
+
+
+def _index_type(t, what):
+    import torch
+
+    if t.dtype == torch.int32:
+        return TYPE_INT32
+    if t.dtype == torch.int64:
+        return TYPE_INT64
+    raise TypeError(f"{what} must be int32 or int64, got {t.dtype}")
+
+
+def _check_logits(t, what="logits"):
+    """(rows, V, row stride) of an R x V tensor whose rows are contiguous."""
+    if not t.is_cuda or t.dim() != 2 or t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be an R x V CUDA tensor (V >= 1) with contiguous rows")
+    R, V = t.shape
+    ld = t.stride(0) if R > 1 else V
+    if ld < V:
+        raise ValueError(f"{what}: rows overlap")
+    return R, V, ld
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"all tensors must be on {first.device}, got one on {t.device}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def token_logprobs(logits, tokens=None, top: int = 0, temperature: float = 1.0, ctx: Context | None = None,
+                   stream=None) -> TokenLogprobs:
+    """Log probability of ``tokens[r]`` under softmax(logits[r] / temperature),
+    the distribution's entropy (nats), and its ``top`` (at most 64) most likely
+    tokens in order, equal logits by the lowest index.
+
+    logits: R x V, fp32 or bf16, rows contiguous (any row stride, so a padded
+    vocabulary is passed as ``buffer[:, :V]``). tokens: R, int32 or int64; a
+    negative token has log probability 0, one past the vocabulary NaN."""
+    import torch
+
+    R, V, ld = _check_logits(logits)
+    ztype = _float_type(logits, "logits")
+    if not 0 <= top <= min(64, V):
+        raise ValueError(f"top must be between 0 and {min(64, V)}, got {top}")
+    _same_device(logits, tokens)
+    ttype, logprob = TYPE_INT64, None
+    if tokens is not None:
+        ttype = _index_type(tokens, "tokens")
+        _check(tokens, tokens.dtype, (R,), "tokens")
+        logprob = torch.empty(R, dtype=torch.float32, device=logits.device)
+    stats = torch.empty((2, R), dtype=torch.float32, device=logits.device)
+    top_logprob = torch.empty((R, top), dtype=torch.float32, device=logits.device)
+    top_ids = torch.empty((R, top), dtype=torch.int32, device=logits.device)
+    dev = logits.device.index if logits.device.index is not None else 0
+    ctx = ctx or default_context(dev)
+    rc = library().lin_token_logprobs(ctx._h, R, V, logits.data_ptr(), ld, ztype, _ptr(tokens), ttype,
+                                      float(temperature), int(top), _ptr(logprob), stats[0].data_ptr(),
+                                      stats[1].data_ptr(), top_logprob.data_ptr(), top_ids.data_ptr(),
+                                      _stream_ptr(stream, dev))
+    if rc != OK:
+        raise LinError(rc, "lin_token_logprobs")
+    return TokenLogprobs(logprob, stats[0], stats[1], top_logprob, top_ids)
+
+
+def _distill_args(logits, ids, teacher, rows):
+    import torch
+
+    R, V, ld = _check_logits(logits)
+    if ids.dim() != 2 or ids.shape[0] != R:
+        raise ValueError(f"ids must be R x K with R = {R}, got {tuple(ids.shape)}")
+    itype, ttype = _index_type(ids, "ids"), _float_type(teacher, "teacher")
+    _check(ids, ids.dtype, tuple(ids.shape), "ids")
+    _check(teacher, teacher.dtype, tuple(ids.shape), "teacher")
+    for what, t in rows.items():
+        if t is not None:
+            _check(t, torch.float32, (R,), what)
+    _same_device(logits, ids, teacher, *rows.values())
+    return (R, V, ids.shape[1], logits.data_ptr(), ld, _float_type(logits, "logits"), ids.data_ptr(), itype,
+            teacher.data_ptr(), ttype)
+
+
+def _dlogits(logits, out):
+    """The gradient's tensor and row stride: ``out``, or a new one whose rows
+    lie like the logits' (padding included, so that both move in whole units)."""
+    import torch
+
+    if out is None:
+        R, V, ld = _check_logits(logits)
+        pitch = ld if ld <= V + 1024 else V
+        out = torch.empty((R, pitch), dtype=logits.dtype, device=logits.device)[:, :V]
+    elif out.dtype != logits.dtype or out.shape != logits.shape:
+        raise ValueError("out must have the logits' shape and type")
+    _same_device(logits, out)
+    return out, _check_logits(out, "out")[2]
+
+
+def distill_forward(logits, ids, teacher, temperature: float = 1.0, ctx: Context | None = None, stream=None):
+    """Distillation loss of each row towards a teacher's top logits:
+    tau^2 KL(softmax(teacher / tau) over the row's entries || softmax(logits / tau)).
+
+    logits: R x V (fp32 or bf16, any row stride). ids, teacher: R x K token ids
+    (int32 or int64, negative = padding) and the teacher's logits or log
+    probabilities for them (fp32 or bf16). Returns (loss, lse), R fp32 each;
+    lse is what :func:`distill_backward` needs."""
+    import torch
+
+    args = _distill_args(logits, ids, teacher, {})
+    out = torch.empty((2, args[0]), dtype=torch.float32, device=logits.device)
+    dev = logits.device.index if logits.device.index is not None else 0
+    ctx = ctx or default_context(dev)
+    rc = library().lin_distill_forward(ctx._h, *args, float(temperature), out[0].data_ptr(), out[1].data_ptr(),
+                                       _stream_ptr(stream, dev))
+    if rc != OK:
+        raise LinError(rc, "lin_distill_forward")
+    return out[0], out[1]
+
+
+def distill_backward(logits, ids, teacher, lse, grad_loss, temperature: float = 1.0, out=None,
+                     ctx: Context | None = None, stream=None):
+    """The logits' gradient, from :func:`distill_forward`'s lse and the
+    gradient of each row's loss (R fp32). ``out`` may be ``logits``."""
+    args = _distill_args(logits, ids, teacher, {"lse": lse, "grad_loss": grad_loss})
+    out, ldd = _dlogits(logits, out)
+    dev = logits.device.index if logits.device.index is not None else 0
+    ctx = ctx or default_context(dev)
+    rc = library().lin_distill_backward(ctx._h, *args, float(temperature), lse.data_ptr(), grad_loss.data_ptr(),
+                                        out.data_ptr(), ldd, _stream_ptr(stream, dev))
+    if rc != OK:
+        raise LinError(rc, "lin_distill_backward")
+    return out
+
+
+def distill_forward_backward(logits, ids, teacher, weight=None, temperature: float = 1.0, out=None,
+                             ctx: Context | None = None, stream=None):
+    """(loss, dlogits) in one pass over the logits: the rows' losses and the
+    gradient of sum_r weight[r] * loss[r] (weight: R fp32, default 1).
+    ``out`` may be ``logits``: the gradient then replaces them."""
+    import torch
+
+    args = _distill_args(logits, ids, teacher, {"weight": weight})
+    out, ldd = _dlogits(logits, out)
+    loss = torch.empty(args[0], dtype=torch.float32, device=logits.device)
+    dev = logits.device.index if logits.device.index is not None else 0
+    ctx = ctx or default_context(dev)
+    rc = library().lin_distill_forward_backward(ctx._h, *args, float(temperature), _ptr(weight), loss.data_ptr(),
+                                                out.data_ptr(), ldd, _stream_ptr(stream, dev))
+    if rc != OK:
+        raise LinError(rc, "lin_distill_forward_backward")
+    return loss, out

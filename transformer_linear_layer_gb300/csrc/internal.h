@@ -177,6 +177,60 @@ struct AttnProblem {
 };
 int launch_attention(const AttnProblem& p);
 
+// Attention backward (attn_bwd.cu): dqkv from qkv, the forward's out and lse,
+// and dout, all in the forward's layouts.
+struct AttnBwdProblem {
+    int B = 0, T = 0, H = 0;
+    const void* qkv = nullptr;
+    const void* out = nullptr;
+    const float* lse = nullptr;
+    const void* dout = nullptr;
+    void* dqkv = nullptr;
+    bool causal = true;
+    float scale = 0.f;             // softmax scale (> 0)
+    cudaStream_t stream = nullptr;
+    void* workspace = nullptr;     // fp32 partial sums of dq, past the counter block
+    size_t workspace_bytes = 0;
+    int* dev_status = nullptr;
+    int sm_count = 0;
+    bool early_start = false;      // programmatic launch (nothing is read before the dependency wait)
+};
+int launch_attention_backward(const AttnBwdProblem& p);
+
+// Operators on the logits (logits.cu): R rows of V values, ld elements apart.
+constexpr int kLogprobMaxTop = 64;       // top alternatives of a row
+constexpr int kDistillMaxEntries = 1024; // teacher entries of a row
+struct LogitsProblem {
+    long long R = 0, ld = 0;
+    int V = 0;
+    const void* z = nullptr;
+    bool bf16 = true;              // logits (and their gradient): bf16 or fp32
+    float tau = 1.f;               // temperature (> 0)
+    const void* ids = nullptr;     // tokens (R, or null) / teacher entries (R x K)
+    bool wide_ids = false;         // 64-bit
+    // token log probabilities
+    int top = 0;
+    float* logprob = nullptr;
+    float* entropy = nullptr;
+    float* lse = nullptr;          // also of the distillation's forward
+    float* top_logprob = nullptr;
+    int* top_ids = nullptr;
+    // distillation; forward: lse_in null, gradient: dz not null
+    int K = 0;
+    const void* teacher = nullptr;
+    bool teacher_bf16 = false;
+    const float* weight = nullptr;
+    const float* lse_in = nullptr;
+    float* loss = nullptr;
+    void* dz = nullptr;
+    long long ldd = 0;
+    cudaStream_t stream = nullptr;
+    int sm_count = 0;
+    bool early_start = false;
+};
+int launch_logprobs(const LogitsProblem& p);
+int launch_distill(const LogitsProblem& p);
+
 // Kernel timelines (timeline build only, see timeline.cuh): copy up to `bytes`
 // of the stamp array to host memory at `dst` (if not null), then zero it (if
 // `clear`). LIN_ERR_UNSUPPORTED in the library build.

@@ -990,6 +990,169 @@ int lin_attention_forward(lin_ctx* ctx, int B, int T, int H, int D, const void* 
     return launch_attention(p);
 }
 
+namespace {
+
+bool float_type(int t) { return t == LIN_TYPE_FP32 || t == LIN_TYPE_BF16; }
+bool index_type(int t) { return t == LIN_TYPE_INT32 || t == LIN_TYPE_INT64; }
+size_t type_bytes(int t) { return t == LIN_TYPE_BF16 ? 2 : t == LIN_TYPE_INT64 ? 8 : 4; }
+size_t row_bytes(int R, int V, long long ld, size_t esz) { return ((size_t)(R - 1) * (size_t)ld + (size_t)V) * esz; }
+
+// A range, its element size and whether the call writes it.
+struct Operand {
+    const void* p;
+    size_t bytes, esz;
+    bool written;
+};
+
+// Alignment, and no output over another operand. Records the outputs' hull as
+// the stream's newest output.
+int check_operands(const Operand* o, int N, cudaStream_t st) {
+    using namespace lin;
+    for (int i = 0; i < N; ++i)
+        for (int j = 0; j < N; ++j)
+            if (i != j && o[i].written && overlaps(o[i].p, o[i].p ? o[i].bytes : 0, o[j].p, o[j].p ? o[j].bytes : 0))
+                return LIN_ERR_ARG;
+    uintptr_t lo = UINTPTR_MAX, hi = 0;
+    for (int i = 0; i < N; ++i) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(o[i].p);
+        if (!a) continue;
+        if (a % o[i].esz != 0) return LIN_ERR_ALIGN;
+        if (!o[i].written) continue;
+        if (a < lo) lo = a;
+        if (a + o[i].bytes > hi) hi = a + o[i].bytes;
+    }
+    bool w_ok = false, x_ok = false, known = false;
+    early_reads_ok(st, Range{nullptr, 0}, Range{nullptr, 0}, Range{nullptr, 0},
+                   Range{reinterpret_cast<const void*>(lo), hi - lo}, &w_ok, &x_ok, &known);
+    return LIN_OK;
+}
+
+int logits_setup(lin_ctx* ctx, int R, int V, const void* logits, long long ld, int type, float tau, void* stream,
+                 lin::LogitsProblem* p) {
+    if (!ctx || R < 0 || V < 0 || !float_type(type) || !(tau > 0.f) || isinf(tau) || isinf(1.0f / tau))
+        return LIN_ERR_ARG;
+    if (R == 0) return LIN_OK;
+    if (V == 0 || ld < V || !logits) return LIN_ERR_ARG;
+    if (V > (1 << 30) || R > (1 << 27) || ld > (1ll << 40)) return LIN_ERR_UNSUPPORTED;
+    p->R = R;
+    p->V = V;
+    p->ld = ld;
+    p->z = logits;
+    p->bf16 = type == LIN_TYPE_BF16;
+    p->tau = tau;
+    p->stream = static_cast<cudaStream_t>(stream);
+    p->sm_count = ctx->sm_count;
+    p->early_start = ctx->programmatic;
+    return LIN_OK;
+}
+
+int distill_run(lin_ctx* ctx, int R, int V, int K, const void* logits, long long ld, int logits_type, const void* ids,
+                int ids_type, const void* teacher, int teacher_type, float tau, const float* weight,
+                const float* lse_in, float* loss, float* lse, void* dz, long long ldd, bool grad, void* stream) {
+    lin::LogitsProblem p;
+    const int rc = logits_setup(ctx, R, V, logits, ld, logits_type, tau, stream, &p);
+    if (rc != LIN_OK) return rc;
+    if (K < 0 || !index_type(ids_type) || !float_type(teacher_type)) return LIN_ERR_ARG;
+    if (R == 0) return LIN_OK;
+    if (K > lin::kDistillMaxEntries) return LIN_ERR_UNSUPPORTED;
+    if ((K > 0 && (!ids || !teacher)) || (grad && (!dz || ldd < V))) return LIN_ERR_ARG;
+    if (ldd > (1ll << 40)) return LIN_ERR_UNSUPPORTED;
+    const size_t esz = type_bytes(logits_type), rk = (size_t)R * K, r4 = (size_t)R * 4;
+    const bool in_place = grad && dz == logits && ldd == ld;
+    const Operand ops[] = {
+        {in_place ? nullptr : logits, row_bytes(R, V, ld, esz), esz, false},
+        {ids, rk * type_bytes(ids_type), type_bytes(ids_type), false},
+        {teacher, rk * type_bytes(teacher_type), type_bytes(teacher_type), false},
+        {weight, r4, 4, false},
+        {lse_in, r4, 4, false},
+        {loss, r4, 4, true},
+        {lse, r4, 4, true},
+        {grad ? dz : nullptr, grad ? row_bytes(R, V, ldd, esz) : 0, esz, true},
+    };
+    const int ok = check_operands(ops, (int)(sizeof(ops) / sizeof(ops[0])), p.stream);
+    if (ok != LIN_OK) return ok;
+    lin::DeviceGuard guard(ctx->device);
+    if (!guard.ok) return LIN_ERR_CUDA;
+    p.K = K;
+    p.ids = ids;
+    p.wide_ids = ids_type == LIN_TYPE_INT64;
+    p.teacher = teacher;
+    p.teacher_bf16 = teacher_type == LIN_TYPE_BF16;
+    p.weight = weight;
+    p.lse_in = lse_in;
+    p.loss = loss;
+    p.lse = lse;
+    p.dz = grad ? dz : nullptr;
+    p.ldd = ldd;
+    return lin::launch_distill(p);
+}
+
+}  // namespace
+
+int lin_token_logprobs(lin_ctx* ctx, int R, int V, const void* logits, long long ld, int logits_type,
+                       const void* tokens, int tokens_type, float tau, int top, float* logprob, float* entropy,
+                       float* lse, float* top_logprob, int* top_ids, void* stream) {
+    lin::LogitsProblem p;
+    const int rc = logits_setup(ctx, R, V, logits, ld, logits_type, tau, stream, &p);
+    if (rc != LIN_OK) return rc;
+    if (top < 0 || (tokens && !index_type(tokens_type)) || (R > 0 && (tokens == nullptr) != (logprob == nullptr)))
+        return LIN_ERR_ARG;
+    if (R == 0) return LIN_OK;
+    if (top > lin::kLogprobMaxTop) return LIN_ERR_UNSUPPORTED;
+    if (top > V || (top > 0 && (!top_logprob || !top_ids))) return LIN_ERR_ARG;
+    if (!logprob && !entropy && !lse && top == 0) return LIN_OK;
+    if (top == 0) {
+        top_logprob = nullptr;
+        top_ids = nullptr;
+    }
+    const size_t esz = type_bytes(logits_type), r4 = (size_t)R * 4;
+    const Operand ops[] = {
+        {logits, row_bytes(R, V, ld, esz), esz, false},
+        {tokens, (size_t)R * type_bytes(tokens_type), type_bytes(tokens_type), false},
+        {logprob, r4, 4, true},
+        {entropy, r4, 4, true},
+        {lse, r4, 4, true},
+        {top_logprob, r4 * top, 4, true},
+        {top_ids, r4 * top, 4, true},
+    };
+    const int ok = check_operands(ops, (int)(sizeof(ops) / sizeof(ops[0])), p.stream);
+    if (ok != LIN_OK) return ok;
+    lin::DeviceGuard guard(ctx->device);
+    if (!guard.ok) return LIN_ERR_CUDA;
+    p.ids = tokens;
+    p.wide_ids = tokens_type == LIN_TYPE_INT64;
+    p.top = top;
+    p.logprob = logprob;
+    p.entropy = entropy;
+    p.lse = lse;
+    p.top_logprob = top_logprob;
+    p.top_ids = top_ids;
+    return lin::launch_logprobs(p);
+}
+
+int lin_distill_forward(lin_ctx* ctx, int R, int V, int K, const void* logits, long long ld, int logits_type,
+                        const void* ids, int ids_type, const void* teacher, int teacher_type, float tau, float* loss,
+                        float* lse, void* stream) {
+    if (R > 0 && !loss) return LIN_ERR_ARG;
+    return distill_run(ctx, R, V, K, logits, ld, logits_type, ids, ids_type, teacher, teacher_type, tau, nullptr,
+                       nullptr, loss, lse, nullptr, 0, false, stream);
+}
+
+int lin_distill_backward(lin_ctx* ctx, int R, int V, int K, const void* logits, long long ld, int logits_type,
+                         const void* ids, int ids_type, const void* teacher, int teacher_type, float tau,
+                         const float* lse, const float* grad_loss, void* dlogits, long long ldd, void* stream) {
+    if (R > 0 && (!lse || !grad_loss)) return LIN_ERR_ARG;
+    return distill_run(ctx, R, V, K, logits, ld, logits_type, ids, ids_type, teacher, teacher_type, tau, grad_loss,
+                       lse, nullptr, nullptr, dlogits, ldd, true, stream);
+}
+
+int lin_distill_forward_backward(lin_ctx* ctx, int R, int V, int K, const void* logits, long long ld, int logits_type,
+                                 const void* ids, int ids_type, const void* teacher, int teacher_type, float tau,
+                                 const float* weight, float* loss, void* dlogits, long long ldd, void* stream) {
+    return distill_run(ctx, R, V, K, logits, ld, logits_type, ids, ids_type, teacher, teacher_type, tau, weight,
+                       nullptr, loss, nullptr, dlogits, ldd, true, stream);
+}
+
 int lin_check_device(lin_ctx* ctx, void* stream) {
     if (!ctx) return LIN_ERR_ARG;
     lin::DeviceGuard guard(ctx->device);
