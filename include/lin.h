@@ -453,6 +453,32 @@ LIN_API int lin_forward_fp32_static(int M, int N, int K, const float* X, const f
 LIN_API int lin_attention_forward(lin_ctx* ctx, int B, int T, int H, int D, const void* qkv, void* out, float* lse,
                                   int causal, float scale, void* stream);
 
+/* Backward pass of lin_attention_forward, in its layouts: the probabilities are
+ * rebuilt from the forward's lse, so nothing of size T x T reaches memory.
+ *   s_ij = (q_i . k_j) * scale,  p_ij = exp(s_ij - lse_i) (0 where masked),
+ *   delta_i = dout_i . out_i,    dp_ij = dout_i . v_j,
+ *   ds_ij = p_ij (dp_ij - delta_i),
+ *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,
+ *   dv_j = sum_i p_ij dout_i.
+ *   qkv  : (B*T) x 3C bf16, the forward's input.
+ *   out  : (B*T) x C bf16, the forward's output.   lse : B x H x T fp32, its lse
+ *          (-inf marks a query that sees no key: it contributes nothing).
+ *   dout : (B*T) x C bf16, the gradient of out.
+ *   dqkv : (B*T) x 3C bf16, written whole; must not overlap the inputs.
+ *   B, T, H, D, causal, scale as in the forward.
+ * Arithmetic: bf16 products accumulated in fp32 on the tensor cores; p and ds
+ * in fp32, each rounded once to bf16 for the products that take it; sums in
+ * fp32, each gradient rounded once. The sums' order is fixed by the sizes, the
+ * SM count and the workspace, so results repeat bit for bit. Uses the context
+ * workspace (up to about 256 bytes a head and token per partial sum of dq;
+ * heads that do not fit at once go in several launches; LIN_ERR_WORKSPACE
+ * when not even one head fits). qkv, out, dout and dqkv must be 16-byte aligned
+ * (LIN_ERR_ALIGN), lse 4-byte aligned. Asynchronous on `stream`; reads and
+ * writes only after the previous kernel on the stream has finished. */
+LIN_API int lin_attention_backward(lin_ctx* ctx, int B, int T, int H, int D, const void* qkv, const void* out,
+                                   const float* lse, const void* dout, void* dqkv, int causal, float scale,
+                                   void* stream);
+
 /* ---- Operators on the LM head's logits ----
  * R rows of V logits, row r at logits + r * ld elements (ld >= V: a padded
  * vocabulary's columns are neither read nor written), z_rj below. Element

@@ -22,7 +22,7 @@ from .build import build
 
 __all__ = [
     "LinError", "Context", "Plan", "forward", "forward_plan", "plan_query", "plan_make", "build",
-    "backward_data", "backward_weight", "gelu_backward", "attention_forward",
+    "backward_data", "backward_weight", "gelu_backward", "attention_forward", "attention_backward",
     "TokenLogprobs", "token_logprobs", "distill_forward", "distill_backward", "distill_forward_backward",
     "library", "PREC_FP32", "PREC_TF32", "PREC_BF16", "EPI_NONE", "EPI_GELU_TANH",
     "KERNEL_NONE", "KERNEL_FILL", "KERNEL_SKINNY", "KERNEL_FFMA", "KERNEL_TC", "KERNEL_GEMV",
@@ -116,6 +116,7 @@ def library() -> ctypes.CDLL:
                 "lin_probe_ffma": ([P, I, P, ctypes.POINTER(ctypes.c_double), P], I),
                 "lin_timeline": ([I, P, Z, I], I),
                 "lin_attention_forward": ([P, I, I, I, I, P, P, P, I, ctypes.c_float, P], I),
+                "lin_attention_backward": ([P, I, I, I, I, P, P, P, P, P, I, F, P], I),
                 "lin_token_logprobs": ([P, I, I, P, L, I, P, I, F, I, P, P, P, P, P, P], I),
                 "lin_distill_forward": ([P, I, I, I, P, L, I, P, I, P, I, F, P, P, P], I),
                 "lin_distill_backward": ([P, I, I, I, P, L, I, P, I, P, I, F, P, P, P, L, P], I),
@@ -557,6 +558,35 @@ def attention_forward(qkv, B: int, T: int, H: int, causal: bool = True, scale: f
     if rc != OK:
         raise LinError(rc, "lin_attention_forward")
     return (out, lse) if lse is not None else out
+
+
+def attention_backward(qkv, out, lse, dout, B: int, T: int, H: int, causal: bool = True, scale: float | None = None,
+                       dqkv=None, ctx: Context | None = None, stream=None):
+    """Gradient of :func:`attention_forward` with respect to qkv.
+
+    qkv ((B*T) x 3C), out ((B*T) x C) and lse (B, H, T) are the forward's input
+    and outputs (``with_lse=True``), dout ((B*T) x C bf16) the gradient of out.
+    Returns dqkv ((B*T) x 3C bf16). Uses the context's workspace."""
+    import torch
+
+    D = 64
+    C = H * D
+    _check(qkv, torch.bfloat16, (B * T, 3 * C), "qkv")
+    _check(out, torch.bfloat16, (B * T, C), "out")
+    _check(lse, torch.float32, (B, H, T), "lse")
+    _check(dout, torch.bfloat16, (B * T, C), "dout")
+    if dqkv is None:
+        dqkv = torch.empty_like(qkv)
+    _check(dqkv, torch.bfloat16, (B * T, 3 * C), "dqkv")
+    _same_device(qkv, out, lse, dout, dqkv)
+    dev = qkv.device.index if qkv.device.index is not None else 0
+    ctx = ctx or default_context(dev)
+    rc = library().lin_attention_backward(ctx._h, B, T, H, D, qkv.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                          dout.data_ptr(), dqkv.data_ptr(), int(bool(causal)),
+                                          0.0 if scale is None else float(scale), _stream_ptr(stream, dev))
+    if rc != OK:
+        raise LinError(rc, "lin_attention_backward")
+    return dqkv
 
 
 # ---------------------------------------------------------------- logits

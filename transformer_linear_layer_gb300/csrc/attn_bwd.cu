@@ -1,0 +1,855 @@
+// Backward pass of the fused self-attention, in the forward's layouts: from
+// qkv ((B*T) x 3C), the forward's out and dout ((B*T) x C) and lse (B x H x T)
+// it writes dqkv ((B*T) x 3C). The probabilities are rebuilt from lse, so the
+// score matrix reaches memory in neither direction ("Writing a CUDA matmul that
+// catches cuBLAS", section "Fusing attention: the score matrix never exists"):
+//
+//   s_ij  = (q_i . k_j) scale,   p_ij = exp(s_ij - lse_i)   (0 where masked)
+//   delta_i = dout_i . out_i     (= sum_j p_ij dp_ij)
+//   dv_j  = sum_i p_ij dout_i,   dp_ij = dout_i . v_j
+//   ds_ij = p_ij (dp_ij - delta_i)
+//   dq_i  = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i
+//
+// Three kernels:
+//   attn_bwd_prep    delta and lse in base-2 units, one pair a query, padded to
+//                    whole blocks of 128 queries.
+//   attn_bwd_kernel  a persistent block per SM walks work items (sequence, head,
+//                    block of 128 keys); an item walks the query blocks that see
+//                    its keys, with dk and dv accumulating in TMEM. dq is summed
+//                    over the key blocks in fp32 in the workspace, or written
+//                    straight to dqkv when a sequence is one block long.
+//   attn_bwd_dq      the fp32 sums to bf16.
+//
+// One step (key block j, query block i) takes five products of 128 x 128 x 64
+// on the tensor cores, scores transposed (keys on the TMEM lanes):
+//   S'  = K Q',  dP' = V dO'      operands in shared memory as they were loaded
+//   dV += P' dO                   P' (bf16) from TMEM, dO read MN-major
+//   dK += dS' Q                   dS' (bf16) in shared memory, read K-major,
+//   dQ  = dS K                    and the same tile read MN-major as dS
+// With the keys on the lanes P' needs no trip through shared memory, whose
+// bandwidth the five products' operands otherwise exceed.
+//
+// Warps: 0 TMA; 1 tcgen05.mma issuer; 4-11 two groups that turn S' and dP' into
+// P' and dS' (a thread has one key and 64 of the block's queries); 12-15 dQ out
+// of TMEM, and dK and dV at an item's end. S'(n+1) and dP'(n+1) are issued while
+// step n is turned into P' and dS', so the exponentials overlap the products.
+//
+// Order of the dq sums: the key blocks of a head form `chains` chains (block j in
+// chain j % chains), each with its own fp32 copy of dq; within a chain block j
+// adds to a tile after block j - chains has (a counter per tile, waited for).
+// The sums' order is thus fixed, results are repeatable bit for bit, and a wait
+// is only ever for an item that comes earlier in the walk. Every wait is
+// bounded (about 1 s); a block that gives up sets the device status word.
+#include <math.h>
+
+#include <algorithm>
+
+#include "device_common.cuh"
+#include "internal.h"
+#include "tc_common.cuh"
+
+namespace lin {
+namespace {
+
+constexpr int kAbB = 128;                          // keys, and queries, of a block
+constexpr int kAbD = 64;                           // head width
+constexpr int kAbThreads = 512;
+constexpr uint32_t kAbTile = kAbB * kAbD * 2;      // 16 KiB: 128 rows of 128 bytes, 128-byte swizzle
+constexpr uint32_t kAbStat = 2 * kAbB * 4;         // -lse log2(e) and -delta of 128 queries
+constexpr int kAbKvStages = 2, kAbQStages = 3;
+constexpr uint32_t kAbQStage = 2 * kAbTile + kAbStat;
+constexpr uint32_t kAbDs = kAbB * kAbB * 2;        // dS': two 64-query K-major blocks of 16 KiB
+constexpr int kAbBars = 2 * kAbKvStages + 2 * kAbQStages + 13;
+constexpr size_t kAbSmem = 1024 + kAbKvStages * 2 * kAbTile + kAbQStages * kAbQStage + kAbDs + kAbBars * 8 + 16;
+static_assert(kAbSmem <= 227 * 1024, "shared memory");
+constexpr size_t kAbDqTile = (size_t)kAbB * kAbD * 4;  // fp32 dq of a query block: [column / 4][row][4]
+// TMEM columns
+constexpr uint32_t kAbS = 0, kAbDp = 128, kAbDv = 256, kAbDk = 320, kAbDq = 384, kAbP = 448, kAbTmem = 512;
+constexpr float kAbLog2e = 1.4426950408889634f;
+
+struct AbArgs {
+    int B, T, H, C;
+    int nb;              // blocks of 128 in a sequence
+    int bh0, heads;      // the launch's (sequence, head) pairs: bh0 .. bh0 + heads - 1
+    int items;           // heads * nb
+    int chains;
+    int causal, single;  // single: nb == 1
+    float scale, scale_log2;
+    const float* stats;  // heads x nb x 256
+    unsigned* flags;     // heads x chains x nb
+    float* dq;           // heads x chains x nb tiles
+    int* status;
+};
+
+__device__ __forceinline__ float ab_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t ab_pack(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void ab_unpack(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t ab_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t ab_add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t ab_mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// 128 tokens x 64 columns of a (B, T, columns) tensor; tokens past T read as zero.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void ab_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+// Untiled copy; addresses and size are multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// D (+)= A B with A (bf16, two to a 32-bit column) in TMEM.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// 16 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void ab_tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The dS' tile read MN-major (rows are keys = K, 64-query chunks 16 KiB apart).
+__device__ __forceinline__ uint64_t ab_ds_mn_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>((kAbDs / 2) >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+__device__ __forceinline__ void red_add_v4(float* p, float a, float b, float c, float d) {
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d)
+                 : "memory");
+}
+
+// The block's items: rounds of gridDim.x items, every other round in reverse, so
+// that the sums of the items' lengths (which fall along the walk when causal)
+// stay close. Items are ordered by key block, then by head.
+struct AbWalker {
+    int round, m;        // round, items so far
+    int j, bh;           // key block, launch-local (sequence, head)
+    int i, i0;           // query block, the item's first
+    bool valid;
+    __device__ __forceinline__ void place(const AbArgs& a) {
+        const int c = blockIdx.x, g = gridDim.x;
+        const long long idx = (long long)round * g + ((round & 1) ? g - 1 - c : c);
+        valid = idx < a.items;
+        j = valid ? (int)(idx / a.heads) : 0;
+        bh = valid ? (int)(idx % a.heads) : 0;
+        i = i0 = a.causal ? j : 0;
+    }
+    __device__ __forceinline__ void init(const AbArgs& a) {
+        round = m = 0;
+        place(a);
+    }
+    __device__ __forceinline__ bool first() const { return i == i0; }
+    __device__ __forceinline__ bool last(const AbArgs& a) const { return i == a.nb - 1; }
+    __device__ __forceinline__ void next(const AbArgs& a) {
+        if (++i < a.nb) return;
+        next_item(a);
+    }
+    __device__ __forceinline__ void next_item(const AbArgs& a) {
+        ++round;
+        ++m;
+        place(a);
+    }
+};
+
+__global__ void __launch_bounds__(kAbThreads, 1)
+attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant__ CUtensorMap tmDo,
+                const __grid_constant__ CUtensorMap tmDqkv, const AbArgs a) {
+    constexpr uint32_t IDESC_S = make_idesc(1u, kAbB, kAbB);                  // both K-major
+    constexpr uint32_t IDESC_DKV = make_idesc(1u, kAbB, kAbD, false, true);   // A K-major (or TMEM), B MN-major
+    constexpr uint32_t IDESC_DQ = make_idesc(1u, kAbB, kAbD, true, true);     // both MN-major
+    constexpr int KS = kAbKvStages, QS = kAbQStages;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sKV = smem;                       // stage: K, V
+    uint8_t* sQ = sKV + KS * 2 * kAbTile;      // stage: Q, dO, statistics
+    uint8_t* sDS = sQ + QS * kAbQStage;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sDS + kAbDs);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kAbBars);
+    int* s_abort = reinterpret_cast<int*>(tmem_slot + 1);
+    int* s_go = s_abort + 1;
+
+    const uint32_t kvfull = smem_u32(bars), kvempty = kvfull + 8 * KS, qfull = kvempty + 8 * KS,
+                   qempty = qfull + 8 * QS, one = qempty + 8 * QS;
+    const uint32_t sfull = one, sread = one + 8, pready = one + 16, pvdone = one + 24, dpfull = one + 32,
+                   dpread = one + 40, dsready = one + 48, dsfree = one + 56, dqfull = one + 64, dqfree = one + 72,
+                   accfull = one + 80, accfree = one + 88, drained = one + 96;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < KS; ++s) {
+            mbar_init(kvfull + 8 * s, 1);
+            mbar_init(kvempty + 8 * s, 4);
+        }
+        for (int s = 0; s < QS; ++s) {
+            mbar_init(qfull + 8 * s, 1);
+            mbar_init(qempty + 8 * s, a.single ? 4 : 1);
+        }
+        mbar_init(sfull, 1);
+        mbar_init(sread, 8);
+        mbar_init(pready, 8);
+        mbar_init(pvdone, 1);
+        mbar_init(dpfull, 1);
+        mbar_init(dpread, 8);
+        mbar_init(dsready, 8);
+        mbar_init(dsfree, 1);
+        mbar_init(dqfull, 1);
+        mbar_init(dqfree, 4);
+        mbar_init(accfull, 1);
+        mbar_init(accfree, 4);
+        mbar_init(drained, 4);
+        *s_abort = 0;
+        *s_go = 1;
+        mbar_fence_init();
+        tma_prefetch_map(&tmQkv);
+        tma_prefetch_map(&tmDo);
+        tma_prefetch_map(&tmDqkv);
+    }
+    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), kAbTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (threadIdx.x == 0) pdl_launch_dependents();
+
+    auto give_up = [&]() {
+        atomicExch(s_abort, 1);
+        atomicExch(a.status, (int)LIN_ERR_DEVICE_TIMEOUT);
+    };
+    auto aborted = [&]() { return *(volatile int*)s_abort != 0; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            pdl_wait();  // the statistics are the previous kernel's output
+            uint32_t m = 0, n = 0;
+            bool ok = true;
+            AbWalker w;
+            for (w.init(a); ok && w.valid; w.next_item(a), ++m) {
+                const int bh = a.bh0 + w.bh, b = bh / a.H, h = bh % a.H;
+                const uint32_t ks = m % KS;
+                if (aborted() || !mbar_wait(kvempty + 8 * ks, ((m / KS) & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* kv = sKV + ks * 2 * kAbTile;
+                mbar_expect_tx(kvfull + 8 * ks, 2 * kAbTile);
+                tma_load_3d(smem_u32(kv), &tmQkv, kvfull + 8 * ks, a.C + h * kAbD, w.j * kAbB, b);
+                tma_load_3d(smem_u32(kv + kAbTile), &tmQkv, kvfull + 8 * ks, 2 * a.C + h * kAbD, w.j * kAbB, b);
+                for (int i = w.i0; i < a.nb; ++i, ++n) {
+                    const uint32_t qs = n % QS;
+                    if (aborted() || !mbar_wait(qempty + 8 * qs, ((n / QS) & 1) ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* q = sQ + qs * kAbQStage;
+                    mbar_expect_tx(qfull + 8 * qs, kAbQStage);
+                    tma_load_3d(smem_u32(q), &tmQkv, qfull + 8 * qs, h * kAbD, i * kAbB, b);
+                    tma_load_3d(smem_u32(q + kAbTile), &tmDo, qfull + 8 * qs, h * kAbD, i * kAbB, b);
+                    bulk_load(smem_u32(q + 2 * kAbTile), a.stats + ((size_t)w.bh * a.nb + i) * (2 * kAbB), kAbStat,
+                              qfull + 8 * qs);
+                }
+                if (!ok) {
+                    ++m;  // its K and V are in flight
+                    break;
+                }
+            }
+            if (!ok) {
+                give_up();
+                // let the copies still in flight land before the block exits
+                for (uint32_t k = m > (uint32_t)KS ? m - KS : 0; k < m; ++k) mbar_wait(kvfull + 8 * (k % KS), (k / KS) & 1);
+                for (uint32_t k = n > (uint32_t)QS ? n - QS : 0; k < n; ++k) mbar_wait(qfull + 8 * (k % QS), (k / QS) & 1);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            AbWalker cur, lead;
+            cur.init(a);
+            lead.init(a);
+            uint32_t n = 0;
+            bool ok = true;
+            auto issue_s = [&](uint32_t k) {  // S' of step k, the lead's
+                if (aborted() || (lead.first() && !mbar_wait(kvfull + 8 * (lead.m % KS), (lead.m / KS) & 1)) ||
+                    !mbar_wait(qfull + 8 * (k % QS), (k / QS) & 1) || (k > 0 && !mbar_wait(sread, (k - 1) & 1)))
+                    return false;
+                tc_fence_after();
+                const uint64_t kd = sw128_kmajor_desc(smem_u32(sKV + (lead.m % KS) * 2 * kAbTile));
+                const uint64_t qd = sw128_kmajor_desc(smem_u32(sQ + (k % QS) * kAbQStage));
+#pragma unroll
+                for (int kk = 0; kk < kAbD / 16; ++kk)
+                    tc_mma<true>(tmem + kAbS, kd + 2u * kk, qd + 2u * kk, IDESC_S, kk != 0 ? 1u : 0u);
+                tc_commit(sfull);
+                return true;
+            };
+            auto issue_dp = [&](uint32_t k) {  // dP' of step k
+                if (aborted() || (k > 0 && !mbar_wait(dpread, (k - 1) & 1))) return false;
+                tc_fence_after();
+                const uint64_t vd = sw128_kmajor_desc(smem_u32(sKV + (lead.m % KS) * 2 * kAbTile + kAbTile));
+                const uint64_t od = sw128_kmajor_desc(smem_u32(sQ + (k % QS) * kAbQStage + kAbTile));
+#pragma unroll
+                for (int kk = 0; kk < kAbD / 16; ++kk)
+                    tc_mma<true>(tmem + kAbDp, vd + 2u * kk, od + 2u * kk, IDESC_S, kk != 0 ? 1u : 0u);
+                tc_commit(dpfull);
+                return true;
+            };
+            if (cur.valid) {
+                ok = issue_s(0) && issue_dp(0);
+                lead.next(a);
+            }
+            while (ok && cur.valid) {
+                const bool first = cur.first(), last = cur.last(a);
+                if (lead.valid && !issue_s(n + 1)) {
+                    ok = false;
+                    break;
+                }
+                // dV += P' dO
+                if (aborted() || !mbar_wait(pready, n & 1) ||
+                    (first && cur.m > 0 && !mbar_wait(accfree, (cur.m - 1) & 1))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint8_t* q = sQ + (n % QS) * kAbQStage;
+                const uint64_t od = sw128_mnmajor_desc(smem_u32(q + kAbTile));
+#pragma unroll
+                for (int kk = 0; kk < kAbB / 16; ++kk)
+                    tc_mma_ts(tmem + kAbDv, tmem + kAbP + 8u * kk, od + 128u * kk, IDESC_DKV,
+                              (kk != 0 || !first) ? 1u : 0u);
+                tc_commit(pvdone);
+                if (lead.valid) {
+                    if (!issue_dp(n + 1)) {
+                        ok = false;
+                        break;
+                    }
+                    lead.next(a);
+                }
+                // dK += dS' Q, dQ = dS K
+                if (aborted() || !mbar_wait(dsready, n & 1) || (n > 0 && !mbar_wait(dqfree, (n - 1) & 1))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t dsk = sw128_kmajor_desc(smem_u32(sDS)), dsm = ab_ds_mn_desc(smem_u32(sDS));
+                const uint64_t qd = sw128_mnmajor_desc(smem_u32(q));
+                const uint64_t kd = sw128_mnmajor_desc(smem_u32(sKV + (cur.m % KS) * 2 * kAbTile));
+#pragma unroll
+                for (int kk = 0; kk < kAbB / 16; ++kk)
+                    tc_mma<true>(tmem + kAbDk, dsk + 1024u * (kk >> 2) + 2u * (kk & 3), qd + 128u * kk, IDESC_DKV,
+                                 (kk != 0 || !first) ? 1u : 0u);
+#pragma unroll
+                for (int kk = 0; kk < kAbB / 16; ++kk)
+                    tc_mma<true>(tmem + kAbDq, dsm + 128u * kk, kd + 128u * kk, IDESC_DQ, kk != 0 ? 1u : 0u);
+                tc_commit(dsfree);
+                tc_commit(dqfull);
+                if (!a.single) tc_commit(qempty + 8 * (n % QS));
+                if (last) tc_commit(accfull);
+                cur.next(a);
+                ++n;
+            }
+            if (!ok) {
+                give_up();
+                // the products issued so far end before the block does: one more
+                // commit on a barrier whose phase the other warps no longer follow
+                tc_commit(accfull);
+                mbar_wait(accfull, cur.m & 1);
+            }
+        }
+    } else if (warp >= 4 && warp < 12) {
+        pdl_wait();
+        const int grp = (warp - 4) >> 2, quad = warp & 3;
+        const int r = 32 * quad + lane;  // key within the block, TMEM lane
+        const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+        const uint32_t tS = tmem + lanes + kAbS + 64u * grp, tDp = tmem + lanes + kAbDp + 64u * grp,
+                       tP = tmem + lanes + kAbP + 32u * grp;
+        uint8_t* ds_row = sDS + grp * (kAbDs / 2) + r * 128;
+        const uint64_t sl2 = ab_pack(a.scale_log2, a.scale_log2);
+        uint32_t n = 0;
+        bool ok = true;
+        AbWalker w;
+        for (w.init(a); w.valid; w.next(a), ++n) {
+            const float* stat = reinterpret_cast<const float*>(sQ + (n % QS) * kAbQStage + 2 * kAbTile) + 64 * grp;
+            const bool diag = a.causal && w.i == w.j;
+            const bool masked = diag || (w.j + 1) * kAbB > a.T;
+            // query c of this group is visible to the thread's key from `from` on
+            const int from = w.j * kAbB + r >= a.T ? 64 : diag ? r - 64 * grp : 0;
+            if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(qfull + 8 * (n % QS), (n / QS) & 1) &&
+                                             mbar_wait(sfull, n & 1))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t s[2][32];
+            tmem_ld32_async(tS, s[0]);
+            tmem_ld32_async(tS + 32u, s[1]);
+            tmem_wait_ld(s[0]);
+            tmem_wait_ld(s[1]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sread);
+            // p = 2^(s scale log2(e) - lse log2(e))
+            uint64_t p[2][16];
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) {
+                    const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(stat + 32 * ch + c);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float x0, x1;
+                        ab_unpack(ab_fma2(ab_pack(__uint_as_float(s[ch][c + 2 * k]), __uint_as_float(s[ch][c + 2 * k + 1])),
+                                          sl2, k ? l.y : l.x),
+                                  x0, x1);
+                        p[ch][c / 2 + k] = ab_pack(ab_ex2(x0), ab_ex2(x1));
+                    }
+                }
+            if (masked) {
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        float x0, x1;
+                        ab_unpack(p[ch][c], x0, x1);
+                        p[ch][c] = ab_pack(32 * ch + 2 * c >= from ? x0 : 0.f, 32 * ch + 2 * c + 1 >= from ? x1 : 0.f);
+                    }
+            }
+            if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(pvdone, (n - 1) & 1))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    float x0, x1;
+                    ab_unpack(p[ch][c], x0, x1);
+                    pk[c] = pack_bf16x2(x0, x1);
+                }
+                tmem_st16(tP + 16u * ch, pk);
+            }
+            ab_tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pready);
+            // ds = p (dp - delta)
+            if (!__all_sync(0xffffffffu, mbar_wait(dpfull, n & 1) && (n == 0 || mbar_wait(dsfree, (n - 1) & 1)))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+                tmem_ld32_async(tDp + 32u * ch, s[0]);
+                tmem_wait_ld(s[0]);
+                if (ch == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(dpread);
+                }
+                uint32_t pk[16];
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) {
+                    const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(stat + kAbB + 32 * ch + c);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint64_t dp = ab_pack(__uint_as_float(s[0][c + 2 * k]), __uint_as_float(s[0][c + 2 * k + 1]));
+                        float x0, x1;
+                        ab_unpack(ab_mul2(p[ch][c / 2 + k], ab_add2(dp, k ? d.y : d.x)), x0, x1);
+                        if (masked) {  // a masked pair takes nothing from dp, whatever it is
+                            x0 = 32 * ch + c + 2 * k >= from ? x0 : 0.f;
+                            x1 = 32 * ch + c + 2 * k + 1 >= from ? x1 : 0.f;
+                        }
+                        pk[c / 2 + k] = pack_bf16x2(x0, x1);
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    *reinterpret_cast<uint4*>(ds_row + (((4 * ch + v) ^ (r & 7)) << 4)) =
+                        make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dsready);
+        }
+        if (!ok) give_up();
+    } else if (warp >= 12) {
+        pdl_wait();
+        const int quad = warp & 3;
+        const int r = 32 * quad + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+        // 64 fp32 columns of this thread's lane, scaled, as a bf16 row of a 128-byte-swizzled tile
+        auto stage_row = [&](uint8_t* tile, const uint32_t (&v)[2][32], float f) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t* x = &v[k >> 2][8 * (k & 3)];
+                *reinterpret_cast<uint4*>(tile + r * 128 + ((k ^ (r & 7)) << 4)) = make_uint4(
+                    pack_bf16x2(__uint_as_float(x[0]) * f, __uint_as_float(x[1]) * f),
+                    pack_bf16x2(__uint_as_float(x[2]) * f, __uint_as_float(x[3]) * f),
+                    pack_bf16x2(__uint_as_float(x[4]) * f, __uint_as_float(x[5]) * f),
+                    pack_bf16x2(__uint_as_float(x[6]) * f, __uint_as_float(x[7]) * f));
+            }
+        };
+        auto read64 = [&](uint32_t col, uint32_t (&v)[2][32]) {
+            tmem_ld32_async(tmem + lanes + col, v[0]);
+            tmem_ld32_async(tmem + lanes + col + 32u, v[1]);
+            tmem_wait_ld(v[0]);
+            tmem_wait_ld(v[1]);
+        };
+        uint32_t n = 0, syncs = 0;
+        bool ok = true;
+        // the four warps meet (bounded, like every wait here)
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(drained);
+            return __all_sync(0xffffffffu, mbar_wait(drained, syncs++ & 1)) != 0;
+        };
+        AbWalker w;
+        for (w.init(a); w.valid; w.next(a), ++n) {
+            const int bh = a.bh0 + w.bh, b = bh / a.H, h = bh % a.H;
+            const bool last = w.last(a);
+            if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(dqfull, n & 1))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t v[2][32];
+            read64(kAbDq, v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dqfree);
+            uint8_t* q = sQ + (n % QS) * kAbQStage;
+            if (a.single) {
+                // the step's products are complete: its Q tile holds dq on the way out
+                stage_row(q, v, a.scale);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    ab_store_3d(&tmDqkv, smem_u32(q + quad * 4096), h * kAbD, w.i * kAbB + 32 * quad, b);
+                    bulk_commit();
+                }
+            } else {
+                const int chain = w.j % a.chains, pos = w.j / a.chains;
+                const size_t slot = ((size_t)w.bh * a.chains + chain) * a.nb + w.i;
+                if (pos > 0) {
+                    if (threadIdx.x == 12 * 32) {
+                        // until the chain's earlier block has added to this tile
+                        const unsigned long long t0 = global_ns();
+                        bool there = false;
+                        for (uint32_t k = 0; k < kWaitIters; ++k) {
+                            there = ld_acquire_gpu(a.flags + slot) == (unsigned)pos;
+                            if (there || aborted()) break;
+                            if ((k & 63u) == 63u && global_ns() - t0 > kWaitNs) break;
+                        }
+                        // (once 0 it stays 0: the block gives up)
+                        if (!there) *(volatile int*)s_go = 0;
+                    }
+                    ok = meet() && *(volatile int*)s_go != 0;
+                    if (!ok) break;
+                }
+                float* tile = a.dq + slot * (kAbDqTile / 4) + r * 4;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const uint32_t* x = &v[c >> 3][4 * (c & 7)];
+                    float* dst = tile + c * (kAbB * 4);
+                    if (pos == 0)
+                        *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+                    else
+                        red_add_v4(dst, __uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]),
+                                   __uint_as_float(x[3]));
+                }
+                if (w.j + a.chains <= (a.causal ? w.i : a.nb - 1)) {
+                    ok = meet();
+                    if (!ok) break;
+                    if (threadIdx.x == 12 * 32) {
+                        __threadfence();
+                        st_release_gpu(a.flags + slot, (unsigned)pos + 1u);
+                    }
+                }
+            }
+            if (last) {
+                // dk and dv of the item, through its K and V tiles
+                if (!__all_sync(0xffffffffu, mbar_wait(accfull, w.m & 1))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint8_t* kv = sKV + (w.m % KS) * 2 * kAbTile;
+                read64(kAbDk, v);
+                stage_row(kv, v, a.scale);
+                read64(kAbDv, v);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(accfree);
+                stage_row(kv + kAbTile, v, 1.0f);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    const int y = w.j * kAbB + 32 * quad;  // tokens past T lie outside the map and are not written
+                    ab_store_3d(&tmDqkv, smem_u32(kv + quad * 4096), a.C + h * kAbD, y, b);
+                    ab_store_3d(&tmDqkv, smem_u32(kv + kAbTile + quad * 4096), 2 * a.C + h * kAbD, y, b);
+                    bulk_commit();
+                    bulk_wait_read_all();
+                    mbar_arrive(kvempty + 8 * (w.m % KS));
+                    if (a.single) mbar_arrive(qempty + 8 * (n % QS));
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) give_up();
+        if (lane == 0) bulk_wait_read_all();
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kAbTmem);
+    }
+}
+
+// Statistics of 128 queries of one head (two threads a query): -lse log2(e),
+// -inf (probability 0) past the sequence's end and for a query that sees no key,
+// and -delta. Also zeroes the dq counters of the head's query block.
+__global__ void __launch_bounds__(256) attn_bwd_prep(const uint16_t* out, const uint16_t* dout, const float* lse, int T,
+                                                     int H, int nb, int bh0, int chains, float* stats,
+                                                     unsigned* flags) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int local = blockIdx.x / nb, i = blockIdx.x % nb;
+    const int bh = bh0 + local, b = bh / H, h = bh % H;
+    const int row = threadIdx.x >> 1, half = threadIdx.x & 1;
+    const int t = i * kAbB + row;
+    float sum = 0.f;
+    if (t < T) {
+        const size_t off = ((size_t)b * T + t) * ((size_t)H * kAbD) + h * kAbD + 32 * half;
+        uint4 o[4], g[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            o[k] = *reinterpret_cast<const uint4*>(out + off + 8 * k);
+            g[k] = *reinterpret_cast<const uint4*>(dout + off + 8 * k);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t x[4] = {o[k].x, o[k].y, o[k].z, o[k].w}, y[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), sum);
+                sum = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), sum);
+            }
+        }
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    float* st = stats + (size_t)blockIdx.x * (2 * kAbB);
+    if (half) {
+        st[kAbB + row] = -sum;
+    } else {
+        const float l = t < T ? lse[(size_t)bh * T + t] : -INFINITY;
+        st[row] = l == -INFINITY ? -INFINITY : -l * kAbLog2e;
+    }
+    if (flags)
+        for (int g = threadIdx.x; g < chains; g += 256) flags[((size_t)local * chains + g) * nb + i] = 0u;
+}
+
+// dq of 128 queries of one head: the chains' fp32 sums added in order, scaled,
+// rounded once. A thread has 16 columns of a row.
+__global__ void __launch_bounds__(512) attn_bwd_dq(const float* dq, uint16_t* dqkv, int T, int H, int nb, int bh0,
+                                                   int chains, int causal, float scale) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int local = blockIdx.x / nb, i = blockIdx.x % nb;
+    const int bh = bh0 + local, b = bh / H, h = bh % H;
+    const int row = threadIdx.x & 127, part = threadIdx.x >> 7;
+    const int t = i * kAbB + row;
+    if (t >= T) return;
+    const int used = min(chains, causal ? i + 1 : nb);
+    float4 s[4];
+    for (int g = 0; g < used; ++g) {
+        const float4* p = reinterpret_cast<const float4*>(dq + (((size_t)local * chains + g) * nb + i) * (kAbDqTile / 4)) +
+                          4 * part * kAbB + row;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 x = p[k * kAbB];
+            if (g == 0) {
+                s[k] = x;
+            } else {
+                s[k].x += x.x;
+                s[k].y += x.y;
+                s[k].z += x.z;
+                s[k].w += x.w;
+            }
+        }
+    }
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        o[2 * k] = pack_bf16x2(s[k].x * scale, s[k].y * scale);
+        o[2 * k + 1] = pack_bf16x2(s[k].z * scale, s[k].w * scale);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(dqkv + ((size_t)b * T + t) * ((size_t)3 * H * kAbD) + h * kAbD + 16 * part);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 ab_encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
+// (B, T, cols) bf16, box = 64 columns x `rows` tokens of one sequence, 128-byte swizzle.
+bool ab_map(CUtensorMap* map, const void* base, int B, int T, int cols, int rows) {
+    auto fn = ab_encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(B)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(T) * cols * 2};
+    cuuint32_t box[3] = {kAbD, static_cast<cuuint32_t>(rows), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+int launch_attention_backward(const AttnBwdProblem& p) {
+    const int C = p.H * kAbD;
+    const int nb = (p.T + kAbB - 1) / kAbB;
+    const bool single = nb == 1;
+    const long long bh_all = (long long)p.B * p.H;
+
+    // Workspace after the counter block: statistics, counters, dq sums. Heads go
+    // in as many launches as it takes.
+    const size_t avail = p.workspace_bytes > kCounterBytes + 1024 ? p.workspace_bytes - kCounterBytes - 1024 : 0;
+    const size_t stat = (size_t)nb * kAbStat;
+    const size_t chain = single ? 0 : (size_t)nb * (kAbDqTile + sizeof(unsigned));
+    if (stat + chain > avail) return LIN_ERR_WORKSPACE;
+    long long heads = bh_all;
+    if ((size_t)heads > avail / (stat + chain)) heads = (long long)(avail / (stat + chain));
+    // Chains: as many of a head's key blocks as run at the same time, so that
+    // none waits, where the workspace has room for their sums.
+    int chains = 1;
+    if (!single) {
+        const long long together = (p.sm_count + heads - 1) / heads;
+        const long long room = (long long)((avail / heads - stat) / chain);
+        chains = (int)std::max(1ll, std::min({together, room, (long long)nb}));
+    }
+
+    CUtensorMap tq, tdo, tdq;
+    if (!ab_map(&tq, p.qkv, p.B, p.T, 3 * C, kAbB) || !ab_map(&tdo, p.dout, p.B, p.T, C, kAbB) ||
+        !ab_map(&tdq, p.dqkv, p.B, p.T, 3 * C, 32))
+        return LIN_ERR_CUDA;
+    static std::atomic<unsigned long long> attr_set{0};
+    if (ensure_smem_attr(attr_set, attn_bwd_kernel, kAbSmem) != LIN_OK) return LIN_ERR_CUDA;
+
+    char* ws = static_cast<char*>(p.workspace) + kCounterBytes;
+    AbArgs a;
+    a.B = p.B;
+    a.T = p.T;
+    a.H = p.H;
+    a.C = C;
+    a.nb = nb;
+    a.chains = chains;
+    a.causal = p.causal ? 1 : 0;
+    a.single = single ? 1 : 0;
+    a.scale = p.scale;
+    a.scale_log2 = p.scale * kAbLog2e;
+    a.status = p.dev_status;
+
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = p.stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = p.early_start ? 1 : 0;
+    for (long long bh0 = 0; bh0 < bh_all; bh0 += heads) {
+        const int count = (int)std::min(heads, bh_all - bh0);
+        a.bh0 = (int)bh0;
+        a.heads = count;
+        a.items = count * nb;
+        float* stats = reinterpret_cast<float*>(ws);
+        char* rest = ws + align_up((size_t)count * stat, 256);
+        unsigned* flags = reinterpret_cast<unsigned*>(rest);
+        float* dq = reinterpret_cast<float*>(rest + align_up((size_t)count * chains * nb * sizeof(unsigned), 256));
+        a.stats = stats;
+        a.flags = single ? nullptr : flags;
+        a.dq = single ? nullptr : dq;
+        cfg.gridDim = dim3((unsigned)a.items);
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = 0;
+        if (cudaLaunchKernelEx(&cfg, attn_bwd_prep, static_cast<const uint16_t*>(p.out),
+                               static_cast<const uint16_t*>(p.dout), p.lse, p.T, p.H, nb, a.bh0, chains, stats,
+                               a.flags) != cudaSuccess)
+            return LIN_ERR_CUDA;
+        cfg.gridDim = dim3((unsigned)std::min(a.items, p.sm_count));
+        cfg.blockDim = dim3(kAbThreads);
+        cfg.dynamicSmemBytes = kAbSmem;
+        if (cudaLaunchKernelEx(&cfg, attn_bwd_kernel, tq, tdo, tdq, a) != cudaSuccess) return LIN_ERR_CUDA;
+        if (!single) {
+            cfg.gridDim = dim3((unsigned)a.items);
+            cfg.blockDim = dim3(512);
+            cfg.dynamicSmemBytes = 0;
+            if (cudaLaunchKernelEx(&cfg, attn_bwd_dq, static_cast<const float*>(dq), static_cast<uint16_t*>(p.dqkv),
+                                   p.T, p.H, nb, a.bh0, chains, a.causal, a.scale) != cudaSuccess)
+                return LIN_ERR_CUDA;
+        }
+    }
+    return cudaGetLastError() == cudaSuccess ? LIN_OK : LIN_ERR_CUDA;
+}
+
+}  // namespace lin

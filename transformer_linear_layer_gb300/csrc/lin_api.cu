@@ -1089,6 +1089,47 @@ int distill_run(lin_ctx* ctx, int R, int V, int K, const void* logits, long long
 
 }  // namespace
 
+int lin_attention_backward(lin_ctx* ctx, int B, int T, int H, int D, const void* qkv, const void* out,
+                           const float* lse, const void* dout, void* dqkv, int causal, float scale, void* stream) {
+    using namespace lin;
+    if (!ctx || B < 0 || T < 0 || H < 0 || D < 0 || (causal != 0 && causal != 1)) return LIN_ERR_ARG;
+    if (!(scale >= 0.f) || isinf(scale)) return LIN_ERR_ARG;  // NaN, negative or infinite
+    if (B == 0 || T == 0 || H == 0) return LIN_OK;
+    if (D != 64) return LIN_ERR_UNSUPPORTED;
+    const long long rows = (long long)B * T, nb = (T + 127ll) / 128;
+    if (rows > INT_MAX || (long long)H * D * 3 > INT_MAX || (long long)B * H > INT_MAX ||
+        (long long)B * H * nb > INT_MAX)
+        return LIN_ERR_UNSUPPORTED;
+    if (!qkv || !out || !lse || !dout || !dqkv) return LIN_ERR_ARG;
+    const size_t bytes = (size_t)rows * H * D * 2;
+    const Operand ops[] = {
+        {qkv, 3 * bytes, 16, false}, {out, bytes, 16, false},      {lse, (size_t)B * H * T * 4, 4, false},
+        {dout, bytes, 16, false},    {dqkv, 3 * bytes, 16, true},
+    };
+    const int ok = check_operands(ops, (int)(sizeof(ops) / sizeof(ops[0])), static_cast<cudaStream_t>(stream));
+    if (ok != LIN_OK) return ok;
+    DeviceGuard guard(ctx->device);
+    if (!guard.ok) return LIN_ERR_CUDA;
+    AttnBwdProblem p;
+    p.B = B;
+    p.T = T;
+    p.H = H;
+    p.qkv = qkv;
+    p.out = out;
+    p.lse = lse;
+    p.dout = dout;
+    p.dqkv = dqkv;
+    p.causal = causal != 0;
+    p.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)D);
+    p.stream = static_cast<cudaStream_t>(stream);
+    p.workspace = ctx->workspace;
+    p.workspace_bytes = ctx->workspace_bytes;
+    p.dev_status = ctx->dev_status;
+    p.sm_count = ctx->sm_count;
+    p.early_start = ctx->programmatic;
+    return launch_attention_backward(p);
+}
+
 int lin_token_logprobs(lin_ctx* ctx, int R, int V, const void* logits, long long ld, int logits_type,
                        const void* tokens, int tokens_type, float tau, int top, float* logprob, float* entropy,
                        float* lse, float* top_logprob, int* top_ids, void* stream) {
