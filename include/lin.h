@@ -535,7 +535,7 @@ LIN_API int lin_token_logprobs(lin_ctx* ctx, int R, int V, const void* logits, l
  * row without entries (or whose teacher logits are all -inf) has loss 0 and
  * gradient 0, and so has the gradient where g_r = 0, whatever the logits are.
  * An id >= V makes its row's loss and gradient NaN.
- *   ids     : R x K, LIN_TYPE_INT32 or LIN_TYPE_INT64 (ids_type), 0 <= K <= 1024.
+ *   ids     : R x K, LIN_TYPE_INT32 or LIN_TYPE_INT64 (ids_type), 0 <= K <= 256.
  *   teacher : R x K, LIN_TYPE_FP32 or LIN_TYPE_BF16 (teacher_type). */
 
 /* loss (R fp32) and, if not NULL, lse (R fp32, log sum exp(z / tau): what

@@ -197,9 +197,9 @@ struct AttnBwdProblem {
 };
 int launch_attention_backward(const AttnBwdProblem& p);
 
-// Operators on the logits (logits.cu): R rows of V values, ld elements apart.
+// Operators on the logits (logprobs.cu, distill.cu): R rows of V values, ld elements apart.
 constexpr int kLogprobMaxTop = 64;       // top alternatives of a row
-constexpr int kDistillMaxEntries = 1024; // teacher entries of a row
+constexpr int kDistillMaxEntries = 256;  // teacher entries of a row
 struct LogitsProblem {
     long long R = 0, ld = 0;
     int V = 0;
@@ -225,6 +225,7 @@ struct LogitsProblem {
     void* dz = nullptr;
     long long ldd = 0;
     cudaStream_t stream = nullptr;
+    int* dev_status = nullptr;
     int sm_count = 0;
     bool early_start = false;
 };

@@ -1041,6 +1041,7 @@ int logits_setup(lin_ctx* ctx, int R, int V, const void* logits, long long ld, i
     p->bf16 = type == LIN_TYPE_BF16;
     p->tau = tau;
     p->stream = static_cast<cudaStream_t>(stream);
+    p->dev_status = ctx->dev_status;
     p->sm_count = ctx->sm_count;
     p->early_start = ctx->programmatic;
     return LIN_OK;
