@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kDfThreads, 8) distill_loss_kernel(const Disti
     const Teacher te = lg_teacher_at(entries, a.K, 0);
     TeacherSums s{0.f, 0.f, false};
     if (rank == 0 && threadIdx.x < 32) s = lg_teacher<BF16>(a, r, te);
-    Stats st = lg_stream<BF16, false, kDfBatch>(row, rank * kDfThreads + threadIdx.x, kDfThreads * CL, a.c);
+    Stats st = lg_stream<BF16, false, kDfBatch>(row, rank * kDfThreads + threadIdx.x, kDfThreads * CL, a.c, [](float) {});
     st = lg_join_blocks<kDfThreads, CL>(st, a.c, sh, rank);
     if (rank != 0 || threadIdx.x >= 32) return;
     const float base = lg_base(st.m), logs = log2f(st.s);

@@ -236,11 +236,12 @@ __device__ __forceinline__ void lg_sums(Stats& st, const uint4 (&r)[N], int n, f
 }
 
 // Add the first n units to the running statistics (n is the same for a warp).
+// Returns their largest value.
 template <bool BF16, bool ENTROPY, int N>
-__device__ __forceinline__ void lg_accumulate(Stats& st, const uint4 (&r)[N], int n, float c) {
-    float m = st.m;
+__device__ __forceinline__ float lg_accumulate(Stats& st, const uint4 (&r)[N], int n, float c) {
+    float m = lg_unit_max<BF16>(r[0]);
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
+    for (int k = 1; k < N; ++k) {
         if (k >= n) break;
         m = fmaxf(m, lg_unit_max<BF16>(r[k]));
     }
@@ -256,10 +257,13 @@ __device__ __forceinline__ void lg_accumulate(Stats& st, const uint4 (&r)[N], in
             for (int j = 0; j < 4; ++j) asm("min.bf16x2 %0, %0, %1;" : "+r"(low) : "r"(w[j]));
         }
         const float least = fminf(__uint_as_float(low << 16), __uint_as_float(low & 0xFFFF0000u));
-        if (__all_sync(0xffffffffu, (least - lg_base(st.m)) * c > kFarBelow))
-            return lg_sums<BF16, true, false>(st, r, n, c);
+        if (__all_sync(0xffffffffu, (least - lg_base(st.m)) * c > kFarBelow)) {
+            lg_sums<BF16, true, false>(st, r, n, c);
+            return m;
+        }
     }
     lg_sums<BF16, ENTROPY, true>(st, r, n, c);
+    return m;
 }
 
 __device__ __forceinline__ Stats lg_warp_join(Stats st, float c) {
@@ -277,13 +281,14 @@ __device__ __forceinline__ Stats lg_warp_join(Stats st, float c) {
 
 // Statistics of a whole row read straight from memory by a cluster of CL blocks
 // of NT threads, which take its units in turn.
-template <bool BF16, bool ENTROPY, int N>
-__device__ __forceinline__ Stats lg_stream(const Row<BF16>& row, int u0, int stride, float c) {
+// seen(largest value) is called after every N units of the thread.
+template <bool BF16, bool ENTROPY, int N, class Seen>
+__device__ __forceinline__ Stats lg_stream(const Row<BF16>& row, int u0, int stride, float c, Seen seen) {
     Stats st{-INFINITY, 0.f, 0.f, 0u};
     for (int u = u0; u - (int)(threadIdx.x & 31) < row.units; u += stride * N) {
         uint4 raw[N];
         row.load(raw, u, stride);
-        lg_accumulate<BF16, ENTROPY>(st, raw, (row.units - (u - (int)(threadIdx.x & 31)) + stride - 1) / stride, c);
+        seen(lg_accumulate<BF16, ENTROPY>(st, raw, (row.units - (u - (int)(threadIdx.x & 31)) + stride - 1) / stride, c));
     }
     return st;
 }

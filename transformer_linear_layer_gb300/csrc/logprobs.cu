@@ -14,6 +14,7 @@ namespace {
 constexpr int kLpThreads = 128;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpBatch = 8;    // units a thread loads before it uses the first
+constexpr int kLpFolds = 16;   // maxima kept of a thread's batches (batch n in place n % 16)
 constexpr int kLpList = 512;   // candidates of the top selection held in shared memory
 
 // Whole-number order of the values: a larger value has a larger key, zeros of
@@ -44,6 +45,7 @@ struct LogprobArgs {
 struct TopShared {
     uint64_t list[kLpList];
     uint64_t best[kLgMaxCluster * kLogprobMaxTop];  // a list of `top` from each block
+    float seen[kLpFolds][kLpThreads];               // largest value of a thread's batches
     int count;
 };
 
@@ -98,7 +100,14 @@ __global__ void __launch_bounds__(kLpThreads, 8) logprob_kernel(const LogprobArg
         tok = lg_load_id(a.tokens, a.wide, r);
         if (tok >= 0 && tok < a.V) z_tok = row.at(tok);
     }
-    Stats st = lg_stream<BF16, true, kLpBatch>(row, u0, stride, a.c);
+    int batches = 0;
+    Stats st = lg_stream<BF16, true, kLpBatch>(row, u0, stride, a.c, [&](float m) {
+        if (a.top > 0) {
+            float& kept = tp.seen[batches % kLpFolds][threadIdx.x];
+            kept = batches < kLpFolds ? m : fmaxf(kept, m);
+            ++batches;
+        }
+    });
 
     // A lower bound of the row's top-th largest value: of the W warps whose threads
     // all have units, each finds the largest key (its upper 16 bits, all that bf16
@@ -132,8 +141,13 @@ __global__ void __launch_bounds__(kLpThreads, 8) logprob_kernel(const LogprobArg
 
     const uint32_t bound = st.bound;
     const float least_value = lg_key_value(bound);
-    if (have != 0 && have >= bound) {
-        for (int u = u0; u < row.units; u += stride * kLpBatch) {
+    uint32_t folds = 0;  // batches of this thread that reach the bound
+    if (have != 0)
+        for (int f = 0; f < min(batches, kLpFolds); ++f)
+            if (!(tp.seen[f][threadIdx.x] < least_value)) folds |= 1u << f;
+    for (; folds; folds &= folds - 1) {
+        for (int f = __ffs(folds) - 1; f < batches; f += kLpFolds) {
+            const int u = u0 + f * stride * kLpBatch;
             uint4 raw[kLpBatch];
             row.load(raw, u, stride);
             uint32_t in = 0;
