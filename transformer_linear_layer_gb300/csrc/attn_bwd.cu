@@ -10,18 +10,8 @@
 //   ds_ij = p_ij (dp_ij - delta_i)
 //   dq_i  = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i
 //
-// Three kernels:
-//   attn_bwd_prep    delta and lse in base-2 units, one pair a query, padded to
-//                    whole blocks of 128 queries.
-//   attn_bwd_kernel  a persistent block per SM walks work items (sequence, head,
-//                    block of 128 keys); an item walks the query blocks that see
-//                    its keys, with dk and dv accumulating in TMEM. dq is summed
-//                    over the key blocks in fp32 in the workspace, or written
-//                    straight to dqkv when a sequence is one block long.
-//   attn_bwd_dq      the fp32 sums to bf16.
-//
-// One step (key block j, query block i) takes five products of 128 x 128 x 64
-// on the tensor cores, scores transposed (keys on the TMEM lanes):
+// For one block of 128 keys and one of 128 queries these are five products of
+// 128 x 128 x 64 on the tensor cores, scores transposed (keys on the TMEM lanes):
 //   S'  = K Q',  dP' = V dO'      operands in shared memory as they were loaded
 //   dV += P' dO                   P' (bf16) from TMEM, dO read MN-major
 //   dK += dS' Q                   dS' (bf16) in shared memory, read K-major,
@@ -29,17 +19,36 @@
 // With the keys on the lanes P' needs no trip through shared memory, whose
 // bandwidth the five products' operands otherwise exceed.
 //
-// Warps: 0 TMA; 1 tcgen05.mma issuer; 4-11 two groups that turn S' and dP' into
-// P' and dS' (a thread has one key and 64 of the block's queries); 12-15 dQ out
-// of TMEM, and dK and dV at an item's end. S'(n+1) and dP'(n+1) are issued while
-// step n is turned into P' and dS', so the exponentials overlap the products.
+// Sequences of one block (T <= 128): attn_bwd_short_kernel, a block per
+// (sequence, head), two blocks an SM so that one's loads and stores run under the
+// other's products and exponentials.
+//
+// Longer ones: three kernels:
+//   attn_bwd_prep    delta and lse in base-2 units, a pair a query, padded to
+//                    whole blocks of 128 queries.
+//   attn_bwd_kernel  a persistent block per SM walks work items (sequence, head,
+//                    block of 128 keys); an item walks the query blocks that see
+//                    its keys, with dk and dv accumulating in TMEM. dq is summed
+//                    over the key blocks in fp32 in the workspace.
+//   attn_bwd_dq      the fp32 sums to bf16.
+//
+// attn_bwd_kernel's warps: 0 TMA; 1 tcgen05.mma issuer; 4-11 two groups that
+// turn S' and dP' into P' and dS' (a thread has one key and 64 of the block's
+// queries); 12-15 dQ out of TMEM, and dK and dV at an item's end. S'(n+1) and
+// dP'(n+1) are issued while step n is turned into P' and dS', so the exponentials
+// overlap the products. A chain of products into one accumulator runs at about
+// half the rate of two chains in turn, so dV(n) is issued in turn with dP'(n+1),
+// and dK(n) with dQ(n); a commit costs the issuer about 350 cycles, so a step has
+// three, and what else waits for them is told by the warps that saw them.
 //
 // Order of the dq sums: the key blocks of a head form `chains` chains (block j in
 // chain j % chains), each with its own fp32 copy of dq; within a chain block j
-// adds to a tile after block j - chains has (a counter per tile, waited for).
-// The sums' order is thus fixed, results are repeatable bit for bit, and a wait
-// is only ever for an item that comes earlier in the walk. Every wait is
-// bounded (about 1 s); a block that gives up sets the device status word.
+// adds to a tile after block j - chains has (a counter per tile, waited for). The
+// sums' order is thus fixed, results are repeatable bit for bit, and a wait is
+// only ever for an item that comes earlier in the walk. A tile is added by one bulk
+// reduction from shared memory, whose completion is looked for a step later.
+// Every wait is bounded (about 1 s); a block that gives up sets the device status
+// word.
 #include <math.h>
 
 #include <algorithm>
@@ -56,24 +65,34 @@ constexpr int kAbD = 64;                           // head width
 constexpr int kAbThreads = 512;
 constexpr uint32_t kAbTile = kAbB * kAbD * 2;      // 16 KiB: 128 rows of 128 bytes, 128-byte swizzle
 constexpr uint32_t kAbStat = 2 * kAbB * 4;         // -lse log2(e) and -delta of 128 queries
-constexpr int kAbKvStages = 2, kAbQStages = 3;
+constexpr int kAbKStages = 2, kAbQStages = 3;      // (V has one)
 constexpr uint32_t kAbQStage = 2 * kAbTile + kAbStat;
 constexpr uint32_t kAbDs = kAbB * kAbB * 2;        // dS': two 64-query K-major blocks of 16 KiB
-constexpr int kAbBars = 2 * kAbKvStages + 2 * kAbQStages + 13;
-constexpr size_t kAbSmem = 1024 + kAbKvStages * 2 * kAbTile + kAbQStages * kAbQStage + kAbDs + kAbBars * 8 + 16;
+constexpr uint32_t kAbDqTile = kAbB * kAbD * 4;    // fp32 dq of a query block: [column / 4][row][4]
+constexpr int kAbBars = 2 * kAbKStages + 2 + 2 * kAbQStages + 10;
+constexpr size_t kAbSmem =
+    1024 + (kAbKStages + 1) * kAbTile + kAbQStages * kAbQStage + kAbDs + kAbDqTile + kAbBars * 8 + 16;
 static_assert(kAbSmem <= 227 * 1024, "shared memory");
-constexpr size_t kAbDqTile = (size_t)kAbB * kAbD * 4;  // fp32 dq of a query block: [column / 4][row][4]
 // TMEM columns
 constexpr uint32_t kAbS = 0, kAbDp = 128, kAbDv = 256, kAbDk = 320, kAbDq = 384, kAbP = 448, kAbTmem = 512;
+// and of the short kernel, where dV and dK take dP's place and dQ half of S's
+constexpr int kAsThreads = 256;
+constexpr uint32_t kAsP = 0, kAsDq = 64, kAsDp = 128, kAsDv = 128, kAsDk = 192, kAsTmem = 256;
+constexpr size_t kAsSmem = 1024 + 4 * kAbTile + kAbDs + kAbStat + 6 * 8 + 16;
+static_assert(2 * (kAsSmem + 1024) <= 228 * 1024, "two blocks an SM");
+// Register split (setmaxnreg, per warpgroup): launched at 128 a thread; TMA and MMA
+// give theirs to the groups that hold 64 probabilities and 64 dp a thread.
+constexpr int kAbLaunchRegs = 128, kAbRegsIssue = 64, kAbRegsSoftmax = 168, kAbRegsOut = 112;
+static_assert(kAbRegsIssue + 2 * kAbRegsSoftmax + kAbRegsOut <= 4 * kAbLaunchRegs, "register split");
 constexpr float kAbLog2e = 1.4426950408889634f;
 
 struct AbArgs {
-    int B, T, H, C;
+    int T, H, C;
     int nb;              // blocks of 128 in a sequence
     int bh0, heads;      // the launch's (sequence, head) pairs: bh0 .. bh0 + heads - 1
     int items;           // heads * nb
     int chains;
-    int causal, single;  // single: nb == 1
+    int causal;
     float scale, scale_log2;
     const float* stats;  // heads x nb x 256
     unsigned* flags;     // heads x chains x nb
@@ -129,15 +148,34 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-// D (+)= A B with A (bf16, two to a 32-bit column) in TMEM.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// Products and commits are issued by a whole warp with one lane's predicate:
+// descriptors then stay in uniform registers.
+__device__ __forceinline__ void ab_mma(uint32_t one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
         : "memory");
 }
+// D (+)= A B with A (bf16, two to a 32-bit column) in TMEM.
+__device__ __forceinline__ void ab_mma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void ab_commit(uint32_t one, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
+        : "memory");
+}
+constexpr uint32_t kIdescS = make_idesc(1u, kAbB, kAbB);                  // both K-major
+constexpr uint32_t kIdescDkv = make_idesc(1u, kAbB, kAbD, false, true);   // A K-major (or TMEM), B MN-major
+constexpr uint32_t kIdescDq = make_idesc(1u, kAbB, kAbD, true, true);     // both MN-major
 // 16 consecutive 32-bit columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -159,9 +197,148 @@ __device__ __forceinline__ uint64_t ab_ds_mn_desc(uint32_t saddr) {
     d |= static_cast<uint64_t>(2u) << 61;
     return d;
 }
-__device__ __forceinline__ void red_add_v4(float* p, float a, float b, float c, float d) {
-    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d)
+// A tile of the workspace from shared memory: stored, or added to what is there.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
                  : "memory");
+}
+__device__ __forceinline__ void bulk_add_f32(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(dst), "r"(src),
+                 "r"(bytes)
+                 : "memory");
+}
+// Wait until this thread's bulk operations have completed, not only read their source.
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ---- one thread's key and 64 of the block's queries ----
+
+// p = 2^(s scale log2(e) - lse log2(e)); nl = -lse log2(e) of the queries.
+__device__ __forceinline__ void ab_probs(const uint32_t (&s)[2][32], const float* nl, uint64_t sl2,
+                                         uint64_t (&p)[2][16]) {
+#pragma unroll
+    for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+            const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(nl + 32 * ch + c);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float x0, x1;
+                ab_unpack(ab_fma2(ab_pack(__uint_as_float(s[ch][c + 2 * k]), __uint_as_float(s[ch][c + 2 * k + 1])), sl2,
+                                  k ? l.y : l.x),
+                          x0, x1);
+                p[ch][c / 2 + k] = ab_pack(ab_ex2(x0), ab_ex2(x1));
+            }
+        }
+}
+// Only queries from `from` on see the key.
+__device__ __forceinline__ void ab_hide(uint64_t (&p)[2][16], int from) {
+#pragma unroll
+    for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            float x0, x1;
+            ab_unpack(p[ch][c], x0, x1);
+            p[ch][c] = ab_pack(32 * ch + 2 * c >= from ? x0 : 0.f, 32 * ch + 2 * c + 1 >= from ? x1 : 0.f);
+        }
+}
+// P' in bf16 to 32 columns of TMEM.
+__device__ __forceinline__ void ab_put_p(uint32_t taddr, const uint64_t (&p)[2][16]) {
+#pragma unroll
+    for (int ch = 0; ch < 2; ++ch) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            float x0, x1;
+            ab_unpack(p[ch][c], x0, x1);
+            pk[c] = pack_bf16x2(x0, x1);
+        }
+        tmem_st16(taddr + 16u * ch, pk);
+    }
+    ab_tmem_wait_st();
+}
+// ds = p (dp - delta) of 32 queries in bf16 to the thread's row of dS'; nd = -delta.
+// MASKED: a hidden pair takes nothing from dp or delta, whatever they are.
+template <bool MASKED>
+__device__ __forceinline__ void ab_put_ds(int ch, const uint32_t (&dp)[32], const uint64_t (&p)[16], const float* nd,
+                                          uint8_t* ds_row, int r, int from) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+        const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(nd + c);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint64_t x = ab_pack(__uint_as_float(dp[c + 2 * k]), __uint_as_float(dp[c + 2 * k + 1]));
+            float x0, x1;
+            ab_unpack(ab_mul2(p[c / 2 + k], ab_add2(x, k ? d.y : d.x)), x0, x1);
+            if constexpr (MASKED) {
+                x0 = 32 * ch + c + 2 * k >= from ? x0 : 0.f;
+                x1 = 32 * ch + c + 2 * k + 1 >= from ? x1 : 0.f;
+            }
+            pk[c / 2 + k] = pack_bf16x2(x0, x1);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        *reinterpret_cast<uint4*>(ds_row + (((4 * ch + v) ^ (r & 7)) << 4)) =
+            make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+}
+// 8 * N fp32 values, scaled, in bf16 to pieces `first`.. of row r of a 128-byte-swizzled tile.
+template <int N>
+__device__ __forceinline__ void ab_stage(uint8_t* tile, int r, int first, const uint32_t* v, float f) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const uint32_t* x = v + 8 * k;
+        *reinterpret_cast<uint4*>(tile + r * 128 + (((first + k) ^ (r & 7)) << 4)) =
+            make_uint4(pack_bf16x2(__uint_as_float(x[0]) * f, __uint_as_float(x[1]) * f),
+                       pack_bf16x2(__uint_as_float(x[2]) * f, __uint_as_float(x[3]) * f),
+                       pack_bf16x2(__uint_as_float(x[4]) * f, __uint_as_float(x[5]) * f),
+                       pack_bf16x2(__uint_as_float(x[6]) * f, __uint_as_float(x[7]) * f));
+    }
+}
+
+// Statistics of 128 queries of one head by 256 threads (two a query): -lse
+// log2(e), -inf (probability 0) past the sequence's end and for a query that sees
+// no key, and -delta.
+__device__ __forceinline__ void ab_stats(const uint16_t* out, const uint16_t* dout, const float* lse, int T, int H,
+                                         int b, int h, int i, float* st) {
+    const int row = threadIdx.x >> 1, half = threadIdx.x & 1;
+    const int t = i * kAbB + row;
+    float sum = 0.f;
+    if (t < T) {
+        const size_t off = ((size_t)b * T + t) * ((size_t)H * kAbD) + h * kAbD + 32 * half;
+        uint4 o[4], g[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            o[k] = *reinterpret_cast<const uint4*>(out + off + 8 * k);
+            g[k] = *reinterpret_cast<const uint4*>(dout + off + 8 * k);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t x[4] = {o[k].x, o[k].y, o[k].z, o[k].w}, y[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), sum);
+                sum = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), sum);
+            }
+        }
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    if (half) {
+        st[kAbB + row] = -sum;
+    } else {
+        const float l = t < T ? lse[((size_t)b * H + h) * T + t] : -INFINITY;
+        st[row] = l == -INFINITY ? -INFINITY : -l * kAbLog2e;
+    }
 }
 
 // The block's items: rounds of gridDim.x items, every other round in reverse, so
@@ -200,52 +377,51 @@ struct AbWalker {
 __global__ void __launch_bounds__(kAbThreads, 1)
 attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant__ CUtensorMap tmDo,
                 const __grid_constant__ CUtensorMap tmDqkv, const AbArgs a) {
-    constexpr uint32_t IDESC_S = make_idesc(1u, kAbB, kAbB);                  // both K-major
-    constexpr uint32_t IDESC_DKV = make_idesc(1u, kAbB, kAbD, false, true);   // A K-major (or TMEM), B MN-major
-    constexpr uint32_t IDESC_DQ = make_idesc(1u, kAbB, kAbD, true, true);     // both MN-major
-    constexpr int KS = kAbKvStages, QS = kAbQStages;
-
+    constexpr int KS = kAbKStages, QS = kAbQStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* sKV = smem;                       // stage: K, V
-    uint8_t* sQ = sKV + KS * 2 * kAbTile;      // stage: Q, dO, statistics
+    uint8_t* sK = smem;
+    uint8_t* sV = sK + KS * kAbTile;
+    uint8_t* sQ = sV + kAbTile;                // stage: Q, dO, statistics
     uint8_t* sDS = sQ + QS * kAbQStage;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sDS + kAbDs);
+    uint8_t* sOut = sDS + kAbDs;               // dq on its way out; dk and dv at an item's end
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + kAbDqTile);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kAbBars);
     int* s_abort = reinterpret_cast<int*>(tmem_slot + 1);
-    int* s_go = s_abort + 1;
 
-    const uint32_t kvfull = smem_u32(bars), kvempty = kvfull + 8 * KS, qfull = kvempty + 8 * KS,
-                   qempty = qfull + 8 * QS, one = qempty + 8 * QS;
-    const uint32_t sfull = one, sread = one + 8, pready = one + 16, pvdone = one + 24, dpfull = one + 32,
-                   dpread = one + 40, dsready = one + 48, dsfree = one + 56, dqfull = one + 64, dqfree = one + 72,
-                   accfull = one + 80, accfree = one + 88, drained = one + 96;
+    // Full / empty of the stages; then, once a step: sfull, dpfull, done (the
+    // products of S', of dV and dP', of dK and dQ), sread, pready, dpread, dsready
+    // (the eight warps), dqfree, accfree, met (the four).
+    const uint32_t kfull = smem_u32(bars), kempty = kfull + 8 * KS, vfull = kempty + 8 * KS, vempty = vfull + 8,
+                   qfull = vempty + 8, qempty = qfull + 8 * QS, one_a_step = qempty + 8 * QS;
+    const uint32_t sfull = one_a_step, dpfull = one_a_step + 8, done = one_a_step + 16, sread = one_a_step + 24,
+                   pready = one_a_step + 32, dpread = one_a_step + 40, dsready = one_a_step + 48,
+                   dqfree = one_a_step + 56, accfree = one_a_step + 64, met = one_a_step + 72;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (the same in every lane, and known to be: roles branch without divergence)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < KS; ++s) {
-            mbar_init(kvfull + 8 * s, 1);
-            mbar_init(kvempty + 8 * s, 4);
+            mbar_init(kfull + 8 * s, 1);
+            mbar_init(kempty + 8 * s, 4);
         }
+        mbar_init(vfull, 1);
+        mbar_init(vempty, 8);
         for (int s = 0; s < QS; ++s) {
             mbar_init(qfull + 8 * s, 1);
-            mbar_init(qempty + 8 * s, a.single ? 4 : 1);
+            mbar_init(qempty + 8 * s, 4);
         }
         mbar_init(sfull, 1);
+        mbar_init(dpfull, 1);
+        mbar_init(done, 1);
         mbar_init(sread, 8);
         mbar_init(pready, 8);
-        mbar_init(pvdone, 1);
-        mbar_init(dpfull, 1);
         mbar_init(dpread, 8);
         mbar_init(dsready, 8);
-        mbar_init(dsfree, 1);
-        mbar_init(dqfull, 1);
         mbar_init(dqfree, 4);
-        mbar_init(accfull, 1);
         mbar_init(accfree, 4);
-        mbar_init(drained, 4);
+        mbar_init(met, 4);
         *s_abort = 0;
-        *s_go = 1;
         mbar_fence_init();
         tma_prefetch_map(&tmQkv);
         tma_prefetch_map(&tmDo);
@@ -255,152 +431,163 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     if (threadIdx.x == 0) pdl_launch_dependents();
 
     auto give_up = [&]() {
         atomicExch(s_abort, 1);
         atomicExch(a.status, (int)LIN_ERR_DEVICE_TIMEOUT);
     };
-    auto aborted = [&]() { return *(volatile int*)s_abort != 0; };
+    // A warp's wait: false when it, or another warp's, has run out.
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, *(volatile int*)s_abort == 0 && mbar_wait(bar, parity)) != 0;
+    };
+    auto arrive = [&](uint32_t bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
 
+    if (warp < 4) regs_dec<kAbRegsIssue>();
     if (warp == 0) {
-        if (lane == 0) {
-            pdl_wait();  // the statistics are the previous kernel's output
-            uint32_t m = 0, n = 0;
-            bool ok = true;
-            AbWalker w;
-            for (w.init(a); ok && w.valid; w.next_item(a), ++m) {
-                const int bh = a.bh0 + w.bh, b = bh / a.H, h = bh % a.H;
-                const uint32_t ks = m % KS;
-                if (aborted() || !mbar_wait(kvempty + 8 * ks, ((m / KS) & 1) ^ 1)) {
+        // ---- TMA ----
+        pdl_wait();  // the statistics are the previous kernel's output
+        uint32_t m = 0, n = 0;
+        bool ok = true;
+        AbWalker w;
+        for (w.init(a); ok && w.valid; w.next_item(a), ++m) {
+            const int bh = a.bh0 + w.bh, b = bh / a.H, h = bh % a.H;
+            const uint32_t ks = m % KS;
+            if (!wait(kempty + 8 * ks, ((m / KS) & 1) ^ 1)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                mbar_expect_tx(kfull + 8 * ks, kAbTile);
+                tma_load_3d(smem_u32(sK + ks * kAbTile), &tmQkv, kfull + 8 * ks, a.C + h * kAbD, w.j * kAbB, b);
+            }
+            for (int i = w.i0; i < a.nb; ++i, ++n) {
+                const uint32_t qs = n % QS;
+                if (!wait(qempty + 8 * qs, ((n / QS) & 1) ^ 1)) {
                     ok = false;
                     break;
                 }
-                uint8_t* kv = sKV + ks * 2 * kAbTile;
-                mbar_expect_tx(kvfull + 8 * ks, 2 * kAbTile);
-                tma_load_3d(smem_u32(kv), &tmQkv, kvfull + 8 * ks, a.C + h * kAbD, w.j * kAbB, b);
-                tma_load_3d(smem_u32(kv + kAbTile), &tmQkv, kvfull + 8 * ks, 2 * a.C + h * kAbD, w.j * kAbB, b);
-                for (int i = w.i0; i < a.nb; ++i, ++n) {
-                    const uint32_t qs = n % QS;
-                    if (aborted() || !mbar_wait(qempty + 8 * qs, ((n / QS) & 1) ^ 1)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* q = sQ + qs * kAbQStage;
+                uint8_t* q = sQ + qs * kAbQStage;
+                if (lane == 0) {
                     mbar_expect_tx(qfull + 8 * qs, kAbQStage);
                     tma_load_3d(smem_u32(q), &tmQkv, qfull + 8 * qs, h * kAbD, i * kAbB, b);
                     tma_load_3d(smem_u32(q + kAbTile), &tmDo, qfull + 8 * qs, h * kAbD, i * kAbB, b);
                     bulk_load(smem_u32(q + 2 * kAbTile), a.stats + ((size_t)w.bh * a.nb + i) * (2 * kAbB), kAbStat,
                               qfull + 8 * qs);
                 }
-                if (!ok) {
-                    ++m;  // its K and V are in flight
-                    break;
-                }
-            }
-            if (!ok) {
-                give_up();
-                // let the copies still in flight land before the block exits
-                for (uint32_t k = m > (uint32_t)KS ? m - KS : 0; k < m; ++k) mbar_wait(kvfull + 8 * (k % KS), (k / KS) & 1);
-                for (uint32_t k = n > (uint32_t)QS ? n - QS : 0; k < n; ++k) mbar_wait(qfull + 8 * (k % QS), (k / QS) & 1);
-            }
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            AbWalker cur, lead;
-            cur.init(a);
-            lead.init(a);
-            uint32_t n = 0;
-            bool ok = true;
-            auto issue_s = [&](uint32_t k) {  // S' of step k, the lead's
-                if (aborted() || (lead.first() && !mbar_wait(kvfull + 8 * (lead.m % KS), (lead.m / KS) & 1)) ||
-                    !mbar_wait(qfull + 8 * (k % QS), (k / QS) & 1) || (k > 0 && !mbar_wait(sread, (k - 1) & 1)))
-                    return false;
-                tc_fence_after();
-                const uint64_t kd = sw128_kmajor_desc(smem_u32(sKV + (lead.m % KS) * 2 * kAbTile));
-                const uint64_t qd = sw128_kmajor_desc(smem_u32(sQ + (k % QS) * kAbQStage));
-#pragma unroll
-                for (int kk = 0; kk < kAbD / 16; ++kk)
-                    tc_mma<true>(tmem + kAbS, kd + 2u * kk, qd + 2u * kk, IDESC_S, kk != 0 ? 1u : 0u);
-                tc_commit(sfull);
-                return true;
-            };
-            auto issue_dp = [&](uint32_t k) {  // dP' of step k
-                if (aborted() || (k > 0 && !mbar_wait(dpread, (k - 1) & 1))) return false;
-                tc_fence_after();
-                const uint64_t vd = sw128_kmajor_desc(smem_u32(sKV + (lead.m % KS) * 2 * kAbTile + kAbTile));
-                const uint64_t od = sw128_kmajor_desc(smem_u32(sQ + (k % QS) * kAbQStage + kAbTile));
-#pragma unroll
-                for (int kk = 0; kk < kAbD / 16; ++kk)
-                    tc_mma<true>(tmem + kAbDp, vd + 2u * kk, od + 2u * kk, IDESC_S, kk != 0 ? 1u : 0u);
-                tc_commit(dpfull);
-                return true;
-            };
-            if (cur.valid) {
-                ok = issue_s(0) && issue_dp(0);
-                lead.next(a);
-            }
-            while (ok && cur.valid) {
-                const bool first = cur.first(), last = cur.last(a);
-                if (lead.valid && !issue_s(n + 1)) {
-                    ok = false;
-                    break;
-                }
-                // dV += P' dO
-                if (aborted() || !mbar_wait(pready, n & 1) ||
-                    (first && cur.m > 0 && !mbar_wait(accfree, (cur.m - 1) & 1))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                uint8_t* q = sQ + (n % QS) * kAbQStage;
-                const uint64_t od = sw128_mnmajor_desc(smem_u32(q + kAbTile));
-#pragma unroll
-                for (int kk = 0; kk < kAbB / 16; ++kk)
-                    tc_mma_ts(tmem + kAbDv, tmem + kAbP + 8u * kk, od + 128u * kk, IDESC_DKV,
-                              (kk != 0 || !first) ? 1u : 0u);
-                tc_commit(pvdone);
-                if (lead.valid) {
-                    if (!issue_dp(n + 1)) {
+                if (i == w.i0) {  // V's one stage frees when the item before has its last dP'
+                    if (!wait(vempty, (m & 1) ^ 1)) {
+                        ++n;
                         ok = false;
                         break;
                     }
-                    lead.next(a);
+                    if (lane == 0) {
+                        mbar_expect_tx(vfull, kAbTile);
+                        tma_load_3d(smem_u32(sV), &tmQkv, vfull, 2 * a.C + h * kAbD, w.j * kAbB, b);
+                    }
                 }
-                // dK += dS' Q, dQ = dS K
-                if (aborted() || !mbar_wait(dsready, n & 1) || (n > 0 && !mbar_wait(dqfree, (n - 1) & 1))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t dsk = sw128_kmajor_desc(smem_u32(sDS)), dsm = ab_ds_mn_desc(smem_u32(sDS));
-                const uint64_t qd = sw128_mnmajor_desc(smem_u32(q));
-                const uint64_t kd = sw128_mnmajor_desc(smem_u32(sKV + (cur.m % KS) * 2 * kAbTile));
-#pragma unroll
-                for (int kk = 0; kk < kAbB / 16; ++kk)
-                    tc_mma<true>(tmem + kAbDk, dsk + 1024u * (kk >> 2) + 2u * (kk & 3), qd + 128u * kk, IDESC_DKV,
-                                 (kk != 0 || !first) ? 1u : 0u);
-#pragma unroll
-                for (int kk = 0; kk < kAbB / 16; ++kk)
-                    tc_mma<true>(tmem + kAbDq, dsm + 128u * kk, kd + 128u * kk, IDESC_DQ, kk != 0 ? 1u : 0u);
-                tc_commit(dsfree);
-                tc_commit(dqfull);
-                if (!a.single) tc_commit(qempty + 8 * (n % QS));
-                if (last) tc_commit(accfull);
-                cur.next(a);
-                ++n;
             }
             if (!ok) {
-                give_up();
-                // the products issued so far end before the block does: one more
-                // commit on a barrier whose phase the other warps no longer follow
-                tc_commit(accfull);
-                mbar_wait(accfull, cur.m & 1);
+                ++m;  // its K is in flight, and V if it came that far
+                break;
             }
         }
+        if (!ok) {
+            if (lane == 0) {
+                give_up();
+                // let the copies still in flight land before the block exits
+                for (uint32_t k = m > (uint32_t)KS ? m - KS : 0; k < m; ++k) mbar_wait(kfull + 8 * (k % KS), (k / KS) & 1);
+                for (uint32_t k = n > (uint32_t)QS ? n - QS : 0; k < n; ++k) mbar_wait(qfull + 8 * (k % QS), (k / QS) & 1);
+                if (m > 0) mbar_wait(vfull, (m - 1) & 1);
+            }
+            __syncwarp();
+        }
+    } else if (warp == 1) {
+        // ---- tcgen05.mma ----
+        const uint32_t one = lane == 0;
+        AbWalker cur, lead;
+        cur.init(a);
+        lead.init(a);
+        uint32_t n = 0;
+        bool ok = true;
+        auto issue_s = [&](uint32_t k) {  // S' of step k, the lead's
+            if ((lead.first() && !wait(kfull + 8 * (lead.m % KS), (lead.m / KS) & 1)) ||
+                !wait(qfull + 8 * (k % QS), (k / QS) & 1) || (k > 0 && !wait(sread, (k - 1) & 1)))
+                return false;
+            tc_fence_after();
+            const uint64_t kd = sw128_kmajor_desc(smem_u32(sK + (lead.m % KS) * kAbTile));
+            const uint64_t qd = sw128_kmajor_desc(smem_u32(sQ + (k % QS) * kAbQStage));
+#pragma unroll
+            for (int kk = 0; kk < kAbD / 16; ++kk)
+                ab_mma(one, tmem + kAbS, kd + 2u * kk, qd + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
+            ab_commit(one, sfull);
+            return true;
+        };
+        // dV of step k - 1 (`with_dv`) in turn with dP' of step k (`with_dp`, the lead's)
+        auto issue_dv_dp = [&](uint32_t k, bool with_dv, bool dv_first, bool with_dp) {
+            if ((with_dp && lead.first() && !wait(vfull, lead.m & 1)) || (k > 0 && !wait(dpread, (k - 1) & 1)))
+                return false;
+            tc_fence_after();
+            const uint64_t dod = sw128_mnmajor_desc(smem_u32(sQ + ((k + QS - 1) % QS) * kAbQStage + kAbTile));
+            const uint64_t vd = sw128_kmajor_desc(smem_u32(sV));
+            const uint64_t od = sw128_kmajor_desc(smem_u32(sQ + (k % QS) * kAbQStage + kAbTile));
+#pragma unroll
+            for (int kk = 0; kk < kAbB / 16; ++kk) {
+                if (with_dv)
+                    ab_mma_ts(one, tmem + kAbDv, tmem + kAbP + 8u * kk, dod + 128u * kk, kIdescDkv,
+                              (kk != 0 || !dv_first) ? 1u : 0u);
+                if (with_dp && (kk & 1) == 0)
+                    ab_mma(one, tmem + kAbDp, vd + 1u * kk, od + 1u * kk, kIdescS, kk != 0 ? 1u : 0u);
+            }
+            ab_commit(one, dpfull);
+            return true;
+        };
+        if (cur.valid) {
+            ok = issue_s(0) && issue_dv_dp(0, false, false, true);
+            lead.next(a);
+        }
+        while (ok && cur.valid) {
+            const bool first = cur.first();
+            if (lead.valid && !issue_s(n + 1)) ok = false;
+            if (!ok || !wait(pready, n & 1) || (first && cur.m > 0 && !wait(accfree, (cur.m - 1) & 1)) ||
+                !issue_dv_dp(n + 1, true, first, lead.valid)) {
+                ok = false;
+                break;
+            }
+            if (lead.valid) lead.next(a);
+            // dK += dS' Q in turn with dQ = dS K
+            if (!wait(dsready, n & 1) || (n > 0 && !wait(dqfree, (n - 1) & 1))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint64_t dsk = sw128_kmajor_desc(smem_u32(sDS)), dsm = ab_ds_mn_desc(smem_u32(sDS));
+            const uint64_t qd = sw128_mnmajor_desc(smem_u32(sQ + (n % QS) * kAbQStage));
+            const uint64_t kd = sw128_mnmajor_desc(smem_u32(sK + (cur.m % KS) * kAbTile));
+#pragma unroll
+            for (int kk = 0; kk < kAbB / 16; ++kk) {
+                ab_mma(one, tmem + kAbDk, dsk + 1024u * (kk >> 2) + 2u * (kk & 3), qd + 128u * kk, kIdescDkv,
+                       (kk != 0 || !first) ? 1u : 0u);
+                ab_mma(one, tmem + kAbDq, dsm + 128u * kk, kd + 128u * kk, kIdescDq, kk != 0 ? 1u : 0u);
+            }
+            ab_commit(one, done);
+            cur.next(a);
+            ++n;
+        }
+        if (!ok) {
+            if (lane == 0) give_up();
+            __syncwarp();
+            // the products issued so far end before the block does
+            ab_commit(one, done);
+            mbar_wait(done, n & 1);
+        }
     } else if (warp >= 4 && warp < 12) {
-        pdl_wait();
+        // ---- P' and dS' ----
+        regs_inc<kAbRegsSoftmax>();
         const int grp = (warp - 4) >> 2, quad = warp & 3;
         const int r = 32 * quad + lane;  // key within the block, TMEM lane
         const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
@@ -417,11 +604,8 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
             const bool masked = diag || (w.j + 1) * kAbB > a.T;
             // query c of this group is visible to the thread's key from `from` on
             const int from = w.j * kAbB + r >= a.T ? 64 : diag ? r - 64 * grp : 0;
-            if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(qfull + 8 * (n % QS), (n / QS) & 1) &&
-                                             mbar_wait(sfull, n & 1))) {
-                ok = false;
-                break;
-            }
+            ok = wait(qfull + 8 * (n % QS), (n / QS) & 1) && wait(sfull, n & 1);
+            if (!ok) break;
             tc_fence_after();
             uint32_t s[2][32];
             tmem_ld32_async(tS, s[0]);
@@ -429,220 +613,142 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
             tmem_wait_ld(s[0]);
             tmem_wait_ld(s[1]);
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sread);
-            // p = 2^(s scale log2(e) - lse log2(e))
+            arrive(sread);
             uint64_t p[2][16];
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(stat + 32 * ch + c);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float x0, x1;
-                        ab_unpack(ab_fma2(ab_pack(__uint_as_float(s[ch][c + 2 * k]), __uint_as_float(s[ch][c + 2 * k + 1])),
-                                          sl2, k ? l.y : l.x),
-                                  x0, x1);
-                        p[ch][c / 2 + k] = ab_pack(ab_ex2(x0), ab_ex2(x1));
-                    }
-                }
-            if (masked) {
-#pragma unroll
-                for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        float x0, x1;
-                        ab_unpack(p[ch][c], x0, x1);
-                        p[ch][c] = ab_pack(32 * ch + 2 * c >= from ? x0 : 0.f, 32 * ch + 2 * c + 1 >= from ? x1 : 0.f);
-                    }
-            }
-            if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(pvdone, (n - 1) & 1))) {
-                ok = false;
-                break;
-            }
+            ab_probs(s, stat, sl2, p);
+            if (masked) ab_hide(p, from);
+            // dP' of this step, and so dV of the step before: P' may be rewritten
+            ok = wait(dpfull, n & 1);
+            if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    float x0, x1;
-                    ab_unpack(p[ch][c], x0, x1);
-                    pk[c] = pack_bf16x2(x0, x1);
-                }
-                tmem_st16(tP + 16u * ch, pk);
-            }
-            ab_tmem_wait_st();
+            tmem_ld32_async(tDp, s[0]);
+            tmem_ld32_async(tDp + 32u, s[1]);
+            ab_put_p(tP, p);
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pready);
-            // ds = p (dp - delta)
-            if (!__all_sync(0xffffffffu, mbar_wait(dpfull, n & 1) && (n == 0 || mbar_wait(dsfree, (n - 1) & 1)))) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
+            arrive(pready);
+            tmem_wait_ld(s[0]);
+            tmem_wait_ld(s[1]);
+            tc_fence_before();
+            arrive(dpread);
+            if (w.last(a)) arrive(vempty);
+            // dK and dQ of the step before: dS' may be rewritten
+            ok = n == 0 || wait(done, (n - 1) & 1);
+            if (!ok) break;
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch) {
-                tmem_ld32_async(tDp + 32u * ch, s[0]);
-                tmem_wait_ld(s[0]);
-                if (ch == 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(dpread);
-                }
-                uint32_t pk[16];
-#pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(stat + kAbB + 32 * ch + c);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint64_t dp = ab_pack(__uint_as_float(s[0][c + 2 * k]), __uint_as_float(s[0][c + 2 * k + 1]));
-                        float x0, x1;
-                        ab_unpack(ab_mul2(p[ch][c / 2 + k], ab_add2(dp, k ? d.y : d.x)), x0, x1);
-                        if (masked) {  // a masked pair takes nothing from dp, whatever it is
-                            x0 = 32 * ch + c + 2 * k >= from ? x0 : 0.f;
-                            x1 = 32 * ch + c + 2 * k + 1 >= from ? x1 : 0.f;
-                        }
-                        pk[c / 2 + k] = pack_bf16x2(x0, x1);
-                    }
-                }
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    *reinterpret_cast<uint4*>(ds_row + (((4 * ch + v) ^ (r & 7)) << 4)) =
-                        make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+                if (masked) ab_put_ds<true>(ch, s[ch], p[ch], stat + kAbB + 32 * ch, ds_row, r, from);
+                else ab_put_ds<false>(ch, s[ch], p[ch], stat + kAbB + 32 * ch, ds_row, r, from);
             }
             fence_proxy_async_smem();
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(dsready);
+            arrive(dsready);
         }
-        if (!ok) give_up();
+        if (!ok && lane == 0) give_up();
     } else if (warp >= 12) {
+        // ---- dq, dk and dv out ----
+        regs_dec<kAbRegsOut>();
         pdl_wait();
         const int quad = warp & 3;
         const int r = 32 * quad + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-        // 64 fp32 columns of this thread's lane, scaled, as a bf16 row of a 128-byte-swizzled tile
-        auto stage_row = [&](uint8_t* tile, const uint32_t (&v)[2][32], float f) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t* x = &v[k >> 2][8 * (k & 3)];
-                *reinterpret_cast<uint4*>(tile + r * 128 + ((k ^ (r & 7)) << 4)) = make_uint4(
-                    pack_bf16x2(__uint_as_float(x[0]) * f, __uint_as_float(x[1]) * f),
-                    pack_bf16x2(__uint_as_float(x[2]) * f, __uint_as_float(x[3]) * f),
-                    pack_bf16x2(__uint_as_float(x[4]) * f, __uint_as_float(x[5]) * f),
-                    pack_bf16x2(__uint_as_float(x[6]) * f, __uint_as_float(x[7]) * f));
-            }
-        };
+        const bool sender = threadIdx.x == 12 * 32;
         auto read64 = [&](uint32_t col, uint32_t (&v)[2][32]) {
             tmem_ld32_async(tmem + lanes + col, v[0]);
             tmem_ld32_async(tmem + lanes + col + 32u, v[1]);
             tmem_wait_ld(v[0]);
             tmem_wait_ld(v[1]);
         };
-        uint32_t n = 0, syncs = 0;
+        uint32_t n = 0, meets = 0;
         bool ok = true;
-        // the four warps meet (bounded, like every wait here)
-        auto meet = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(drained);
-            return __all_sync(0xffffffffu, mbar_wait(drained, syncs++ & 1)) != 0;
+        auto meet = [&]() {  // the four warps
+            arrive(met);
+            return wait(met, meets++ & 1);
+        };
+        // A chain's tile that the sender has under way: its counter is raised once
+        // the addition has completed (a step later).
+        unsigned* pending = nullptr;
+        unsigned pending_value = 0;
+        auto settle = [&]() {
+            if (!pending) return;
+            bulk_wait_all();
+            fence_proxy_async_global();
+            __threadfence();
+            st_release_gpu(pending, pending_value);
+            pending = nullptr;
         };
         AbWalker w;
         for (w.init(a); w.valid; w.next(a), ++n) {
             const int bh = a.bh0 + w.bh, b = bh / a.H, h = bh % a.H;
             const bool last = w.last(a);
-            if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(dqfull, n & 1))) {
-                ok = false;
-                break;
-            }
+            ok = wait(done, n & 1);
+            if (!ok) break;
             tc_fence_after();
+            arrive(qempty + 8 * (n % QS));
+            if (last) arrive(kempty + 8 * (w.m % KS));
             uint32_t v[2][32];
             read64(kAbDq, v);
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(dqfree);
-            uint8_t* q = sQ + (n % QS) * kAbQStage;
-            if (a.single) {
-                // the step's products are complete: its Q tile holds dq on the way out
-                stage_row(q, v, a.scale);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    ab_store_3d(&tmDqkv, smem_u32(q + quad * 4096), h * kAbD, w.i * kAbB + 32 * quad, b);
-                    bulk_commit();
-                }
-            } else {
+            arrive(dqfree);
+            if (lane == 0) bulk_wait_read_all();  // what this warp sent has been read out
+            ok = meet();
+            if (!ok) break;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const uint32_t* x = &v[c >> 3][4 * (c & 7)];
+                *reinterpret_cast<uint4*>(sOut + c * (kAbB * 16) + r * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            fence_proxy_async_smem();
+            ok = meet();
+            if (!ok) break;
+            if (sender) {
+                settle();
                 const int chain = w.j % a.chains, pos = w.j / a.chains;
                 const size_t slot = ((size_t)w.bh * a.chains + chain) * a.nb + w.i;
-                if (pos > 0) {
-                    if (threadIdx.x == 12 * 32) {
-                        // until the chain's earlier block has added to this tile
-                        const unsigned long long t0 = global_ns();
-                        bool there = false;
-                        for (uint32_t k = 0; k < kWaitIters; ++k) {
-                            there = ld_acquire_gpu(a.flags + slot) == (unsigned)pos;
-                            if (there || aborted()) break;
-                            if ((k & 63u) == 63u && global_ns() - t0 > kWaitNs) break;
-                        }
-                        // (once 0 it stays 0: the block gives up)
-                        if (!there) *(volatile int*)s_go = 0;
+                float* tile = a.dq + slot * (kAbDqTile / 4);
+                if (pos == 0) {
+                    bulk_store(tile, smem_u32(sOut), kAbDqTile);
+                } else {
+                    // until the chain's earlier block has added to this tile
+                    const unsigned long long t0 = global_ns();
+                    bool there = ld_acquire_gpu(a.flags + slot) == (unsigned)pos;
+                    for (uint32_t k = 1; !there && k < kWaitIters; ++k) {
+                        there = ld_acquire_gpu(a.flags + slot) == (unsigned)pos;
+                        if ((k & 63u) == 63u && (*(volatile int*)s_abort != 0 || global_ns() - t0 > kWaitNs)) break;
                     }
-                    ok = meet() && *(volatile int*)s_go != 0;
-                    if (!ok) break;
+                    fence_proxy_async_global();
+                    if (there) bulk_add_f32(tile, smem_u32(sOut), kAbDqTile);
+                    else give_up();
                 }
-                float* tile = a.dq + slot * (kAbDqTile / 4) + r * 4;
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const uint32_t* x = &v[c >> 3][4 * (c & 7)];
-                    float* dst = tile + c * (kAbB * 4);
-                    if (pos == 0)
-                        *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
-                    else
-                        red_add_v4(dst, __uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]),
-                                   __uint_as_float(x[3]));
-                }
+                bulk_commit();
                 if (w.j + a.chains <= (a.causal ? w.i : a.nb - 1)) {
-                    ok = meet();
-                    if (!ok) break;
-                    if (threadIdx.x == 12 * 32) {
-                        __threadfence();
-                        st_release_gpu(a.flags + slot, (unsigned)pos + 1u);
-                    }
+                    pending = a.flags + slot;
+                    pending_value = (unsigned)pos + 1u;
                 }
             }
+            __syncwarp();
             if (last) {
-                // dk and dv of the item, through its K and V tiles
-                if (!__all_sync(0xffffffffu, mbar_wait(accfull, w.m & 1))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                uint8_t* kv = sKV + (w.m % KS) * 2 * kAbTile;
                 read64(kAbDk, v);
-                stage_row(kv, v, a.scale);
+                if (lane == 0) bulk_wait_read_all();
+                ok = meet();
+                if (!ok) break;
+                ab_stage<8>(sOut, r, 0, &v[0][0], a.scale);
                 read64(kAbDv, v);
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(accfree);
-                stage_row(kv + kAbTile, v, 1.0f);
+                arrive(accfree);
+                ab_stage<8>(sOut + kAbTile, r, 0, &v[0][0], 1.0f);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     const int y = w.j * kAbB + 32 * quad;  // tokens past T lie outside the map and are not written
-                    ab_store_3d(&tmDqkv, smem_u32(kv + quad * 4096), a.C + h * kAbD, y, b);
-                    ab_store_3d(&tmDqkv, smem_u32(kv + kAbTile + quad * 4096), 2 * a.C + h * kAbD, y, b);
+                    ab_store_3d(&tmDqkv, smem_u32(sOut + quad * 4096), a.C + h * kAbD, y, b);
+                    ab_store_3d(&tmDqkv, smem_u32(sOut + kAbTile + quad * 4096), 2 * a.C + h * kAbD, y, b);
                     bulk_commit();
-                    bulk_wait_read_all();
-                    mbar_arrive(kvempty + 8 * (w.m % KS));
-                    if (a.single) mbar_arrive(qempty + 8 * (n % QS));
                 }
                 __syncwarp();
             }
         }
-        if (!ok) give_up();
+        if (sender && ok) settle();
+        if (!ok && lane == 0) give_up();
         if (lane == 0) bulk_wait_read_all();
     }
 
@@ -655,47 +761,162 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
     }
 }
 
-// Statistics of 128 queries of one head (two threads a query): -lse log2(e),
-// -inf (probability 0) past the sequence's end and for a query that sees no key,
-// and -delta. Also zeroes the dq counters of the head's query block.
+// T <= 128: a block per (sequence, head). Thread: a key (TMEM lane) and 64 queries.
+__global__ void __launch_bounds__(kAsThreads, 2)
+attn_bwd_short_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant__ CUtensorMap tmDo,
+                      const __grid_constant__ CUtensorMap tmDqkv, const uint16_t* out, const uint16_t* dout,
+                      const float* lse, const AbArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sK = smem, *sQ = sK + kAbTile, *sV = sQ + kAbTile, *sDO = sV + kAbTile, *sDS = sDO + kAbTile;
+    float* stat = reinterpret_cast<float*>(sDS + kAbDs);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(stat + 2 * kAbB);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6);
+    const uint32_t kq = smem_u32(bars), vdo = kq + 8, sfull = kq + 16, dpfull = kq + 24, done = kq + 32;
+
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < 5; ++k) mbar_init(kq + 8 * k, 1);
+        mbar_fence_init();
+        tma_prefetch_map(&tmQkv);
+        tma_prefetch_map(&tmDo);
+        tma_prefetch_map(&tmDqkv);
+    }
+    if (warp == 0) tmem_alloc(smem_u32(tmem_slot), kAsTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    pdl_wait();
+    if (threadIdx.x == 0) {
+        pdl_launch_dependents();
+        mbar_expect_tx(kq, 2 * kAbTile);
+        tma_load_3d(smem_u32(sK), &tmQkv, kq, a.C + h * kAbD, 0, b);
+        tma_load_3d(smem_u32(sQ), &tmQkv, kq, h * kAbD, 0, b);
+        mbar_expect_tx(vdo, 2 * kAbTile);
+        tma_load_3d(smem_u32(sV), &tmQkv, vdo, 2 * a.C + h * kAbD, 0, b);
+        tma_load_3d(smem_u32(sDO), &tmDo, vdo, h * kAbD, 0, b);
+    }
+    __syncwarp();
+    ab_stats(out, dout, lse, a.T, a.H, b, h, 0, stat);
+    // A wait that runs out sets the status word; the block then goes on with what
+    // it has, and its outputs are not to be used.
+    auto wait = [&](uint32_t bar) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar, 0))) {
+            if (lane == 0) atomicExch(a.status, (int)LIN_ERR_DEVICE_TIMEOUT);
+            mbar_wait(bar, 0);  // what is in flight once more before the block goes on
+            __syncwarp();
+        }
+    };
+    const uint32_t one = lane == 0;
+    wait(kq);
+    if (warp == 0) {
+        const uint64_t kd = sw128_kmajor_desc(smem_u32(sK)), qd = sw128_kmajor_desc(smem_u32(sQ));
+#pragma unroll
+        for (int kk = 0; kk < kAbD / 16; ++kk)
+            ab_mma(one, tmem + kAbS, kd + 2u * kk, qd + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
+        ab_commit(one, sfull);
+    }
+    wait(vdo);
+    if (warp == 0) {
+        const uint64_t vd = sw128_kmajor_desc(smem_u32(sV)), od = sw128_kmajor_desc(smem_u32(sDO));
+#pragma unroll
+        for (int kk = 0; kk < kAbD / 16; ++kk)
+            ab_mma(one, tmem + kAsDp, vd + 2u * kk, od + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
+        ab_commit(one, dpfull);
+    }
+    const int grp = warp >> 2, quad = warp & 3;
+    const int r = 32 * quad + lane;  // key, TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+    const bool masked = a.causal || a.T < kAbB;
+    const int from = r >= a.T ? 64 : a.causal ? r - 64 * grp : 0;
+    wait(sfull);
+    tc_fence_after();
+    uint32_t s[2][32];
+    tmem_ld32_async(tmem + lanes + kAbS + 64u * grp, s[0]);
+    tmem_ld32_async(tmem + lanes + kAbS + 64u * grp + 32u, s[1]);
+    tmem_wait_ld(s[0]);
+    tmem_wait_ld(s[1]);
+    tc_fence_before();
+    __syncthreads();  // S' has been read (P' and dQ take its place); the statistics are there
+    tc_fence_after();
+    uint64_t p[2][16];
+    ab_probs(s, stat + 64 * grp, ab_pack(a.scale_log2, a.scale_log2), p);
+    if (masked) ab_hide(p, from);
+    ab_put_p(tmem + lanes + kAsP + 32u * grp, p);
+    wait(dpfull);
+    tc_fence_after();
+    uint8_t* ds_row = sDS + grp * (kAbDs / 2) + r * 128;
+#pragma unroll
+    for (int ch = 0; ch < 2; ++ch) {
+        const float* nd = stat + kAbB + 64 * grp + 32 * ch;
+        tmem_ld32_async(tmem + lanes + kAsDp + 64u * grp + 32u * ch, s[0]);
+        tmem_wait_ld(s[0]);
+        if (masked) ab_put_ds<true>(ch, s[0], p[ch], nd, ds_row, r, from);
+        else ab_put_ds<false>(ch, s[0], p[ch], nd, ds_row, r, from);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) {
+        const uint64_t od = sw128_mnmajor_desc(smem_u32(sDO)), qd = sw128_mnmajor_desc(smem_u32(sQ)),
+                       kd = sw128_mnmajor_desc(smem_u32(sK));
+        const uint64_t dsk = sw128_kmajor_desc(smem_u32(sDS)), dsm = ab_ds_mn_desc(smem_u32(sDS));
+#pragma unroll
+        for (int kk = 0; kk < kAbB / 16; ++kk) {
+            const uint32_t add = kk != 0 ? 1u : 0u;
+            ab_mma_ts(one, tmem + kAsDv, tmem + kAsP + 8u * kk, od + 128u * kk, kIdescDkv, add);
+            ab_mma(one, tmem + kAsDk, dsk + 1024u * (kk >> 2) + 2u * (kk & 3), qd + 128u * kk, kIdescDkv, add);
+            ab_mma(one, tmem + kAsDq, dsm + 128u * kk, kd + 128u * kk, kIdescDq, add);
+        }
+        ab_commit(one, done);
+    }
+    wait(done);
+    tc_fence_after();
+    // Group 0 takes dk and half of dq, group 1 dv and the rest, through the tiles
+    // of K, V and Q.
+    uint32_t* v = &s[0][0];
+    tmem_ld32_async(tmem + lanes + (grp ? kAsDv : kAsDk), s[0]);
+    tmem_ld32_async(tmem + lanes + (grp ? kAsDv : kAsDk) + 32u, s[1]);
+    uint32_t q[32];
+    tmem_ld32_async(tmem + lanes + kAsDq + 32u * grp, q);
+    tmem_wait_ld(s[0]);
+    tmem_wait_ld(s[1]);
+    tmem_wait_ld(q);
+    ab_stage<8>(grp ? sV : sK, r, 0, v, grp ? 1.0f : a.scale);
+    ab_stage<4>(sQ, r, 4 * grp, q, a.scale);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kAsTmem);
+    }
+    // tokens past T lie outside the map and are not written
+    if (lane == 0 && 32 * quad < a.T) {
+        if (grp == 0) {
+            ab_store_3d(&tmDqkv, smem_u32(sK + quad * 4096), a.C + h * kAbD, 32 * quad, b);
+            ab_store_3d(&tmDqkv, smem_u32(sQ + quad * 4096), h * kAbD, 32 * quad, b);
+        } else {
+            ab_store_3d(&tmDqkv, smem_u32(sV + quad * 4096), 2 * a.C + h * kAbD, 32 * quad, b);
+        }
+        bulk_commit();
+        bulk_wait_read_all();
+    }
+}
+
+// The statistics of every query block, and its dq counters zeroed.
 __global__ void __launch_bounds__(256) attn_bwd_prep(const uint16_t* out, const uint16_t* dout, const float* lse, int T,
                                                      int H, int nb, int bh0, int chains, float* stats,
                                                      unsigned* flags) {
     pdl_wait();
     pdl_launch_dependents();
     const int local = blockIdx.x / nb, i = blockIdx.x % nb;
-    const int bh = bh0 + local, b = bh / H, h = bh % H;
-    const int row = threadIdx.x >> 1, half = threadIdx.x & 1;
-    const int t = i * kAbB + row;
-    float sum = 0.f;
-    if (t < T) {
-        const size_t off = ((size_t)b * T + t) * ((size_t)H * kAbD) + h * kAbD + 32 * half;
-        uint4 o[4], g[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            o[k] = *reinterpret_cast<const uint4*>(out + off + 8 * k);
-            g[k] = *reinterpret_cast<const uint4*>(dout + off + 8 * k);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t x[4] = {o[k].x, o[k].y, o[k].z, o[k].w}, y[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                sum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), sum);
-                sum = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), sum);
-            }
-        }
-    }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    float* st = stats + (size_t)blockIdx.x * (2 * kAbB);
-    if (half) {
-        st[kAbB + row] = -sum;
-    } else {
-        const float l = t < T ? lse[(size_t)bh * T + t] : -INFINITY;
-        st[row] = l == -INFINITY ? -INFINITY : -l * kAbLog2e;
-    }
-    if (flags)
-        for (int g = threadIdx.x; g < chains; g += 256) flags[((size_t)local * chains + g) * nb + i] = 0u;
+    const int bh = bh0 + local;
+    ab_stats(out, dout, lse, T, H, bh / H, bh % H, i, stats + (size_t)blockIdx.x * (2 * kAbB));
+    for (int g = threadIdx.x; g < chains; g += 256) flags[((size_t)local * chains + g) * nb + i] = 0u;
 }
 
 // dq of 128 queries of one head: the chains' fp32 sums added in order, scaled,
@@ -769,43 +990,20 @@ bool ab_map(CUtensorMap* map, const void* base, int B, int T, int cols, int rows
 int launch_attention_backward(const AttnBwdProblem& p) {
     const int C = p.H * kAbD;
     const int nb = (p.T + kAbB - 1) / kAbB;
-    const bool single = nb == 1;
     const long long bh_all = (long long)p.B * p.H;
-
-    // Workspace after the counter block: statistics, counters, dq sums. Heads go
-    // in as many launches as it takes.
-    const size_t avail = p.workspace_bytes > kCounterBytes + 1024 ? p.workspace_bytes - kCounterBytes - 1024 : 0;
-    const size_t stat = (size_t)nb * kAbStat;
-    const size_t chain = single ? 0 : (size_t)nb * (kAbDqTile + sizeof(unsigned));
-    if (stat + chain > avail) return LIN_ERR_WORKSPACE;
-    long long heads = bh_all;
-    if ((size_t)heads > avail / (stat + chain)) heads = (long long)(avail / (stat + chain));
-    // Chains: as many of a head's key blocks as run at the same time, so that
-    // none waits, where the workspace has room for their sums.
-    int chains = 1;
-    if (!single) {
-        const long long together = (p.sm_count + heads - 1) / heads;
-        const long long room = (long long)((avail / heads - stat) / chain);
-        chains = (int)std::max(1ll, std::min({together, room, (long long)nb}));
-    }
 
     CUtensorMap tq, tdo, tdq;
     if (!ab_map(&tq, p.qkv, p.B, p.T, 3 * C, kAbB) || !ab_map(&tdo, p.dout, p.B, p.T, C, kAbB) ||
         !ab_map(&tdq, p.dqkv, p.B, p.T, 3 * C, 32))
         return LIN_ERR_CUDA;
-    static std::atomic<unsigned long long> attr_set{0};
-    if (ensure_smem_attr(attr_set, attn_bwd_kernel, kAbSmem) != LIN_OK) return LIN_ERR_CUDA;
-
-    char* ws = static_cast<char*>(p.workspace) + kCounterBytes;
-    AbArgs a;
-    a.B = p.B;
+    const uint16_t* out = static_cast<const uint16_t*>(p.out);
+    const uint16_t* dout = static_cast<const uint16_t*>(p.dout);
+    AbArgs a = {};
     a.T = p.T;
     a.H = p.H;
     a.C = C;
     a.nb = nb;
-    a.chains = chains;
     a.causal = p.causal ? 1 : 0;
-    a.single = single ? 1 : 0;
     a.scale = p.scale;
     a.scale_log2 = p.scale * kAbLog2e;
     a.status = p.dev_status;
@@ -817,6 +1015,41 @@ int launch_attention_backward(const AttnBwdProblem& p) {
     cfg.stream = p.stream;
     cfg.attrs = &attr;
     cfg.numAttrs = p.early_start ? 1 : 0;
+
+    if (nb == 1) {
+        static std::atomic<unsigned long long> attr_set{0};
+        if (ensure_smem_attr(attr_set, attn_bwd_short_kernel, kAsSmem) != LIN_OK) return LIN_ERR_CUDA;
+        cfg.gridDim = dim3((unsigned)bh_all);
+        cfg.blockDim = dim3(kAsThreads);
+        cfg.dynamicSmemBytes = kAsSmem;
+        if (cudaLaunchKernelEx(&cfg, attn_bwd_short_kernel, tq, tdo, tdq, out, dout, p.lse, a) != cudaSuccess)
+            return LIN_ERR_CUDA;
+        return cudaGetLastError() == cudaSuccess ? LIN_OK : LIN_ERR_CUDA;
+    }
+
+    // Workspace after the counter block: statistics, counters, dq sums. Heads go
+    // in as many launches as it takes.
+    const size_t avail = p.workspace_bytes > kCounterBytes + 1024 ? p.workspace_bytes - kCounterBytes - 1024 : 0;
+    const size_t stat = (size_t)nb * kAbStat;
+    const size_t chain = (size_t)nb * (kAbDqTile + sizeof(unsigned));
+    if (stat + chain > avail) return LIN_ERR_WORKSPACE;
+    const long long heads = std::min(bh_all, (long long)(avail / (stat + chain)));
+    // Chains: as many of a head's key blocks as run at the same time, so that
+    // none waits, where the workspace has room for their sums.
+    const long long together = (p.sm_count + heads - 1) / heads;
+    const long long room = (long long)((avail / heads - stat) / chain);
+    a.chains = (int)std::max(1ll, std::min({together, room, (long long)nb}));
+
+    static std::atomic<unsigned long long> attr_set{0};
+    if (ensure_smem_attr(attr_set, attn_bwd_kernel, kAbSmem) != LIN_OK) return LIN_ERR_CUDA;
+    // The register split needs the kernel launched at kAbLaunchRegs a thread (else the
+    // increase would wait forever): refuse otherwise.
+    static const int regs = []() {
+        cudaFuncAttributes fa;
+        return cudaFuncGetAttributes(&fa, attn_bwd_kernel) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs < kAbLaunchRegs) return LIN_ERR_UNSUPPORTED;
+    char* ws = static_cast<char*>(p.workspace) + kCounterBytes;
     for (long long bh0 = 0; bh0 < bh_all; bh0 += heads) {
         const int count = (int)std::min(heads, bh_all - bh0);
         a.bh0 = (int)bh0;
@@ -824,30 +1057,25 @@ int launch_attention_backward(const AttnBwdProblem& p) {
         a.items = count * nb;
         float* stats = reinterpret_cast<float*>(ws);
         char* rest = ws + align_up((size_t)count * stat, 256);
-        unsigned* flags = reinterpret_cast<unsigned*>(rest);
-        float* dq = reinterpret_cast<float*>(rest + align_up((size_t)count * chains * nb * sizeof(unsigned), 256));
         a.stats = stats;
-        a.flags = single ? nullptr : flags;
-        a.dq = single ? nullptr : dq;
+        a.flags = reinterpret_cast<unsigned*>(rest);
+        a.dq = reinterpret_cast<float*>(rest + align_up((size_t)count * a.chains * nb * sizeof(unsigned), 256));
         cfg.gridDim = dim3((unsigned)a.items);
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;
-        if (cudaLaunchKernelEx(&cfg, attn_bwd_prep, static_cast<const uint16_t*>(p.out),
-                               static_cast<const uint16_t*>(p.dout), p.lse, p.T, p.H, nb, a.bh0, chains, stats,
-                               a.flags) != cudaSuccess)
+        if (cudaLaunchKernelEx(&cfg, attn_bwd_prep, out, dout, p.lse, p.T, p.H, nb, a.bh0, a.chains, stats, a.flags) !=
+            cudaSuccess)
             return LIN_ERR_CUDA;
         cfg.gridDim = dim3((unsigned)std::min(a.items, p.sm_count));
         cfg.blockDim = dim3(kAbThreads);
         cfg.dynamicSmemBytes = kAbSmem;
         if (cudaLaunchKernelEx(&cfg, attn_bwd_kernel, tq, tdo, tdq, a) != cudaSuccess) return LIN_ERR_CUDA;
-        if (!single) {
-            cfg.gridDim = dim3((unsigned)a.items);
-            cfg.blockDim = dim3(512);
-            cfg.dynamicSmemBytes = 0;
-            if (cudaLaunchKernelEx(&cfg, attn_bwd_dq, static_cast<const float*>(dq), static_cast<uint16_t*>(p.dqkv),
-                                   p.T, p.H, nb, a.bh0, chains, a.causal, a.scale) != cudaSuccess)
-                return LIN_ERR_CUDA;
-        }
+        cfg.gridDim = dim3((unsigned)a.items);
+        cfg.blockDim = dim3(512);
+        cfg.dynamicSmemBytes = 0;
+        if (cudaLaunchKernelEx(&cfg, attn_bwd_dq, static_cast<const float*>(a.dq), static_cast<uint16_t*>(p.dqkv), p.T,
+                               p.H, nb, a.bh0, a.chains, a.causal, a.scale) != cudaSuccess)
+            return LIN_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? LIN_OK : LIN_ERR_CUDA;
 }
