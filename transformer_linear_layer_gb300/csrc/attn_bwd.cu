@@ -32,14 +32,12 @@
 //                    over the key blocks in fp32 in the workspace.
 //   attn_bwd_dq      the fp32 sums to bf16.
 //
-// attn_bwd_kernel's warps: 0 TMA; 1 tcgen05.mma issuer; 4-11 two groups that
-// turn S' and dP' into P' and dS' (a thread has one key and 64 of the block's
-// queries); 12-15 dQ out of TMEM, and dK and dV at an item's end. S'(n+1) and
-// dP'(n+1) are issued while step n is turned into P' and dS', so the exponentials
-// overlap the products. A chain of products into one accumulator runs at about
-// half the rate of two chains in turn, so dV(n) is issued in turn with dP'(n+1),
-// and dK(n) with dQ(n); a commit costs the issuer about 350 cycles, so a step has
-// three, and what else waits for them is told by the warps that saw them.
+// attn_bwd_kernel's warps: 0 TMA; 1 tcgen05.mma issuer; 2 and 3 send what is staged
+// for memory; 4-19 four groups that turn S' and dP' into P' and dS' (a thread has one
+// key and 32 of the block's queries); 20-23 dQ out of TMEM, and dK and dV at an
+// item's end. S'(n+1) and dP'(n+1) are issued while step n is turned into P' and
+// dS', so the exponentials overlap the products. A step has three commits (S', dV with the next dP', dK with
+// dQ); what else waits for products is told by the warps that saw them.
 //
 // Order of the dq sums: the key blocks of a head form `chains` chains (block j in
 // chain j % chains), each with its own fp32 copy of dq; within a chain block j
@@ -62,7 +60,8 @@ namespace {
 
 constexpr int kAbB = 128;                          // keys, and queries, of a block
 constexpr int kAbD = 64;                           // head width
-constexpr int kAbThreads = 512;
+constexpr int kAbGroups = 4;                       // groups of four warps that make P' and dS', 32 queries each
+constexpr int kAbThreads = 128 * (kAbGroups + 2);
 constexpr uint32_t kAbTile = kAbB * kAbD * 2;      // 16 KiB: 128 rows of 128 bytes, 128-byte swizzle
 constexpr uint32_t kAbStat = 2 * kAbB * 4;         // -lse log2(e) and -delta of 128 queries
 constexpr int kAbKStages = 2, kAbQStages = 3;      // (V has one)
@@ -80,10 +79,10 @@ constexpr int kAsThreads = 256;
 constexpr uint32_t kAsP = 0, kAsDq = 64, kAsDp = 128, kAsDv = 128, kAsDk = 192, kAsTmem = 256;
 constexpr size_t kAsSmem = 1024 + 4 * kAbTile + kAbDs + kAbStat + 6 * 8 + 16;
 static_assert(2 * (kAsSmem + 1024) <= 228 * 1024, "two blocks an SM");
-// Register split (setmaxnreg, per warpgroup): launched at 128 a thread; TMA and MMA
-// give theirs to the groups that hold 64 probabilities and 64 dp a thread.
-constexpr int kAbLaunchRegs = 128, kAbRegsIssue = 64, kAbRegsSoftmax = 168, kAbRegsOut = 112;
-static_assert(kAbRegsIssue + 2 * kAbRegsSoftmax + kAbRegsOut <= 4 * kAbLaunchRegs, "register split");
+// Register split (setmaxnreg, per warpgroup): launched at 80 a thread; the groups that
+// hold 32 probabilities and 32 dp a thread take what the others give back.
+constexpr int kAbLaunchRegs = 80, kAbRegsIssue = 64, kAbRegsSoftmax = 88, kAbRegsOut = 64;
+static_assert(kAbRegsIssue + kAbGroups * kAbRegsSoftmax + kAbRegsOut <= (kAbGroups + 2) * kAbLaunchRegs, "register split");
 constexpr float kAbLog2e = 1.4426950408889634f;
 
 struct AbArgs {
@@ -148,29 +147,23 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-// Products and commits are issued by a whole warp with one lane's predicate:
-// descriptors then stay in uniform registers.
-__device__ __forceinline__ void ab_mma(uint32_t one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// True in one lane. The issuing warp runs its loop whole and issues inside such a
+// branch, which the compiler knows to be one thread's: descriptors stay in uniform
+// registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
-        : "memory");
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
 }
 // D (+)= A B with A (bf16, two to a 32-bit column) in TMEM.
-__device__ __forceinline__ void ab_mma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                          uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
-        : "memory");
-}
-__device__ __forceinline__ void ab_commit(uint32_t one, uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 constexpr uint32_t kIdescS = make_idesc(1u, kAbB, kAbB);                  // both K-major
@@ -220,77 +213,68 @@ __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// ---- one thread's key and 64 of the block's queries ----
+// ---- one thread's key and 32 of the block's queries ----
 
 // p = 2^(s scale log2(e) - lse log2(e)); nl = -lse log2(e) of the queries.
-__device__ __forceinline__ void ab_probs(const uint32_t (&s)[2][32], const float* nl, uint64_t sl2,
-                                         uint64_t (&p)[2][16]) {
-#pragma unroll
-    for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-            const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(nl + 32 * ch + c);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float x0, x1;
-                ab_unpack(ab_fma2(ab_pack(__uint_as_float(s[ch][c + 2 * k]), __uint_as_float(s[ch][c + 2 * k + 1])), sl2,
-                                  k ? l.y : l.x),
-                          x0, x1);
-                p[ch][c / 2 + k] = ab_pack(ab_ex2(x0), ab_ex2(x1));
-            }
-        }
-}
-// Only queries from `from` on see the key.
-__device__ __forceinline__ void ab_hide(uint64_t (&p)[2][16], int from) {
-#pragma unroll
-    for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            float x0, x1;
-            ab_unpack(p[ch][c], x0, x1);
-            p[ch][c] = ab_pack(32 * ch + 2 * c >= from ? x0 : 0.f, 32 * ch + 2 * c + 1 >= from ? x1 : 0.f);
-        }
-}
-// P' in bf16 to 32 columns of TMEM.
-__device__ __forceinline__ void ab_put_p(uint32_t taddr, const uint64_t (&p)[2][16]) {
-#pragma unroll
-    for (int ch = 0; ch < 2; ++ch) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            float x0, x1;
-            ab_unpack(p[ch][c], x0, x1);
-            pk[c] = pack_bf16x2(x0, x1);
-        }
-        tmem_st16(taddr + 16u * ch, pk);
-    }
-    ab_tmem_wait_st();
-}
-// ds = p (dp - delta) of 32 queries in bf16 to the thread's row of dS'; nd = -delta.
-// MASKED: a hidden pair takes nothing from dp or delta, whatever they are.
-template <bool MASKED>
-__device__ __forceinline__ void ab_put_ds(int ch, const uint32_t (&dp)[32], const uint64_t (&p)[16], const float* nd,
-                                          uint8_t* ds_row, int r, int from) {
-    uint32_t pk[16];
+__device__ __forceinline__ void ab_probs(const uint32_t (&s)[32], const float* nl, uint64_t sl2, uint64_t (&p)[16]) {
 #pragma unroll
     for (int c = 0; c < 32; c += 4) {
-        const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(nd + c);
+        const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(nl + c);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const uint64_t x = ab_pack(__uint_as_float(dp[c + 2 * k]), __uint_as_float(dp[c + 2 * k + 1]));
             float x0, x1;
-            ab_unpack(ab_mul2(p[c / 2 + k], ab_add2(x, k ? d.y : d.x)), x0, x1);
-            if constexpr (MASKED) {
-                x0 = 32 * ch + c + 2 * k >= from ? x0 : 0.f;
-                x1 = 32 * ch + c + 2 * k + 1 >= from ? x1 : 0.f;
-            }
-            pk[c / 2 + k] = pack_bf16x2(x0, x1);
+            ab_unpack(ab_fma2(ab_pack(__uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1])), sl2, k ? l.y : l.x),
+                      x0, x1);
+            p[c / 2 + k] = ab_pack(ab_ex2(x0), ab_ex2(x1));
         }
     }
+}
+// Only queries from `from` on see the key.
+__device__ __forceinline__ void ab_hide(uint64_t (&p)[16], int from) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-        *reinterpret_cast<uint4*>(ds_row + (((4 * ch + v) ^ (r & 7)) << 4)) =
-            make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+    for (int c = 0; c < 16; ++c) {
+        float x0, x1;
+        ab_unpack(p[c], x0, x1);
+        p[c] = ab_pack(2 * c >= from ? x0 : 0.f, 2 * c + 1 >= from ? x1 : 0.f);
+    }
+}
+// P' in bf16 to 16 columns of TMEM.
+__device__ __forceinline__ void ab_put_p(uint32_t taddr, const uint64_t (&p)[16]) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        float x0, x1;
+        ab_unpack(p[c], x0, x1);
+        pk[c] = pack_bf16x2(x0, x1);
+    }
+    tmem_st16(taddr, pk);
+}
+// ds = p (dp - delta) in bf16 to pieces `first`.. of the thread's row of dS'; nd =
+// -delta. MASKED: a hidden pair takes nothing from dp or delta, whatever they are.
+template <bool MASKED>
+__device__ __forceinline__ void ab_put_ds(const uint32_t (&dp)[32], const uint64_t (&p)[16], const float* nd,
+                                          uint8_t* ds_row, int r, int first, int from) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        uint32_t pk[4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int c = 8 * v + 4 * u;
+            const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(nd + c);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint64_t x = ab_pack(__uint_as_float(dp[c + 2 * k]), __uint_as_float(dp[c + 2 * k + 1]));
+                float x0, x1;
+                ab_unpack(ab_mul2(p[c / 2 + k], ab_add2(x, k ? d.y : d.x)), x0, x1);
+                if constexpr (MASKED) {
+                    x0 = c + 2 * k >= from ? x0 : 0.f;
+                    x1 = c + 2 * k + 1 >= from ? x1 : 0.f;
+                }
+                pk[2 * u + k] = pack_bf16x2(x0, x1);
+            }
+        }
+        *reinterpret_cast<uint4*>(ds_row + (((first + v) ^ (r & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    }
 }
 // 8 * N fp32 values, scaled, in bf16 to pieces `first`.. of row r of a 128-byte-swizzled tile.
 template <int N>
@@ -390,13 +374,14 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
     int* s_abort = reinterpret_cast<int*>(tmem_slot + 1);
 
     // Full / empty of the stages; then, once a step: sfull, dpfull, done (the
-    // products of S', of dV and dP', of dK and dQ), sread, pready, dpread, dsready
-    // (the eight warps), dqfree, accfree, met (the four).
+    // products of S', of dV and dP', of dK and dQ), pready, dsready (the groups'
+    // warps), dqfree, accfree (the four); outfull (the four; of even and of odd
+    // messages), outfree (a sender) once a message.
     const uint32_t kfull = smem_u32(bars), kempty = kfull + 8 * KS, vfull = kempty + 8 * KS, vempty = vfull + 8,
                    qfull = vempty + 8, qempty = qfull + 8 * QS, one_a_step = qempty + 8 * QS;
-    const uint32_t sfull = one_a_step, dpfull = one_a_step + 8, done = one_a_step + 16, sread = one_a_step + 24,
-                   pready = one_a_step + 32, dpread = one_a_step + 40, dsready = one_a_step + 48,
-                   dqfree = one_a_step + 56, accfree = one_a_step + 64, met = one_a_step + 72;
+    const uint32_t sfull = one_a_step, dpfull = one_a_step + 8, done = one_a_step + 16, pready = one_a_step + 24,
+                   dsready = one_a_step + 32, dqfree = one_a_step + 40, accfree = one_a_step + 48,
+                   outfull = one_a_step + 56, outfree = one_a_step + 72;
 
     // (the same in every lane, and known to be: roles branch without divergence)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -406,7 +391,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
             mbar_init(kempty + 8 * s, 4);
         }
         mbar_init(vfull, 1);
-        mbar_init(vempty, 8);
+        mbar_init(vempty, 4 * kAbGroups);
         for (int s = 0; s < QS; ++s) {
             mbar_init(qfull + 8 * s, 1);
             mbar_init(qempty + 8 * s, 4);
@@ -414,13 +399,13 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         mbar_init(sfull, 1);
         mbar_init(dpfull, 1);
         mbar_init(done, 1);
-        mbar_init(sread, 8);
-        mbar_init(pready, 8);
-        mbar_init(dpread, 8);
-        mbar_init(dsready, 8);
+        mbar_init(pready, 4 * kAbGroups);
+        mbar_init(dsready, 4 * kAbGroups);
         mbar_init(dqfree, 4);
         mbar_init(accfree, 4);
-        mbar_init(met, 4);
+        mbar_init(outfull, 4);
+        mbar_init(outfull + 8, 4);
+        mbar_init(outfree, 1);
         *s_abort = 0;
         mbar_fence_init();
         tma_prefetch_map(&tmQkv);
@@ -438,10 +423,9 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         atomicExch(s_abort, 1);
         atomicExch(a.status, (int)LIN_ERR_DEVICE_TIMEOUT);
     };
-    // A warp's wait: false when it, or another warp's, has run out.
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, *(volatile int*)s_abort == 0 && mbar_wait(bar, parity)) != 0;
-    };
+    // A warp's wait: false when it has run out.
+    auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
+    auto aborted = [&]() { return __any_sync(0xffffffffu, *(volatile int*)s_abort != 0) != 0; };
     auto arrive = [&](uint32_t bar) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
@@ -457,7 +441,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         for (w.init(a); ok && w.valid; w.next_item(a), ++m) {
             const int bh = a.bh0 + w.bh, b = bh / a.H, h = bh % a.H;
             const uint32_t ks = m % KS;
-            if (!wait(kempty + 8 * ks, ((m / KS) & 1) ^ 1)) {
+            if (aborted() || !wait(kempty + 8 * ks, ((m / KS) & 1) ^ 1)) {
                 ok = false;
                 break;
             }
@@ -467,7 +451,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
             }
             for (int i = w.i0; i < a.nb; ++i, ++n) {
                 const uint32_t qs = n % QS;
-                if (!wait(qempty + 8 * qs, ((n / QS) & 1) ^ 1)) {
+                if (aborted() || !wait(qempty + 8 * qs, ((n / QS) & 1) ^ 1)) {
                     ok = false;
                     break;
                 }
@@ -508,248 +492,253 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         }
     } else if (warp == 1) {
         // ---- tcgen05.mma ----
-        const uint32_t one = lane == 0;
-        AbWalker cur, lead;
-        cur.init(a);
-        lead.init(a);
-        uint32_t n = 0;
-        bool ok = true;
-        auto issue_s = [&](uint32_t k) {  // S' of step k, the lead's
-            if ((lead.first() && !wait(kfull + 8 * (lead.m % KS), (lead.m / KS) & 1)) ||
-                !wait(qfull + 8 * (k % QS), (k / QS) & 1) || (k > 0 && !wait(sread, (k - 1) & 1)))
-                return false;
-            tc_fence_after();
-            const uint64_t kd = sw128_kmajor_desc(smem_u32(sK + (lead.m % KS) * kAbTile));
-            const uint64_t qd = sw128_kmajor_desc(smem_u32(sQ + (k % QS) * kAbQStage));
+        if (elect_one()) {
+            AbWalker cur, lead;
+            cur.init(a);
+            lead.init(a);
+            uint32_t n = 0;
+            bool ok = true;
+            auto issue_s = [&](uint32_t k) {  // S' of step k, the lead's
+                const uint64_t kd = sw128_kmajor_desc(smem_u32(sK + (lead.m % KS) * kAbTile));
+                const uint64_t qd = sw128_kmajor_desc(smem_u32(sQ + (k % QS) * kAbQStage));
 #pragma unroll
-            for (int kk = 0; kk < kAbD / 16; ++kk)
-                ab_mma(one, tmem + kAbS, kd + 2u * kk, qd + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
-            ab_commit(one, sfull);
-            return true;
-        };
-        // dV of step k - 1 (`with_dv`) in turn with dP' of step k (`with_dp`, the lead's)
-        auto issue_dv_dp = [&](uint32_t k, bool with_dv, bool dv_first, bool with_dp) {
-            if ((with_dp && lead.first() && !wait(vfull, lead.m & 1)) || (k > 0 && !wait(dpread, (k - 1) & 1)))
-                return false;
-            tc_fence_after();
-            const uint64_t dod = sw128_mnmajor_desc(smem_u32(sQ + ((k + QS - 1) % QS) * kAbQStage + kAbTile));
-            const uint64_t vd = sw128_kmajor_desc(smem_u32(sV));
-            const uint64_t od = sw128_kmajor_desc(smem_u32(sQ + (k % QS) * kAbQStage + kAbTile));
+                for (int kk = 0; kk < kAbD / 16; ++kk)
+                    tc_mma<true>(tmem + kAbS, kd + 2u * kk, qd + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
+                tc_commit(sfull);
+            };
+            auto issue_dp = [&](uint32_t k) {  // dP' of step k, the lead's
+                const uint64_t vd = sw128_kmajor_desc(smem_u32(sV));
+                const uint64_t od = sw128_kmajor_desc(smem_u32(sQ + (k % QS) * kAbQStage + kAbTile));
 #pragma unroll
-            for (int kk = 0; kk < kAbB / 16; ++kk) {
-                if (with_dv)
-                    ab_mma_ts(one, tmem + kAbDv, tmem + kAbP + 8u * kk, dod + 128u * kk, kIdescDkv,
-                              (kk != 0 || !dv_first) ? 1u : 0u);
-                if (with_dp && (kk & 1) == 0)
-                    ab_mma(one, tmem + kAbDp, vd + 1u * kk, od + 1u * kk, kIdescS, kk != 0 ? 1u : 0u);
+                for (int kk = 0; kk < kAbD / 16; ++kk)
+                    tc_mma<true>(tmem + kAbDp, vd + 2u * kk, od + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
+                tc_commit(dpfull);
+            };
+            // the operands of step k have landed
+            auto loaded = [&](uint32_t k) {
+                return mbar_wait(qfull + 8 * (k % QS), (k / QS) & 1) &&
+                       (!lead.first() || mbar_wait(kfull + 8 * (lead.m % KS), (lead.m / KS) & 1));
+            };
+            if (cur.valid) {
+                ok = loaded(0) && mbar_wait(vfull, 0);
+                if (ok) {
+                    issue_s(0);
+                    issue_dp(0);
+                    lead.next(a);
+                }
             }
-            ab_commit(one, dpfull);
-            return true;
-        };
-        if (cur.valid) {
-            ok = issue_s(0) && issue_dv_dp(0, false, false, true);
-            lead.next(a);
-        }
-        while (ok && cur.valid) {
-            const bool first = cur.first();
-            if (lead.valid && !issue_s(n + 1)) ok = false;
-            if (!ok || !wait(pready, n & 1) || (first && cur.m > 0 && !wait(accfree, (cur.m - 1) & 1)) ||
-                !issue_dv_dp(n + 1, true, first, lead.valid)) {
-                ok = false;
-                break;
-            }
-            if (lead.valid) lead.next(a);
-            // dK += dS' Q in turn with dQ = dS K
-            if (!wait(dsready, n & 1) || (n > 0 && !wait(dqfree, (n - 1) & 1))) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const uint64_t dsk = sw128_kmajor_desc(smem_u32(sDS)), dsm = ab_ds_mn_desc(smem_u32(sDS));
-            const uint64_t qd = sw128_mnmajor_desc(smem_u32(sQ + (n % QS) * kAbQStage));
-            const uint64_t kd = sw128_mnmajor_desc(smem_u32(sK + (cur.m % KS) * kAbTile));
+            while (ok && cur.valid) {
+                const bool first = cur.first();
+                // P' of step n is written, S' and dP' are read: S' of the next step,
+                // dV += P' dO, dP' of the next step (whose commit covers dV too)
+                if (*(volatile int*)s_abort != 0 || !mbar_wait(pready, n & 1) || (lead.valid && !loaded(n + 1)) ||
+                    (first && cur.m > 0 && !mbar_wait(accfree, (cur.m - 1) & 1))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (lead.valid) issue_s(n + 1);
+                const uint32_t q = smem_u32(sQ + (n % QS) * kAbQStage);
+                const uint64_t dod = sw128_mnmajor_desc(q + kAbTile);
 #pragma unroll
-            for (int kk = 0; kk < kAbB / 16; ++kk) {
-                ab_mma(one, tmem + kAbDk, dsk + 1024u * (kk >> 2) + 2u * (kk & 3), qd + 128u * kk, kIdescDkv,
-                       (kk != 0 || !first) ? 1u : 0u);
-                ab_mma(one, tmem + kAbDq, dsm + 128u * kk, kd + 128u * kk, kIdescDq, kk != 0 ? 1u : 0u);
+                for (int kk = 0; kk < kAbB / 16; ++kk)
+                    tc_mma_ts(tmem + kAbDv, tmem + kAbP + 8u * kk, dod + 128u * kk, kIdescDkv,
+                              (kk != 0 || !first) ? 1u : 0u);
+                if (lead.valid) {
+                    if (lead.first() && !mbar_wait(vfull, lead.m & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    issue_dp(n + 1);
+                    lead.next(a);
+                }
+                // dS' of step n is written: dK += dS' Q, dQ = dS K
+                if (!mbar_wait(dsready, n & 1) || (n > 0 && !mbar_wait(dqfree, (n - 1) & 1))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t dsk = sw128_kmajor_desc(smem_u32(sDS)), dsm = ab_ds_mn_desc(smem_u32(sDS));
+                const uint64_t qd = sw128_mnmajor_desc(q);
+                const uint64_t kd = sw128_mnmajor_desc(smem_u32(sK + (cur.m % KS) * kAbTile));
+#pragma unroll
+                for (int kk = 0; kk < kAbB / 16; ++kk)
+                    tc_mma<true>(tmem + kAbDk, dsk + 1024u * (kk >> 2) + 2u * (kk & 3), qd + 128u * kk, kIdescDkv,
+                                 (kk != 0 || !first) ? 1u : 0u);
+#pragma unroll
+                for (int kk = 0; kk < kAbB / 16; ++kk)
+                    tc_mma<true>(tmem + kAbDq, dsm + 128u * kk, kd + 128u * kk, kIdescDq, kk != 0 ? 1u : 0u);
+                tc_commit(done);
+                cur.next(a);
+                ++n;
             }
-            ab_commit(one, done);
-            cur.next(a);
-            ++n;
+            if (!ok) {
+                give_up();
+                // the products issued so far end before the block does
+                tc_commit(done);
+                mbar_wait(done, n & 1);
+            }
         }
-        if (!ok) {
-            if (lane == 0) give_up();
-            __syncwarp();
-            // the products issued so far end before the block does
-            ab_commit(one, done);
-            mbar_wait(done, n & 1);
+        __syncwarp();
+    } else if (warp == 2 || warp == 3) {
+        // ---- two senders, in turn: what the last group has staged in sOut. One waits
+        // for its tile's addition to complete, and tells the chain, while the other
+        // sends the next. ----
+        pdl_wait();
+        if (elect_one()) {
+            uint32_t msg = 0;
+            bool ok = true;
+            AbWalker w;
+            for (w.init(a); ok && w.valid; w.next(a)) {
+                const int bh = a.bh0 + w.bh, b = bh / a.H, h = bh % a.H;
+                if ((msg++ & 1) == (uint32_t)(warp & 1)) {
+                    if (*(volatile int*)s_abort != 0 || !mbar_wait(outfull + 8 * ((msg - 1) & 1), ((msg - 1) >> 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const int chain = w.j % a.chains, pos = w.j / a.chains;
+                    const size_t slot = ((size_t)w.bh * a.chains + chain) * a.nb + w.i;
+                    float* tile = a.dq + slot * (kAbDqTile / 4);
+                    if (pos == 0) {
+                        bulk_store(tile, smem_u32(sOut), kAbDqTile);
+                    } else {
+                        // until the chain's earlier block has added to this tile
+                        bool there = ld_acquire_gpu(a.flags + slot) == (unsigned)pos;
+                        const unsigned long long t0 = global_ns();
+                        for (uint32_t k = 1; !there && k < kWaitIters; ++k) {
+                            there = ld_acquire_gpu(a.flags + slot) == (unsigned)pos;
+                            if ((k & 63u) == 63u && (*(volatile int*)s_abort != 0 || global_ns() - t0 > kWaitNs)) break;
+                        }
+                        if (!there) {
+                            ok = false;
+                            break;
+                        }
+                        fence_proxy_async_global();
+                        bulk_add_f32(tile, smem_u32(sOut), kAbDqTile);
+                    }
+                    bulk_commit();
+                    bulk_wait_read_all();
+                    mbar_arrive(outfree);
+                    if (w.j + a.chains <= (a.causal ? w.i : a.nb - 1)) {
+                        bulk_wait_all();
+                        fence_proxy_async_global();
+                        st_release_gpu(a.flags + slot, (unsigned)pos + 1u);
+                    }
+                }
+                if (w.last(a) && (msg++ & 1) == (uint32_t)(warp & 1)) {
+                    // dk and dv; tokens past T lie outside the map and are not written
+                    ok = mbar_wait(outfull + 8 * ((msg - 1) & 1), ((msg - 1) >> 1) & 1);
+                    if (!ok) break;
+                    for (int y = 0; y < kAbB; y += 32) {
+                        ab_store_3d(&tmDqkv, smem_u32(sOut + y * 128), a.C + h * kAbD, w.j * kAbB + y, b);
+                        ab_store_3d(&tmDqkv, smem_u32(sOut + kAbTile + y * 128), 2 * a.C + h * kAbD, w.j * kAbB + y, b);
+                    }
+                    bulk_commit();
+                    bulk_wait_read_all();
+                    mbar_arrive(outfree);
+                }
+            }
+            if (!ok) give_up();
+            bulk_wait_all();
         }
-    } else if (warp >= 4 && warp < 12) {
+        __syncwarp();
+    } else if (warp >= 4 && warp < 4 + 4 * kAbGroups) {
         // ---- P' and dS' ----
         regs_inc<kAbRegsSoftmax>();
         const int grp = (warp - 4) >> 2, quad = warp & 3;
         const int r = 32 * quad + lane;  // key within the block, TMEM lane
         const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-        const uint32_t tS = tmem + lanes + kAbS + 64u * grp, tDp = tmem + lanes + kAbDp + 64u * grp,
-                       tP = tmem + lanes + kAbP + 32u * grp;
-        uint8_t* ds_row = sDS + grp * (kAbDs / 2) + r * 128;
+        const uint32_t tS = tmem + lanes + kAbS + 32u * grp, tDp = tmem + lanes + kAbDp + 32u * grp,
+                       tP = tmem + lanes + kAbP + 16u * grp;
+        uint8_t* ds_row = sDS + (grp >> 1) * (kAbDs / 2) + r * 128;
         const uint64_t sl2 = ab_pack(a.scale_log2, a.scale_log2);
         uint32_t n = 0;
         bool ok = true;
         AbWalker w;
         for (w.init(a); w.valid; w.next(a), ++n) {
-            const float* stat = reinterpret_cast<const float*>(sQ + (n % QS) * kAbQStage + 2 * kAbTile) + 64 * grp;
+            const float* stat = reinterpret_cast<const float*>(sQ + (n % QS) * kAbQStage + 2 * kAbTile) + 32 * grp;
             const bool diag = a.causal && w.i == w.j;
             const bool masked = diag || (w.j + 1) * kAbB > a.T;
             // query c of this group is visible to the thread's key from `from` on
-            const int from = w.j * kAbB + r >= a.T ? 64 : diag ? r - 64 * grp : 0;
-            ok = wait(qfull + 8 * (n % QS), (n / QS) & 1) && wait(sfull, n & 1);
+            const int from = w.j * kAbB + r >= a.T ? 32 : diag ? r - 32 * grp : 0;
+            ok = !aborted() && wait(qfull + 8 * (n % QS), (n / QS) & 1) && wait(sfull, n & 1);
             if (!ok) break;
             tc_fence_after();
-            uint32_t s[2][32];
-            tmem_ld32_async(tS, s[0]);
-            tmem_ld32_async(tS + 32u, s[1]);
-            tmem_wait_ld(s[0]);
-            tmem_wait_ld(s[1]);
-            tc_fence_before();
-            arrive(sread);
-            uint64_t p[2][16];
+            uint32_t s[32];
+            tmem_ld32_async(tS, s);
+            tmem_wait_ld(s);
+            uint64_t p[16];
             ab_probs(s, stat, sl2, p);
             if (masked) ab_hide(p, from);
             // dP' of this step, and so dV of the step before: P' may be rewritten
             ok = wait(dpfull, n & 1);
             if (!ok) break;
             tc_fence_after();
-            tmem_ld32_async(tDp, s[0]);
-            tmem_ld32_async(tDp + 32u, s[1]);
+            tmem_ld32_async(tDp, s);
             ab_put_p(tP, p);
+            ab_tmem_wait_st();
+            tmem_wait_ld(s);
             tc_fence_before();
             arrive(pready);
-            tmem_wait_ld(s[0]);
-            tmem_wait_ld(s[1]);
-            tc_fence_before();
-            arrive(dpread);
             if (w.last(a)) arrive(vempty);
             // dK and dQ of the step before: dS' may be rewritten
             ok = n == 0 || wait(done, (n - 1) & 1);
             if (!ok) break;
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-                if (masked) ab_put_ds<true>(ch, s[ch], p[ch], stat + kAbB + 32 * ch, ds_row, r, from);
-                else ab_put_ds<false>(ch, s[ch], p[ch], stat + kAbB + 32 * ch, ds_row, r, from);
-            }
+            if (masked) ab_put_ds<true>(s, p, stat + kAbB, ds_row, r, 4 * (grp & 1), from);
+            else ab_put_ds<false>(s, p, stat + kAbB, ds_row, r, 4 * (grp & 1), from);
             fence_proxy_async_smem();
             tc_fence_before();
             arrive(dsready);
         }
         if (!ok && lane == 0) give_up();
-    } else if (warp >= 12) {
-        // ---- dq, dk and dv out ----
+    } else if (warp >= 4 + 4 * kAbGroups) {
+        // ---- dq, dk and dv out of TMEM ----
         regs_dec<kAbRegsOut>();
-        pdl_wait();
         const int quad = warp & 3;
         const int r = 32 * quad + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-        const bool sender = threadIdx.x == 12 * 32;
-        auto read64 = [&](uint32_t col, uint32_t (&v)[2][32]) {
-            tmem_ld32_async(tmem + lanes + col, v[0]);
-            tmem_ld32_async(tmem + lanes + col + 32u, v[1]);
-            tmem_wait_ld(v[0]);
-            tmem_wait_ld(v[1]);
-        };
-        uint32_t n = 0, meets = 0;
+        uint32_t n = 0, msg = 0;
         bool ok = true;
-        auto meet = [&]() {  // the four warps
-            arrive(met);
-            return wait(met, meets++ & 1);
-        };
-        // A chain's tile that the sender has under way: its counter is raised once
-        // the addition has completed (a step later).
-        unsigned* pending = nullptr;
-        unsigned pending_value = 0;
-        auto settle = [&]() {
-            if (!pending) return;
-            bulk_wait_all();
-            fence_proxy_async_global();
-            __threadfence();
-            st_release_gpu(pending, pending_value);
-            pending = nullptr;
-        };
         AbWalker w;
         for (w.init(a); w.valid; w.next(a), ++n) {
-            const int bh = a.bh0 + w.bh, b = bh / a.H, h = bh % a.H;
             const bool last = w.last(a);
-            ok = wait(done, n & 1);
+            ok = !aborted() && wait(done, n & 1) && (msg == 0 || wait(outfree, (msg - 1) & 1));
             if (!ok) break;
             tc_fence_after();
             arrive(qempty + 8 * (n % QS));
             if (last) arrive(kempty + 8 * (w.m % KS));
-            uint32_t v[2][32];
-            read64(kAbDq, v);
+            uint32_t v[32];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                tmem_ld32_async(tmem + lanes + kAbDq + 32u * half, v);
+                tmem_wait_ld(v);
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(sOut + (8 * half + c) * (kAbB * 16) + r * 16) =
+                        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            }
             tc_fence_before();
             arrive(dqfree);
-            if (lane == 0) bulk_wait_read_all();  // what this warp sent has been read out
-            ok = meet();
-            if (!ok) break;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint32_t* x = &v[c >> 3][4 * (c & 7)];
-                *reinterpret_cast<uint4*>(sOut + c * (kAbB * 16) + r * 16) = make_uint4(x[0], x[1], x[2], x[3]);
-            }
             fence_proxy_async_smem();
-            ok = meet();
-            if (!ok) break;
-            if (sender) {
-                settle();
-                const int chain = w.j % a.chains, pos = w.j / a.chains;
-                const size_t slot = ((size_t)w.bh * a.chains + chain) * a.nb + w.i;
-                float* tile = a.dq + slot * (kAbDqTile / 4);
-                if (pos == 0) {
-                    bulk_store(tile, smem_u32(sOut), kAbDqTile);
-                } else {
-                    // until the chain's earlier block has added to this tile
-                    const unsigned long long t0 = global_ns();
-                    bool there = ld_acquire_gpu(a.flags + slot) == (unsigned)pos;
-                    for (uint32_t k = 1; !there && k < kWaitIters; ++k) {
-                        there = ld_acquire_gpu(a.flags + slot) == (unsigned)pos;
-                        if ((k & 63u) == 63u && (*(volatile int*)s_abort != 0 || global_ns() - t0 > kWaitNs)) break;
-                    }
-                    fence_proxy_async_global();
-                    if (there) bulk_add_f32(tile, smem_u32(sOut), kAbDqTile);
-                    else give_up();
-                }
-                bulk_commit();
-                if (w.j + a.chains <= (a.causal ? w.i : a.nb - 1)) {
-                    pending = a.flags + slot;
-                    pending_value = (unsigned)pos + 1u;
-                }
-            }
-            __syncwarp();
+            arrive(outfull + 8 * (msg & 1));
+            ++msg;
             if (last) {
-                read64(kAbDk, v);
-                if (lane == 0) bulk_wait_read_all();
-                ok = meet();
+                ok = wait(outfree, (msg - 1) & 1);
                 if (!ok) break;
-                ab_stage<8>(sOut, r, 0, &v[0][0], a.scale);
-                read64(kAbDv, v);
+#pragma unroll
+                for (int part = 0; part < 4; ++part) {  // dk, then dv
+                    tmem_ld32_async(tmem + lanes + (part < 2 ? kAbDk : kAbDv) + 32u * (part & 1), v);
+                    tmem_wait_ld(v);
+                    ab_stage<4>(sOut + (part >> 1) * kAbTile, r, 4 * (part & 1), v, part < 2 ? a.scale : 1.0f);
+                }
                 tc_fence_before();
                 arrive(accfree);
-                ab_stage<8>(sOut + kAbTile, r, 0, &v[0][0], 1.0f);
                 fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    const int y = w.j * kAbB + 32 * quad;  // tokens past T lie outside the map and are not written
-                    ab_store_3d(&tmDqkv, smem_u32(sOut + quad * 4096), a.C + h * kAbD, y, b);
-                    ab_store_3d(&tmDqkv, smem_u32(sOut + kAbTile + quad * 4096), 2 * a.C + h * kAbD, y, b);
-                    bulk_commit();
-                }
-                __syncwarp();
+                arrive(outfull + 8 * (msg & 1));
+                ++msg;
             }
         }
-        if (sender && ok) settle();
         if (!ok && lane == 0) give_up();
-        if (lane == 0) bulk_wait_read_all();
     }
 
     __syncwarp();
@@ -809,28 +798,32 @@ attn_bwd_short_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_co
             __syncwarp();
         }
     };
-    const uint32_t one = lane == 0;
     wait(kq);
     if (warp == 0) {
         const uint64_t kd = sw128_kmajor_desc(smem_u32(sK)), qd = sw128_kmajor_desc(smem_u32(sQ));
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kAbD / 16; ++kk)
-            ab_mma(one, tmem + kAbS, kd + 2u * kk, qd + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
-        ab_commit(one, sfull);
+            for (int kk = 0; kk < kAbD / 16; ++kk)
+                tc_mma<true>(tmem + kAbS, kd + 2u * kk, qd + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
+            tc_commit(sfull);
+        }
+        __syncwarp();
     }
     wait(vdo);
     if (warp == 0) {
         const uint64_t vd = sw128_kmajor_desc(smem_u32(sV)), od = sw128_kmajor_desc(smem_u32(sDO));
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kAbD / 16; ++kk)
-            ab_mma(one, tmem + kAsDp, vd + 2u * kk, od + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
-        ab_commit(one, dpfull);
+            for (int kk = 0; kk < kAbD / 16; ++kk)
+                tc_mma<true>(tmem + kAsDp, vd + 2u * kk, od + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
+            tc_commit(dpfull);
+        }
+        __syncwarp();
     }
     const int grp = warp >> 2, quad = warp & 3;
     const int r = 32 * quad + lane;  // key, TMEM lane
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
     const bool masked = a.causal || a.T < kAbB;
-    const int from = r >= a.T ? 64 : a.causal ? r - 64 * grp : 0;
     wait(sfull);
     tc_fence_after();
     uint32_t s[2][32];
@@ -842,19 +835,26 @@ attn_bwd_short_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_co
     __syncthreads();  // S' has been read (P' and dQ take its place); the statistics are there
     tc_fence_after();
     uint64_t p[2][16];
-    ab_probs(s, stat + 64 * grp, ab_pack(a.scale_log2, a.scale_log2), p);
-    if (masked) ab_hide(p, from);
-    ab_put_p(tmem + lanes + kAsP + 32u * grp, p);
+#pragma unroll
+    for (int ch = 0; ch < 2; ++ch) {
+        const int q0 = 64 * grp + 32 * ch;  // the chunk's first query; visible from `from` on
+        const int from = r >= a.T ? 32 : a.causal ? r - q0 : 0;
+        ab_probs(s[ch], stat + q0, ab_pack(a.scale_log2, a.scale_log2), p[ch]);
+        if (masked) ab_hide(p[ch], from);
+        ab_put_p(tmem + lanes + kAsP + 32u * grp + 16u * ch, p[ch]);
+    }
+    ab_tmem_wait_st();
     wait(dpfull);
     tc_fence_after();
     uint8_t* ds_row = sDS + grp * (kAbDs / 2) + r * 128;
 #pragma unroll
     for (int ch = 0; ch < 2; ++ch) {
-        const float* nd = stat + kAbB + 64 * grp + 32 * ch;
-        tmem_ld32_async(tmem + lanes + kAsDp + 64u * grp + 32u * ch, s[0]);
+        const int q0 = 64 * grp + 32 * ch;
+        const int from = r >= a.T ? 32 : a.causal ? r - q0 : 0;
+        tmem_ld32_async(tmem + lanes + kAsDp + q0, s[0]);
         tmem_wait_ld(s[0]);
-        if (masked) ab_put_ds<true>(ch, s[0], p[ch], nd, ds_row, r, from);
-        else ab_put_ds<false>(ch, s[0], p[ch], nd, ds_row, r, from);
+        if (masked) ab_put_ds<true>(s[0], p[ch], stat + kAbB + q0, ds_row, r, 4 * ch, from);
+        else ab_put_ds<false>(s[0], p[ch], stat + kAbB + q0, ds_row, r, 4 * ch, from);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -864,14 +864,17 @@ attn_bwd_short_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_co
         const uint64_t od = sw128_mnmajor_desc(smem_u32(sDO)), qd = sw128_mnmajor_desc(smem_u32(sQ)),
                        kd = sw128_mnmajor_desc(smem_u32(sK));
         const uint64_t dsk = sw128_kmajor_desc(smem_u32(sDS)), dsm = ab_ds_mn_desc(smem_u32(sDS));
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kAbB / 16; ++kk) {
-            const uint32_t add = kk != 0 ? 1u : 0u;
-            ab_mma_ts(one, tmem + kAsDv, tmem + kAsP + 8u * kk, od + 128u * kk, kIdescDkv, add);
-            ab_mma(one, tmem + kAsDk, dsk + 1024u * (kk >> 2) + 2u * (kk & 3), qd + 128u * kk, kIdescDkv, add);
-            ab_mma(one, tmem + kAsDq, dsm + 128u * kk, kd + 128u * kk, kIdescDq, add);
+            for (int kk = 0; kk < kAbB / 16; ++kk) {
+                const uint32_t add = kk != 0 ? 1u : 0u;
+                tc_mma_ts(tmem + kAsDv, tmem + kAsP + 8u * kk, od + 128u * kk, kIdescDkv, add);
+                tc_mma<true>(tmem + kAsDk, dsk + 1024u * (kk >> 2) + 2u * (kk & 3), qd + 128u * kk, kIdescDkv, add);
+                tc_mma<true>(tmem + kAsDq, dsm + 128u * kk, kd + 128u * kk, kIdescDq, add);
+            }
+            tc_commit(done);
         }
-        ab_commit(one, done);
+        __syncwarp();
     }
     wait(done);
     tc_fence_after();
