@@ -17,15 +17,20 @@
 //   dK += dS' Q                   dS' (bf16) in shared memory, read K-major,
 //   dQ  = dS K                    and the same tile read MN-major as dS
 // With the keys on the lanes P' needs no trip through shared memory, whose
-// bandwidth the five products' operands otherwise exceed.
+// bandwidth the five products' operands otherwise exceed. For the same reason lse
+// and delta are not read by the threads (one value for all lanes costs shared
+// memory as much as 32): S' and dP' have one more step of 16, in which a row of
+// ones meets -lse / scale and -delta of the queries, each split into three bf16
+// parts that carry 24 bits. What the threads read from TMEM is then
+//   (s_ij - lse_i) / scale   and   dp_ij - delta_i.
 //
 // Sequences of one block (T <= 128): attn_bwd_short_kernel, a block per
 // (sequence, head), two blocks an SM so that one's loads and stores run under the
 // other's products and exponentials.
 //
 // Longer ones: three kernels:
-//   attn_bwd_prep    delta and lse in base-2 units, a pair a query, padded to
-//                    whole blocks of 128 queries.
+//   attn_bwd_prep    delta and lse, a row of eight bf16 a query, padded to whole
+//                    blocks of 128 queries.
 //   attn_bwd_kernel  a persistent block per SM walks work items (sequence, head,
 //                    block of 128 keys); an item walks the query blocks that see
 //                    its keys, with dk and dv accumulating in TMEM. dq is summed
@@ -63,21 +68,22 @@ constexpr int kAbD = 64;                           // head width
 constexpr int kAbGroups = 4;                       // groups of four warps that make P' and dS', 32 queries each
 constexpr int kAbThreads = 128 * (kAbGroups + 2);
 constexpr uint32_t kAbTile = kAbB * kAbD * 2;      // 16 KiB: 128 rows of 128 bytes, 128-byte swizzle
-constexpr uint32_t kAbStat = 2 * kAbB * 4;         // -lse log2(e) and -delta of 128 queries
+constexpr uint32_t kAbStat = kAbB * 16;            // eight bf16 of 128 queries: -lse / scale and -delta, in three parts each
+constexpr uint32_t kAbOnes = 512;                  // the rows that meet them
 constexpr int kAbKStages = 2, kAbQStages = 3;      // (V has one)
 constexpr uint32_t kAbQStage = 2 * kAbTile + kAbStat;
 constexpr uint32_t kAbDs = kAbB * kAbB * 2;        // dS': two 64-query K-major blocks of 16 KiB
 constexpr uint32_t kAbDqTile = kAbB * kAbD * 4;    // fp32 dq of a query block: [column / 4][row][4]
 constexpr int kAbBars = 2 * kAbKStages + 2 + 2 * kAbQStages + 10;
 constexpr size_t kAbSmem =
-    1024 + (kAbKStages + 1) * kAbTile + kAbQStages * kAbQStage + kAbDs + kAbDqTile + kAbBars * 8 + 16;
+    1024 + (kAbKStages + 1) * kAbTile + kAbQStages * kAbQStage + kAbDs + kAbDqTile + kAbOnes + kAbBars * 8 + 16;
 static_assert(kAbSmem <= 227 * 1024, "shared memory");
 // TMEM columns
 constexpr uint32_t kAbS = 0, kAbDp = 128, kAbDv = 256, kAbDk = 320, kAbDq = 384, kAbP = 448, kAbTmem = 512;
 // and of the short kernel, where dV and dK take dP's place and dQ half of S's
 constexpr int kAsThreads = 256;
 constexpr uint32_t kAsP = 0, kAsDq = 64, kAsDp = 128, kAsDv = 128, kAsDk = 192, kAsTmem = 256;
-constexpr size_t kAsSmem = 1024 + 4 * kAbTile + kAbDs + kAbStat + 6 * 8 + 16;
+constexpr size_t kAsSmem = 1024 + 4 * kAbTile + kAbDs + kAbStat + kAbOnes + 6 * 8 + 16;
 static_assert(2 * (kAsSmem + 1024) <= 228 * 1024, "two blocks an SM");
 // Register split (setmaxnreg, per warpgroup): launched at 80 a thread; the groups that
 // hold 32 probabilities and 32 dp a thread take what the others give back.
@@ -92,8 +98,8 @@ struct AbArgs {
     int items;           // heads * nb
     int chains;
     int causal;
-    float scale, scale_log2;
-    const float* stats;  // heads x nb x 256
+    float scale, scale_log2, inv_scale;
+    const uint4* stats;  // heads x nb x 128
     unsigned* flags;     // heads x chains x nb
     float* dq;           // heads x chains x nb tiles
     int* status;
@@ -111,16 +117,6 @@ __device__ __forceinline__ uint64_t ab_pack(float lo, float hi) {
 }
 __device__ __forceinline__ void ab_unpack(uint64_t v, float& lo, float& hi) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t ab_fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t ab_add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
 }
 __device__ __forceinline__ uint64_t ab_mul2(uint64_t a, uint64_t b) {
     uint64_t d;
@@ -215,18 +211,13 @@ __device__ __forceinline__ void regs_inc() {
 
 // ---- one thread's key and 32 of the block's queries ----
 
-// p = 2^(s scale log2(e) - lse log2(e)); nl = -lse log2(e) of the queries.
-__device__ __forceinline__ void ab_probs(const uint32_t (&s)[32], const float* nl, uint64_t sl2, uint64_t (&p)[16]) {
+// p = 2^(s scale log2(e)), s less lse / scale already.
+__device__ __forceinline__ void ab_probs(const uint32_t (&s)[32], uint64_t sl2, uint64_t (&p)[16]) {
 #pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-        const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(nl + c);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float x0, x1;
-            ab_unpack(ab_fma2(ab_pack(__uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1])), sl2, k ? l.y : l.x),
-                      x0, x1);
-            p[c / 2 + k] = ab_pack(ab_ex2(x0), ab_ex2(x1));
-        }
+    for (int c = 0; c < 16; ++c) {
+        float x0, x1;
+        ab_unpack(ab_mul2(ab_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2), x0, x1);
+        p[c] = ab_pack(ab_ex2(x0), ab_ex2(x1));
     }
 }
 // Only queries from `from` on see the key.
@@ -249,29 +240,24 @@ __device__ __forceinline__ void ab_put_p(uint32_t taddr, const uint64_t (&p)[16]
     }
     tmem_st16(taddr, pk);
 }
-// ds = p (dp - delta) in bf16 to pieces `first`.. of the thread's row of dS'; nd =
-// -delta. MASKED: a hidden pair takes nothing from dp or delta, whatever they are.
+// ds = p dp (dp less delta already) in bf16 to pieces `first`.. of the thread's row
+// of dS'. MASKED: a hidden pair takes nothing from dp, whatever it is.
 template <bool MASKED>
-__device__ __forceinline__ void ab_put_ds(const uint32_t (&dp)[32], const uint64_t (&p)[16], const float* nd,
-                                          uint8_t* ds_row, int r, int first, int from) {
+__device__ __forceinline__ void ab_put_ds(const uint32_t (&dp)[32], const uint64_t (&p)[16], uint8_t* ds_row, int r,
+                                          int first, int from) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
         uint32_t pk[4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int c = 8 * v + 4 * u;
-            const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(nd + c);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint64_t x = ab_pack(__uint_as_float(dp[c + 2 * k]), __uint_as_float(dp[c + 2 * k + 1]));
-                float x0, x1;
-                ab_unpack(ab_mul2(p[c / 2 + k], ab_add2(x, k ? d.y : d.x)), x0, x1);
-                if constexpr (MASKED) {
-                    x0 = c + 2 * k >= from ? x0 : 0.f;
-                    x1 = c + 2 * k + 1 >= from ? x1 : 0.f;
-                }
-                pk[2 * u + k] = pack_bf16x2(x0, x1);
+        for (int k = 0; k < 4; ++k) {
+            const int c = 8 * v + 2 * k;
+            float x0, x1;
+            ab_unpack(ab_mul2(p[c / 2], ab_pack(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1]))), x0, x1);
+            if constexpr (MASKED) {
+                x0 = c >= from ? x0 : 0.f;
+                x1 = c + 1 >= from ? x1 : 0.f;
             }
+            pk[k] = pack_bf16x2(x0, x1);
         }
         *reinterpret_cast<uint4*>(ds_row + (((first + v) ^ (r & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
     }
@@ -290,11 +276,11 @@ __device__ __forceinline__ void ab_stage(uint8_t* tile, int r, int first, const 
     }
 }
 
-// Statistics of 128 queries of one head by 256 threads (two a query): -lse
-// log2(e), -inf (probability 0) past the sequence's end and for a query that sees
-// no key, and -delta.
+// Statistics of 128 queries of one head by 256 threads (two a query), a row of
+// eight bf16 each: -lse / scale (far below everything past the sequence's end and
+// for a query that sees no key: probability 0) and -delta, in three parts.
 __device__ __forceinline__ void ab_stats(const uint16_t* out, const uint16_t* dout, const float* lse, int T, int H,
-                                         int b, int h, int i, float* st) {
+                                         int b, int h, int i, float inv_scale, uint4* st) {
     const int row = threadIdx.x >> 1, half = threadIdx.x & 1;
     const int t = i * kAbB + row;
     float sum = 0.f;
@@ -317,12 +303,44 @@ __device__ __forceinline__ void ab_stats(const uint16_t* out, const uint16_t* do
         }
     }
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    if (half) {
-        st[kAbB + row] = -sum;
-    } else {
+    if (half == 0) {
+        const float far = -1e30f;  // finite, so that it is 0 where it meets a 0
         const float l = t < T ? lse[((size_t)b * H + h) * T + t] : -INFINITY;
-        st[row] = l == -INFINITY ? -INFINITY : -l * kAbLog2e;
+        const float e = l == -INFINITY || l == INFINITY ? far : -l * inv_scale;
+        const float e0 = bf16_bits_to_f32(f32_to_bf16_bits(e)), e1 = bf16_bits_to_f32(f32_to_bf16_bits(e - e0));
+        const float d0 = bf16_bits_to_f32(f32_to_bf16_bits(-sum)), d1 = bf16_bits_to_f32(f32_to_bf16_bits(-sum - d0));
+        const bool cut = e == far;
+        st[row] = make_uint4(pack_bf16x2(e0, cut ? 0.f : e1), pack_bf16x2(cut ? 0.f : (e - e0) - e1, d0),
+                             pack_bf16x2(d1, (-sum - d0) - d1), 0u);
     }
+}
+// The rows that meet them: ones in places 0-2 (lse) and 3-5 (delta). Eight equal
+// rows and eight of zeros stand for all 128 (the descriptor's strides are 0).
+__device__ __forceinline__ void ab_ones(uint4* ones) {
+    const int i = threadIdx.x;
+    if (i < 32) {
+        const bool rows = (i & 8) == 0;
+        ones[i] = !rows    ? make_uint4(0u, 0u, 0u, 0u)
+                  : i < 16 ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u)
+                           : make_uint4(0u, 0x3F800000u, 0x3F803F80u, 0u);
+    }
+}
+// Descriptors without swizzle: 8 x 16-byte cores, `k` bytes apart along K, `mn` along the rows.
+__device__ __forceinline__ uint64_t ab_flat_desc(uint32_t saddr, uint32_t k, uint32_t mn) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(k >> 4) << 16;
+    d |= static_cast<uint64_t>(mn >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    return d;
+}
+// S' and dP' with their extra step. The second half of its K is zero on the ones'
+// side, so the statistics' side may repeat its first half there.
+__device__ __forceinline__ void ab_mma_scores(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t ones, uint32_t stat) {
+    const uint64_t ad = sw128_kmajor_desc(a), bd = sw128_kmajor_desc(b);
+#pragma unroll
+    for (int kk = 0; kk < kAbD / 16; ++kk) tc_mma<true>(d_tmem, ad + 2u * kk, bd + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
+    tc_mma<true>(d_tmem, ab_flat_desc(ones, 128, 0), ab_flat_desc(stat, 0, 128), kIdescS, 1u);
 }
 
 // The block's items: rounds of gridDim.x items, every other round in reverse, so
@@ -369,7 +387,8 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
     uint8_t* sQ = sV + kAbTile;                // stage: Q, dO, statistics
     uint8_t* sDS = sQ + QS * kAbQStage;
     uint8_t* sOut = sDS + kAbDs;               // dq on its way out; dk and dv at an item's end
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + kAbDqTile);
+    uint8_t* sOnes = sOut + kAbDqTile;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sOnes + kAbOnes);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kAbBars);
     int* s_abort = reinterpret_cast<int*>(tmem_slot + 1);
 
@@ -412,6 +431,8 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         tma_prefetch_map(&tmDo);
         tma_prefetch_map(&tmDqkv);
     }
+    ab_ones(reinterpret_cast<uint4*>(sOnes));
+    fence_proxy_async_smem();
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), kAbTmem);
     tc_fence_before();
     __syncthreads();
@@ -460,7 +481,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
                     mbar_expect_tx(qfull + 8 * qs, kAbQStage);
                     tma_load_3d(smem_u32(q), &tmQkv, qfull + 8 * qs, h * kAbD, i * kAbB, b);
                     tma_load_3d(smem_u32(q + kAbTile), &tmDo, qfull + 8 * qs, h * kAbD, i * kAbB, b);
-                    bulk_load(smem_u32(q + 2 * kAbTile), a.stats + ((size_t)w.bh * a.nb + i) * (2 * kAbB), kAbStat,
+                    bulk_load(smem_u32(q + 2 * kAbTile), a.stats + ((size_t)w.bh * a.nb + i) * kAbB, kAbStat,
                               qfull + 8 * qs);
                 }
                 if (i == w.i0) {  // V's one stage frees when the item before has its last dP'
@@ -499,19 +520,13 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
             uint32_t n = 0;
             bool ok = true;
             auto issue_s = [&](uint32_t k) {  // S' of step k, the lead's
-                const uint64_t kd = sw128_kmajor_desc(smem_u32(sK + (lead.m % KS) * kAbTile));
-                const uint64_t qd = sw128_kmajor_desc(smem_u32(sQ + (k % QS) * kAbQStage));
-#pragma unroll
-                for (int kk = 0; kk < kAbD / 16; ++kk)
-                    tc_mma<true>(tmem + kAbS, kd + 2u * kk, qd + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
+                const uint32_t q = smem_u32(sQ + (k % QS) * kAbQStage);
+                ab_mma_scores(tmem + kAbS, smem_u32(sK + (lead.m % KS) * kAbTile), q, smem_u32(sOnes), q + 2 * kAbTile);
                 tc_commit(sfull);
             };
             auto issue_dp = [&](uint32_t k) {  // dP' of step k, the lead's
-                const uint64_t vd = sw128_kmajor_desc(smem_u32(sV));
-                const uint64_t od = sw128_kmajor_desc(smem_u32(sQ + (k % QS) * kAbQStage + kAbTile));
-#pragma unroll
-                for (int kk = 0; kk < kAbD / 16; ++kk)
-                    tc_mma<true>(tmem + kAbDp, vd + 2u * kk, od + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
+                const uint32_t q = smem_u32(sQ + (k % QS) * kAbQStage);
+                ab_mma_scores(tmem + kAbDp, smem_u32(sV), q + kAbTile, smem_u32(sOnes) + 256, q + 2 * kAbTile);
                 tc_commit(dpfull);
             };
             // the operands of step k have landed
@@ -656,19 +671,18 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         bool ok = true;
         AbWalker w;
         for (w.init(a); w.valid; w.next(a), ++n) {
-            const float* stat = reinterpret_cast<const float*>(sQ + (n % QS) * kAbQStage + 2 * kAbTile) + 32 * grp;
             const bool diag = a.causal && w.i == w.j;
             const bool masked = diag || (w.j + 1) * kAbB > a.T;
             // query c of this group is visible to the thread's key from `from` on
             const int from = w.j * kAbB + r >= a.T ? 32 : diag ? r - 32 * grp : 0;
-            ok = !aborted() && wait(qfull + 8 * (n % QS), (n / QS) & 1) && wait(sfull, n & 1);
+            ok = !aborted() && wait(sfull, n & 1);
             if (!ok) break;
             tc_fence_after();
             uint32_t s[32];
             tmem_ld32_async(tS, s);
             tmem_wait_ld(s);
             uint64_t p[16];
-            ab_probs(s, stat, sl2, p);
+            ab_probs(s, sl2, p);
             if (masked) ab_hide(p, from);
             // dP' of this step, and so dV of the step before: P' may be rewritten
             ok = wait(dpfull, n & 1);
@@ -684,8 +698,8 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
             // dK and dQ of the step before: dS' may be rewritten
             ok = n == 0 || wait(done, (n - 1) & 1);
             if (!ok) break;
-            if (masked) ab_put_ds<true>(s, p, stat + kAbB, ds_row, r, 4 * (grp & 1), from);
-            else ab_put_ds<false>(s, p, stat + kAbB, ds_row, r, 4 * (grp & 1), from);
+            if (masked) ab_put_ds<true>(s, p, ds_row, r, 4 * (grp & 1), from);
+            else ab_put_ds<false>(s, p, ds_row, r, 4 * (grp & 1), from);
             fence_proxy_async_smem();
             tc_fence_before();
             arrive(dsready);
@@ -758,8 +772,8 @@ attn_bwd_short_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_co
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sK = smem, *sQ = sK + kAbTile, *sV = sQ + kAbTile, *sDO = sV + kAbTile, *sDS = sDO + kAbTile;
-    float* stat = reinterpret_cast<float*>(sDS + kAbDs);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(stat + 2 * kAbB);
+    uint8_t *sStat = sDS + kAbDs, *sOnes = sStat + kAbStat;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sOnes + kAbOnes);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6);
     const uint32_t kq = smem_u32(bars), vdo = kq + 8, sfull = kq + 16, dpfull = kq + 24, done = kq + 32;
 
@@ -788,7 +802,10 @@ attn_bwd_short_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_co
         tma_load_3d(smem_u32(sDO), &tmDo, vdo, h * kAbD, 0, b);
     }
     __syncwarp();
-    ab_stats(out, dout, lse, a.T, a.H, b, h, 0, stat);
+    ab_ones(reinterpret_cast<uint4*>(sOnes));
+    ab_stats(out, dout, lse, a.T, a.H, b, h, 0, a.inv_scale, reinterpret_cast<uint4*>(sStat));
+    fence_proxy_async_smem();
+    __syncthreads();
     // A wait that runs out sets the status word; the block then goes on with what
     // it has, and its outputs are not to be used.
     auto wait = [&](uint32_t bar) {
@@ -800,22 +817,16 @@ attn_bwd_short_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_co
     };
     wait(kq);
     if (warp == 0) {
-        const uint64_t kd = sw128_kmajor_desc(smem_u32(sK)), qd = sw128_kmajor_desc(smem_u32(sQ));
         if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < kAbD / 16; ++kk)
-                tc_mma<true>(tmem + kAbS, kd + 2u * kk, qd + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
+            ab_mma_scores(tmem + kAbS, smem_u32(sK), smem_u32(sQ), smem_u32(sOnes), smem_u32(sStat));
             tc_commit(sfull);
         }
         __syncwarp();
     }
     wait(vdo);
     if (warp == 0) {
-        const uint64_t vd = sw128_kmajor_desc(smem_u32(sV)), od = sw128_kmajor_desc(smem_u32(sDO));
         if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < kAbD / 16; ++kk)
-                tc_mma<true>(tmem + kAsDp, vd + 2u * kk, od + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
+            ab_mma_scores(tmem + kAsDp, smem_u32(sV), smem_u32(sDO), smem_u32(sOnes) + 256, smem_u32(sStat));
             tc_commit(dpfull);
         }
         __syncwarp();
@@ -832,14 +843,14 @@ attn_bwd_short_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_co
     tmem_wait_ld(s[0]);
     tmem_wait_ld(s[1]);
     tc_fence_before();
-    __syncthreads();  // S' has been read (P' and dQ take its place); the statistics are there
+    __syncthreads();  // S' has been read (P' and dQ take its place)
     tc_fence_after();
     uint64_t p[2][16];
 #pragma unroll
     for (int ch = 0; ch < 2; ++ch) {
         const int q0 = 64 * grp + 32 * ch;  // the chunk's first query; visible from `from` on
         const int from = r >= a.T ? 32 : a.causal ? r - q0 : 0;
-        ab_probs(s[ch], stat + q0, ab_pack(a.scale_log2, a.scale_log2), p[ch]);
+        ab_probs(s[ch], ab_pack(a.scale_log2, a.scale_log2), p[ch]);
         if (masked) ab_hide(p[ch], from);
         ab_put_p(tmem + lanes + kAsP + 32u * grp + 16u * ch, p[ch]);
     }
@@ -853,8 +864,8 @@ attn_bwd_short_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_co
         const int from = r >= a.T ? 32 : a.causal ? r - q0 : 0;
         tmem_ld32_async(tmem + lanes + kAsDp + q0, s[0]);
         tmem_wait_ld(s[0]);
-        if (masked) ab_put_ds<true>(s[0], p[ch], stat + kAbB + q0, ds_row, r, 4 * ch, from);
-        else ab_put_ds<false>(s[0], p[ch], stat + kAbB + q0, ds_row, r, 4 * ch, from);
+        if (masked) ab_put_ds<true>(s[0], p[ch], ds_row, r, 4 * ch, from);
+        else ab_put_ds<false>(s[0], p[ch], ds_row, r, 4 * ch, from);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -912,13 +923,13 @@ attn_bwd_short_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_co
 
 // The statistics of every query block, and its dq counters zeroed.
 __global__ void __launch_bounds__(256) attn_bwd_prep(const uint16_t* out, const uint16_t* dout, const float* lse, int T,
-                                                     int H, int nb, int bh0, int chains, float* stats,
-                                                     unsigned* flags) {
+                                                     int H, int nb, int bh0, int chains, float inv_scale,
+                                                     uint4* stats, unsigned* flags) {
     pdl_wait();
     pdl_launch_dependents();
     const int local = blockIdx.x / nb, i = blockIdx.x % nb;
     const int bh = bh0 + local;
-    ab_stats(out, dout, lse, T, H, bh / H, bh % H, i, stats + (size_t)blockIdx.x * (2 * kAbB));
+    ab_stats(out, dout, lse, T, H, bh / H, bh % H, i, inv_scale, stats + (size_t)blockIdx.x * kAbB);
     for (int g = threadIdx.x; g < chains; g += 256) flags[((size_t)local * chains + g) * nb + i] = 0u;
 }
 
@@ -1009,6 +1020,7 @@ int launch_attention_backward(const AttnBwdProblem& p) {
     a.causal = p.causal ? 1 : 0;
     a.scale = p.scale;
     a.scale_log2 = p.scale * kAbLog2e;
+    a.inv_scale = 1.0f / p.scale;
     a.status = p.dev_status;
 
     cudaLaunchAttribute attr;
@@ -1058,7 +1070,7 @@ int launch_attention_backward(const AttnBwdProblem& p) {
         a.bh0 = (int)bh0;
         a.heads = count;
         a.items = count * nb;
-        float* stats = reinterpret_cast<float*>(ws);
+        uint4* stats = reinterpret_cast<uint4*>(ws);
         char* rest = ws + align_up((size_t)count * stat, 256);
         a.stats = stats;
         a.flags = reinterpret_cast<unsigned*>(rest);
@@ -1066,7 +1078,8 @@ int launch_attention_backward(const AttnBwdProblem& p) {
         cfg.gridDim = dim3((unsigned)a.items);
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;
-        if (cudaLaunchKernelEx(&cfg, attn_bwd_prep, out, dout, p.lse, p.T, p.H, nb, a.bh0, a.chains, stats, a.flags) !=
+        if (cudaLaunchKernelEx(&cfg, attn_bwd_prep, out, dout, p.lse, p.T, p.H, nb, a.bh0, a.chains,
+                               a.inv_scale, stats, a.flags) !=
             cudaSuccess)
             return LIN_ERR_CUDA;
         cfg.gridDim = dim3((unsigned)std::min(a.items, p.sm_count));
