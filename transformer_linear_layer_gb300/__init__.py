@@ -292,6 +292,11 @@ def _stream_ptr(stream, device):
     import torch
 
     if stream is None:
+        # the current stream's handle without the Stream object around it (a call's
+        # host time counts for single tokens)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return ctypes.c_void_p(raw(device))
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -658,52 +663,55 @@ def token_logprobs(logits, tokens=None, top: int = 0, temperature: float = 1.0, 
     if not 0 <= top <= min(64, V):
         raise ValueError(f"top must be between 0 and {min(64, V)}, got {top}")
     _same_device(logits, tokens)
-    ttype, logprob = TYPE_INT64, None
+    ttype = TYPE_INT64
     if tokens is not None:
         ttype = _index_type(tokens, "tokens")
         _check(tokens, tokens.dtype, (R,), "tokens")
-        logprob = torch.empty(R, dtype=torch.float32, device=logits.device)
-    stats = torch.empty((2, R), dtype=torch.float32, device=logits.device)
+    logprob = None if tokens is None else torch.empty(R, dtype=torch.float32, device=logits.device)
+    entropy = torch.empty(R, dtype=torch.float32, device=logits.device)
+    lse = torch.empty(R, dtype=torch.float32, device=logits.device)
     top_logprob = torch.empty((R, top), dtype=torch.float32, device=logits.device)
     top_ids = torch.empty((R, top), dtype=torch.int32, device=logits.device)
     dev = logits.device.index if logits.device.index is not None else 0
     ctx = ctx or default_context(dev)
     rc = library().lin_token_logprobs(ctx._h, R, V, logits.data_ptr(), ld, ztype, _ptr(tokens), ttype,
-                                      float(temperature), int(top), _ptr(logprob), stats[0].data_ptr(),
-                                      stats[1].data_ptr(), top_logprob.data_ptr(), top_ids.data_ptr(),
+                                      float(temperature), int(top), _ptr(logprob), entropy.data_ptr(),
+                                      lse.data_ptr(), top_logprob.data_ptr(), top_ids.data_ptr(),
                                       _stream_ptr(stream, dev))
     if rc != OK:
         raise LinError(rc, "lin_token_logprobs")
-    return TokenLogprobs(logprob, stats[0], stats[1], top_logprob, top_ids)
+    return TokenLogprobs(logprob, entropy, lse, top_logprob, top_ids)
 
 
-def _distill_args(logits, ids, teacher, rows):
+def _distill_args(logits, ids, teacher, lse=None, weight=None):
     import torch
 
     R, V, ld = _check_logits(logits)
     if ids.dim() != 2 or ids.shape[0] != R:
         raise ValueError(f"ids must be R x K with R = {R}, got {tuple(ids.shape)}")
+    K = ids.shape[1]
     itype, ttype = _index_type(ids, "ids"), _float_type(teacher, "teacher")
-    _check(ids, ids.dtype, tuple(ids.shape), "ids")
-    _check(teacher, teacher.dtype, tuple(ids.shape), "teacher")
-    for what, t in rows.items():
+    _check(ids, ids.dtype, (R, K), "ids")
+    _check(teacher, teacher.dtype, (R, K), "teacher")
+    for what, t in (("lse", lse), ("the rows' weight", weight)):
         if t is not None:
             _check(t, torch.float32, (R,), what)
-    _same_device(logits, ids, teacher, *rows.values())
-    return (R, V, ids.shape[1], logits.data_ptr(), ld, _float_type(logits, "logits"), ids.data_ptr(), itype,
+    _same_device(logits, ids, teacher, lse, weight)
+    return (R, V, K, logits.data_ptr(), ld, _float_type(logits, "logits"), ids.data_ptr(), itype,
             teacher.data_ptr(), ttype)
 
 
-def _dlogits(logits, out):
+def _dlogits(logits, out, args):
     """The gradient's tensor and row stride: ``out``, or a new one whose rows
     lie like the logits' (padding included, so that both move in whole units)."""
     import torch
 
+    R, V, ld = args[0], args[1], args[4]
     if out is None:
-        R, V, ld = _check_logits(logits)
         pitch = ld if ld <= V + 1024 else V
-        out = torch.empty((R, pitch), dtype=logits.dtype, device=logits.device)[:, :V]
-    elif out.dtype != logits.dtype or out.shape != logits.shape:
+        out = torch.empty((R, pitch), dtype=logits.dtype, device=logits.device)
+        return (out if pitch == V else out[:, :V]), pitch
+    if out.dtype != logits.dtype or out.shape != logits.shape:
         raise ValueError("out must have the logits' shape and type")
     _same_device(logits, out)
     return out, _check_logits(out, "out")[2]
@@ -719,23 +727,24 @@ def distill_forward(logits, ids, teacher, temperature: float = 1.0, ctx: Context
     lse is what :func:`distill_backward` needs."""
     import torch
 
-    args = _distill_args(logits, ids, teacher, {})
-    out = torch.empty((2, args[0]), dtype=torch.float32, device=logits.device)
+    args = _distill_args(logits, ids, teacher)
+    loss = torch.empty(args[0], dtype=torch.float32, device=logits.device)
+    lse = torch.empty(args[0], dtype=torch.float32, device=logits.device)
     dev = logits.device.index if logits.device.index is not None else 0
     ctx = ctx or default_context(dev)
-    rc = library().lin_distill_forward(ctx._h, *args, float(temperature), out[0].data_ptr(), out[1].data_ptr(),
+    rc = library().lin_distill_forward(ctx._h, *args, float(temperature), loss.data_ptr(), lse.data_ptr(),
                                        _stream_ptr(stream, dev))
     if rc != OK:
         raise LinError(rc, "lin_distill_forward")
-    return out[0], out[1]
+    return loss, lse
 
 
 def distill_backward(logits, ids, teacher, lse, grad_loss, temperature: float = 1.0, out=None,
                      ctx: Context | None = None, stream=None):
     """The logits' gradient, from :func:`distill_forward`'s lse and the
     gradient of each row's loss (R fp32). ``out`` may be ``logits``."""
-    args = _distill_args(logits, ids, teacher, {"lse": lse, "grad_loss": grad_loss})
-    out, ldd = _dlogits(logits, out)
+    args = _distill_args(logits, ids, teacher, lse, grad_loss)
+    out, ldd = _dlogits(logits, out, args)
     dev = logits.device.index if logits.device.index is not None else 0
     ctx = ctx or default_context(dev)
     rc = library().lin_distill_backward(ctx._h, *args, float(temperature), lse.data_ptr(), grad_loss.data_ptr(),
@@ -752,8 +761,8 @@ def distill_forward_backward(logits, ids, teacher, weight=None, temperature: flo
     ``out`` may be ``logits``: the gradient then replaces them."""
     import torch
 
-    args = _distill_args(logits, ids, teacher, {"weight": weight})
-    out, ldd = _dlogits(logits, out)
+    args = _distill_args(logits, ids, teacher, None, weight)
+    out, ldd = _dlogits(logits, out, args)
     loss = torch.empty(args[0], dtype=torch.float32, device=logits.device)
     dev = logits.device.index if logits.device.index is not None else 0
     ctx = ctx or default_context(dev)
