@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kLpThreads, 8) logprob_kernel(const LogprobArg
     }
     st = lg_join_blocks<kLpThreads, CL>(st, a.c, sh, rank);
     const float base = lg_base(st.m), logs = log2f(st.s);
-    auto logprob = [&](float z) { return st.s == 0.f ? -INFINITY : ((z - base) * a.c - logs) * kLn2; };
+    auto logprob = [&](float z) { return st.s == 0.f ? -INFINITY : fmaf(-logs, kLn2, (z - base) * a.inv_tau); };
     if (asked) {
         if (a.logprob) a.logprob[r] = tok < 0 ? 0.f : tok >= a.V ? NAN : logprob(z_tok);
         if (a.entropy) a.entropy[r] = st.s == 0.f ? 0.f : (logs - st.t / st.s) * kLn2;
