@@ -98,7 +98,7 @@ struct AbArgs {
     int items;           // heads * nb
     int chains;
     int ahead;           // blocks that run at once (short kernel)
-    int causal;
+    int causal, snake;
     float scale, scale_log2, inv_scale;
     const uint4* stats;  // heads x nb x 128
     unsigned* flags;     // heads x chains x nb
@@ -349,9 +349,13 @@ __device__ __forceinline__ void ab_mma_scores(uint32_t d_tmem, uint32_t a, uint3
     tc_mma<true>(d_tmem, ab_flat_desc(ones, 128, 0), ab_flat_desc(stat, 0, 128), kIdescS, 1u);
 }
 
-// The block's items: rounds of gridDim.x items, every other round in reverse, so
-// that the sums of the items' lengths (which fall along the walk when causal)
-// stay close. Items are ordered by key block, then by head.
+// The block's items: rounds of gridDim.x items. Items are ordered by key block, then
+// by head; their lengths fall along the walk when causal. With every other round in
+// reverse (`snake`) the sums of the lengths stay close, but an item may follow one of
+// its chain that starts after it: taken where there are chains for at least half of
+// a head's blocks that run together, when causal (24 heads of 4096 causal, 2 chains: 124 steps of
+// the longest block against 109 in plain rounds; 96 heads of 1024, 2 chains: 33
+// against 36).
 struct AbWalker {
     int round, m;        // round, items so far
     int j, bh;           // key block, launch-local (sequence, head)
@@ -359,7 +363,7 @@ struct AbWalker {
     bool valid;
     __device__ __forceinline__ void place(const AbArgs& a) {
         const int c = blockIdx.x, g = gridDim.x;
-        const long long idx = (long long)round * g + ((round & 1) ? g - 1 - c : c);
+        const long long idx = (long long)round * g + (a.snake && (round & 1) ? g - 1 - c : c);
         valid = idx < a.items;
         j = valid ? (int)(idx / a.heads) : 0;
         bh = valid ? (int)(idx % a.heads) : 0;
@@ -565,11 +569,9 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
                 for (int kk = 0; kk < kAbB / 16; ++kk)
                     tc_mma_ts(tmem + kAbDv, tmem + kAbP + 8u * kk, dod + 128u * kk, kIdescDkv,
                               (kk != 0 || !first) ? 1u : 0u);
-                if (lead.valid) {
-                    if (lead.first() && !mbar_wait(vfull, lead.m & 1)) {
-                        ok = false;
-                        break;
-                    }
+                // (a new item's V is still on its way here: its dP' comes after dK and dQ)
+                const bool turn = lead.valid && lead.first();
+                if (lead.valid && !turn) {
                     issue_dp(n + 1);
                     lead.next(a);
                 }
@@ -590,6 +592,15 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
                 for (int kk = 0; kk < kAbB / 16; ++kk)
                     tc_mma<true>(tmem + kAbDq, dsm + 128u * kk, kd + 128u * kk, kIdescDq, kk != 0 ? 1u : 0u);
                 tc_commit(done);
+                if (turn) {
+                    if (!mbar_wait(vfull, lead.m & 1)) {
+                        ok = false;
+                        ++n;
+                        break;
+                    }
+                    issue_dp(n + 1);
+                    lead.next(a);
+                }
                 cur.next(a);
                 ++n;
             }
@@ -612,6 +623,18 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
             AbWalker w;
             for (w.init(a); ok && w.valid; w.next(a)) {
                 const int bh = a.bh0 + w.bh, b = bh / a.H, h = bh % a.H;
+                if (w.last(a) && (msg++ & 1) == (uint32_t)(warp & 1)) {
+                    // dk and dv; tokens past T lie outside the map and are not written
+                    ok = mbar_wait(outfull + 8 * ((msg - 1) & 1), ((msg - 1) >> 1) & 1);
+                    if (!ok) break;
+                    for (int y = 0; y < kAbB; y += 32) {
+                        ab_store_3d(&tmDqkv, smem_u32(sOut + y * 128), a.C + h * kAbD, w.j * kAbB + y, b);
+                        ab_store_3d(&tmDqkv, smem_u32(sOut + kAbTile + y * 128), 2 * a.C + h * kAbD, w.j * kAbB + y, b);
+                    }
+                    bulk_commit();
+                    bulk_wait_read_all();
+                    mbar_arrive(outfree);
+                }
                 if ((msg++ & 1) == (uint32_t)(warp & 1)) {
                     if (*(volatile int*)s_abort != 0 || !mbar_wait(outfull + 8 * ((msg - 1) & 1), ((msg - 1) >> 1) & 1)) {
                         ok = false;
@@ -645,18 +668,6 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
                         fence_proxy_async_global();
                         st_release_gpu(a.flags + slot, (unsigned)pos + 1u);
                     }
-                }
-                if (w.last(a) && (msg++ & 1) == (uint32_t)(warp & 1)) {
-                    // dk and dv; tokens past T lie outside the map and are not written
-                    ok = mbar_wait(outfull + 8 * ((msg - 1) & 1), ((msg - 1) >> 1) & 1);
-                    if (!ok) break;
-                    for (int y = 0; y < kAbB; y += 32) {
-                        ab_store_3d(&tmDqkv, smem_u32(sOut + y * 128), a.C + h * kAbD, w.j * kAbB + y, b);
-                        ab_store_3d(&tmDqkv, smem_u32(sOut + kAbTile + y * 128), 2 * a.C + h * kAbD, w.j * kAbB + y, b);
-                    }
-                    bulk_commit();
-                    bulk_wait_read_all();
-                    mbar_arrive(outfree);
                 }
             }
             if (!ok) give_up();
@@ -728,6 +739,21 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
             arrive(qempty + 8 * (n % QS));
             if (last) arrive(kempty + 8 * (w.m % KS));
             uint32_t v[32];
+            if (last) {  // first, since the next item's dV waits for it
+#pragma unroll
+                for (int part = 0; part < 4; ++part) {  // dk, then dv
+                    tmem_ld32_async(tmem + lanes + (part < 2 ? kAbDk : kAbDv) + 32u * (part & 1), v);
+                    tmem_wait_ld(v);
+                    ab_stage<4>(sOut + (part >> 1) * kAbTile, r, 4 * (part & 1), v, part < 2 ? a.scale : 1.0f);
+                }
+                tc_fence_before();
+                arrive(accfree);
+                fence_proxy_async_smem();
+                arrive(outfull + 8 * (msg & 1));
+                ++msg;
+                ok = wait(outfree, (msg - 1) & 1);
+                if (!ok) break;
+            }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 tmem_ld32_async(tmem + lanes + kAbDq + 32u * half, v);
@@ -742,21 +768,6 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
             fence_proxy_async_smem();
             arrive(outfull + 8 * (msg & 1));
             ++msg;
-            if (last) {
-                ok = wait(outfree, (msg - 1) & 1);
-                if (!ok) break;
-#pragma unroll
-                for (int part = 0; part < 4; ++part) {  // dk, then dv
-                    tmem_ld32_async(tmem + lanes + (part < 2 ? kAbDk : kAbDv) + 32u * (part & 1), v);
-                    tmem_wait_ld(v);
-                    ab_stage<4>(sOut + (part >> 1) * kAbTile, r, 4 * (part & 1), v, part < 2 ? a.scale : 1.0f);
-                }
-                tc_fence_before();
-                arrive(accfree);
-                fence_proxy_async_smem();
-                arrive(outfull + 8 * (msg & 1));
-                ++msg;
-            }
         }
         if (!ok && lane == 0) give_up();
     }
@@ -1075,6 +1086,7 @@ int launch_attention_backward(const AttnBwdProblem& p) {
     const long long together = (p.sm_count + heads - 1) / heads;
     const long long room = (long long)((avail / heads - stat) / chain);
     a.chains = (int)std::max(1ll, std::min({together, room, (long long)nb}));
+    a.snake = p.causal && 2 * a.chains >= std::min(together, (long long)nb);
 
     static std::atomic<unsigned long long> attr_set{0};
     if (ensure_smem_attr(attr_set, attn_bwd_kernel, kAbSmem) != LIN_OK) return LIN_ERR_CUDA;
