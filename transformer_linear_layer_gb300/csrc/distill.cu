@@ -8,7 +8,7 @@
 //   warp 8      bulk copies into a ring of chunks in shared memory, ahead of the
 //               rows; a row stays in the ring from its statistics to its
 //               gradient, so that it is read from memory once;
-//   warps 9-10  the teacher's entries of the rows to come (two dependent reads of
+//   warps 9-12  the teacher's entries of the rows to come (two dependent reads of
 //               memory that nothing else waits for), and, when a row's gradient is
 //               stored, its loss and its teacher's tokens again.
 // The row's way through warps 0-7 then has one barrier. Every wait is bounded
@@ -22,9 +22,9 @@ constexpr int kDfThreads = 128;   // loss alone
 constexpr int kDfBatch = 8;
 constexpr int kDgThreads = 256;   // gradient: the threads that compute
 constexpr int kDgWarps = kDgThreads / 32;
-constexpr int kDgHelpers = 2;
+constexpr int kDgHelpers = 4;
 constexpr int kDgAll = kDgThreads + 32 + 32 * kDgHelpers;
-constexpr int kDgBatch = 8;       // units of a thread in a chunk, at most
+constexpr int kDgBatch = 5;       // units of a thread in a chunk, at most
 constexpr int kDgRing = 32;       // chunks of the ring, at most
 constexpr int kDgRows = 2 * kDgHelpers;  // rows between their teacher's entries and their loss
 // Shared memory of a block when two share an SM (228 KB, 1 KB of it reserved for each block).
