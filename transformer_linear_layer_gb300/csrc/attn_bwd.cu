@@ -523,86 +523,115 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         }
     } else if (warp == 1) {
         // ---- tcgen05.mma ----
+        // (This thread's own instructions count: its loop is about as long as the
+        // groups'. Stages, phases and the steps left are kept, not computed.)
         if (elect_one()) {
-            AbWalker cur, lead;
-            cur.init(a);
+            AbWalker lead;  // the item of the step whose scores are issued next
             lead.init(a);
-            uint32_t n = 0;
-            bool ok = true;
-            auto issue_s = [&](uint32_t k) {  // S' of step k, the lead's
-                const uint32_t q = smem_u32(sQ + (k % QS) * kAbQStage);
-                ab_mma_scores(tmem + kAbS, smem_u32(sK + (lead.m % KS) * kAbTile), q, smem_u32(sOnes), q + 2 * kAbTile);
+            const uint64_t k_desc = sw128_kmajor_desc(smem_u32(sK)), km_desc = sw128_mnmajor_desc(smem_u32(sK));
+            const uint64_t v_desc = sw128_kmajor_desc(smem_u32(sV));
+            const uint64_t q_desc = sw128_kmajor_desc(smem_u32(sQ)), qm_desc = sw128_mnmajor_desc(smem_u32(sQ));
+            const uint64_t dsk = sw128_kmajor_desc(smem_u32(sDS)), dsm = ab_ds_mn_desc(smem_u32(sDS));
+            const uint64_t ones = ab_flat_desc(smem_u32(sOnes), 128, 0);
+            const uint64_t stat = ab_flat_desc(smem_u32(sQ) + 2 * kAbTile, 0, 128);
+            constexpr uint32_t kTile16 = kAbTile >> 4, kStage16 = kAbQStage >> 4;
+            uint32_t n = 0;                        // step whose gradients are issued
+            uint32_t s_stage = 0, s_phase = 0;     // Q stage of the next scores
+            uint32_t g_stage = 0;                  // and of the gradients
+            uint32_t lead_k = 0, lead_kphase = 0, lead_vphase = 0, cur_k = 0, acc_phase = 1;
+            int lead_left = lead.valid ? a.nb - lead.i0 : 0, cur_left = lead_left, lead_len = lead_left;
+            bool lead_first = true, first = true, ok = true, any = lead_left > 0;
+            auto scores = [&](uint32_t d_tmem, uint64_t ad, uint64_t bd, uint64_t one_rows) {
+#pragma unroll
+                for (int kk = 0; kk < kAbD / 16; ++kk)
+                    tc_mma<true>(d_tmem, ad + 2u * kk, bd + 2u * kk, kIdescS, kk != 0 ? 1u : 0u);
+                tc_mma<true>(d_tmem, one_rows, stat + s_stage * kStage16, kIdescS, 1u);
+            };
+            // the operands of the next scores have landed
+            auto loaded = [&]() {
+                return mbar_wait(qfull + 8 * s_stage, s_phase) && (!lead_first || mbar_wait(kfull + 8 * lead_k, lead_kphase));
+            };
+            auto issue_s = [&]() {
+                scores(tmem + kAbS, k_desc + lead_k * kTile16, q_desc + s_stage * kStage16, ones);
                 tc_commit(sfull);
             };
-            auto issue_dp = [&](uint32_t k) {  // dP' of step k, the lead's
-                const uint32_t q = smem_u32(sQ + (k % QS) * kAbQStage);
-                ab_mma_scores(tmem + kAbDp, smem_u32(sV), q + kAbTile, smem_u32(sOnes) + 256, q + 2 * kAbTile);
+            auto issue_dp = [&]() {  // and on to the next step's scores
+                scores(tmem + kAbDp, v_desc, q_desc + (s_stage * kStage16 + kTile16), ones + 16u);
                 tc_commit(dpfull);
+                lead_first = false;
+                if (++s_stage == QS) {
+                    s_stage = 0;
+                    s_phase ^= 1;
+                }
+                if (--lead_left == 0) {
+                    lead.next_item(a);
+                    lead_len = lead_left = lead.valid ? a.nb - lead.i0 : 0;
+                    lead_first = true;
+                    lead_vphase ^= 1;
+                    if (++lead_k == KS) {
+                        lead_k = 0;
+                        lead_kphase ^= 1;
+                    }
+                }
             };
-            // the operands of step k have landed
-            auto loaded = [&](uint32_t k) {
-                return mbar_wait(qfull + 8 * (k % QS), (k / QS) & 1) &&
-                       (!lead.first() || mbar_wait(kfull + 8 * (lead.m % KS), (lead.m / KS) & 1));
-            };
-            if (cur.valid) {
-                ok = loaded(0) && mbar_wait(vfull, 0);
+            if (any) {
+                ok = loaded() && mbar_wait(vfull, 0);
                 if (ok) {
-                    issue_s(0);
-                    issue_dp(0);
-                    lead.next(a);
+                    issue_s();
+                    issue_dp();
                 }
             }
-            while (ok && cur.valid) {
-                const bool first = cur.first();
+            while (ok && any) {
+                const uint32_t parity = n & 1;
                 // P' of step n is written, S' and dP' are read: S' of the next step,
                 // dV += P' dO, dP' of the next step (whose commit covers dV too)
-                if (*(volatile int*)s_abort != 0 || !mbar_wait(pready, n & 1) || (lead.valid && !loaded(n + 1)) ||
-                    (first && cur.m > 0 && !mbar_wait(accfree, (cur.m - 1) & 1))) {
+                if (!mbar_wait(pready, parity) || (lead_left > 0 && !loaded()) ||
+                    (first && n > 0 && (*(volatile int*)s_abort != 0 || !mbar_wait(accfree, acc_phase)))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (lead.valid) issue_s(n + 1);
-                const uint32_t q = smem_u32(sQ + (n % QS) * kAbQStage);
-                const uint64_t dod = sw128_mnmajor_desc(q + kAbTile);
+                if (lead_left > 0) issue_s();
+                const uint64_t qm = qm_desc + g_stage * kStage16;
 #pragma unroll
                 for (int kk = 0; kk < kAbB / 16; ++kk)
-                    tc_mma_ts(tmem + kAbDv, tmem + kAbP + 8u * kk, dod + 128u * kk, kIdescDkv,
+                    tc_mma_ts(tmem + kAbDv, tmem + kAbP + 8u * kk, qm + kTile16 + 128u * kk, kIdescDkv,
                               (kk != 0 || !first) ? 1u : 0u);
                 // (a new item's V is still on its way here: its dP' comes after dK and dQ)
-                const bool turn = lead.valid && lead.first();
-                if (lead.valid && !turn) {
-                    issue_dp(n + 1);
-                    lead.next(a);
-                }
+                const bool turn = lead_first && lead_left > 0;
+                if (lead_left > 0 && !turn) issue_dp();
                 // dS' of step n is written: dK += dS' Q, dQ = dS K
-                if (!mbar_wait(dsready, n & 1) || (n > 0 && !mbar_wait(dqfree, (n - 1) & 1))) {
+                if (!mbar_wait(dsready, parity) || (n > 0 && !mbar_wait(dqfree, parity ^ 1))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t dsk = sw128_kmajor_desc(smem_u32(sDS)), dsm = ab_ds_mn_desc(smem_u32(sDS));
-                const uint64_t qd = sw128_mnmajor_desc(q);
-                const uint64_t kd = sw128_mnmajor_desc(smem_u32(sK + (cur.m % KS) * kAbTile));
+                const uint64_t km = km_desc + cur_k * kTile16;
 #pragma unroll
                 for (int kk = 0; kk < kAbB / 16; ++kk)
-                    tc_mma<true>(tmem + kAbDk, dsk + 1024u * (kk >> 2) + 2u * (kk & 3), qd + 128u * kk, kIdescDkv,
+                    tc_mma<true>(tmem + kAbDk, dsk + 1024u * (kk >> 2) + 2u * (kk & 3), qm + 128u * kk, kIdescDkv,
                                  (kk != 0 || !first) ? 1u : 0u);
 #pragma unroll
                 for (int kk = 0; kk < kAbB / 16; ++kk)
-                    tc_mma<true>(tmem + kAbDq, dsm + 128u * kk, kd + 128u * kk, kIdescDq, kk != 0 ? 1u : 0u);
+                    tc_mma<true>(tmem + kAbDq, dsm + 128u * kk, km + 128u * kk, kIdescDq, kk != 0 ? 1u : 0u);
                 tc_commit(done);
+                ++n;
                 if (turn) {
-                    if (!mbar_wait(vfull, lead.m & 1)) {
+                    if (!mbar_wait(vfull, lead_vphase)) {
                         ok = false;
-                        ++n;
                         break;
                     }
-                    issue_dp(n + 1);
-                    lead.next(a);
+                    cur_left = lead_len + 1;  // (the item that follows)
+                    issue_dp();
                 }
-                cur.next(a);
-                ++n;
+                if (++g_stage == QS) g_stage = 0;
+                first = false;
+                if (--cur_left == 0) break;
+                if (turn) {
+                    first = true;
+                    acc_phase ^= 1;
+                    if (++cur_k == KS) cur_k = 0;
+                }
             }
             if (!ok) {
                 give_up();
@@ -964,13 +993,13 @@ __global__ void __launch_bounds__(256) attn_bwd_prep(const uint16_t* out, const 
 
 // dq of 128 queries of one head: the chains' fp32 sums added in order, scaled,
 // rounded once. A thread has 16 columns of a row.
-__global__ void __launch_bounds__(512) attn_bwd_dq(const float* dq, uint16_t* dqkv, int T, int H, int nb, int bh0,
+__global__ void __launch_bounds__(kAbB) attn_bwd_dq(const float* dq, uint16_t* dqkv, int T, int H, int nb, int bh0,
                                                    int chains, int causal, float scale) {
     pdl_wait();
     pdl_launch_dependents();
-    const int local = blockIdx.x / nb, i = blockIdx.x % nb;
+    const int part = blockIdx.x & 3, tile = blockIdx.x >> 2, local = tile / nb, i = tile % nb;
     const int bh = bh0 + local, b = bh / H, h = bh % H;
-    const int row = threadIdx.x & 127, part = threadIdx.x >> 7;
+    const int row = threadIdx.x;
     const int t = i * kAbB + row;
     if (t >= T) return;
     const int used = min(chains, causal ? i + 1 : nb);
@@ -1119,8 +1148,8 @@ int launch_attention_backward(const AttnBwdProblem& p) {
         cfg.blockDim = dim3(kAbThreads);
         cfg.dynamicSmemBytes = kAbSmem;
         if (cudaLaunchKernelEx(&cfg, attn_bwd_kernel, tq, tdo, tdq, a) != cudaSuccess) return LIN_ERR_CUDA;
-        cfg.gridDim = dim3((unsigned)a.items);
-        cfg.blockDim = dim3(512);
+        cfg.gridDim = dim3((unsigned)a.items * 4u);
+        cfg.blockDim = dim3(kAbB);
         cfg.dynamicSmemBytes = 0;
         if (cudaLaunchKernelEx(&cfg, attn_bwd_dq, static_cast<const float*>(a.dq), static_cast<uint16_t*>(p.dqkv), p.T,
                                p.H, nb, a.bh0, a.chains, a.causal, a.scale) != cudaSuccess)
