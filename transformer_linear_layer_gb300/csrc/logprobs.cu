@@ -6,6 +6,11 @@
 // A row is read once, straight into registers; many small blocks an SM keep
 // enough loads in flight (see logits.cuh). The top selection looks again only at
 // the few threads that can hold one of the top values.
+//
+// Measured (GB300): 8192 x 50257 bf16 without a top 150 us (5.5 TB/s), top 8 180 us;
+// 301 x 128001 fp32, top 32, 53 us; one row of 50257, top 20, 11 us. The large case
+// is bound by issue slots (packed fp32 arithmetic, one exponential a value), the
+// others by latency.
 #include "logits.cuh"
 
 namespace lin {
