@@ -55,8 +55,10 @@
 //
 // Measured (GB300): 64 sequences of 128, 12 heads, causal 29 us (3.5 TB/s of
 // operands); 2 of 4096 211 us (610 TF/s of the visible pairs' products), of which
-// attn_bwd_kernel 178; a step takes 2700 cycles when nothing waits, 1660 of them
-// products.
+// attn_bwd_kernel about 180 (profiled alone); a step takes 2700 cycles when nothing
+// waits, 1660 of them products. Tensor pipe 36 % active, DRAM 6 %: bound by the
+// steps' chain of products, exponentials and additions. T <= 128: DRAM 28 %, tensor
+// pipe 15 %: bound by the latency of a block's own chain, two blocks an SM.
 #include <math.h>
 
 #include <algorithm>
@@ -358,9 +360,9 @@ __device__ __forceinline__ void ab_mma_scores(uint32_t d_tmem, uint32_t a, uint3
 // by head; their lengths fall along the walk when causal. With every other round in
 // reverse (`snake`) the sums of the lengths stay close, but an item may follow one of
 // its chain that starts after it: taken where there are chains for at least half of
-// a head's blocks that run together, when causal (24 heads of 4096 causal, 2 chains: 124 steps of
-// the longest block against 109 in plain rounds; 96 heads of 1024, 2 chains: 33
-// against 36).
+// a head's blocks that run together, when causal (24 heads of 4096 causal,
+// 2 chains: 256 us, 217 in plain rounds; 192 of 4096: 1836 and 1565; 96 of 1024,
+// 2 chains: 86 and 90).
 struct AbWalker {
     int round, m;        // round, items so far
     int j, bh;           // key block, launch-local (sequence, head)

@@ -14,9 +14,11 @@
 // The row's way through warps 0-7 then has one barrier. Every wait is bounded
 // (about 1 s); a block that gives up sets the device status word.
 //
-// Measured (GB300, 8192 x 50257 bf16, 32 entries): loss 137 us (6.0 TB/s), loss and
-// gradient 344 us (4.8 TB/s), gradient 284 us. Both are bound by issue slots, not
-// by memory: a value takes one or two exponentials and about ten instructions.
+// Measured (GB300, 8192 x 50257 bf16, 32 entries): loss 138 us (6.0 TB/s), loss and
+// gradient 344 us (4.8 TB/s), gradient 293 us (5.6 TB/s). Of 2048 rows the gradient
+// kernel issues in 47 % of the cycles (58 % with the loss) with DRAM at 60 % (47 %)
+// of its nominal rate: neither is full. Its warps wait, for memory and for the
+// instruction before, and the rows in shared memory leave room for 26 of them an SM.
 #include "logits.cuh"
 
 namespace lin {
@@ -26,10 +28,12 @@ constexpr int kDfThreads = 128;   // loss alone
 constexpr int kDfBatch = 8;
 constexpr int kDgThreads = 256;   // gradient: the threads that compute
 constexpr int kDgWarps = kDgThreads / 32;
-constexpr int kDgHelpers = 4;     // (32768 x 8000 bf16, gradient: 283 us with 2, 196 with 4)
+constexpr int kDgHelpers = 4;     // (32768 x 8000 bf16, gradient: 283 us with 2, 200 with 4; loss and gradient of
+                                  // 8192 x 50257 348 and 354)
 constexpr int kDgAll = kDgThreads + 32 + 32 * kDgHelpers;
 // Units of a thread in a chunk, at most: a row of 50257 bf16 is five chunks of five
-// (344 us; 377 with 8, 389 with 4, where the chunks do not divide it).
+// (loss and gradient of 8192 rows 354 us back to back, 393 with 8, 399 with 4; 4 is
+// ahead at other widths: 32768 x 8000 314 against 329, 2000 x 128001 297 against 312).
 constexpr int kDgBatch = 5;
 constexpr int kDgRing = 32;       // chunks of the ring, at most
 constexpr int kDgRows = 2 * kDgHelpers;  // rows between their teacher's entries and their loss

@@ -1,8 +1,8 @@
 // Shared pieces of the operators on the LM head's logits (R rows of V values,
 // rows ld apart): token log probabilities and distillation.
 //
-// All of them are bound by memory: a row is read once (and its gradient
-// written once), and what is kept of it is a running maximum m and the sum
+// Their floor is memory's: a row is read once (and its gradient written once),
+// and what is kept of it is a running maximum m and the sum
 // s = sum exp((z - m) / tau) of a softmax. The differences z - m are formed
 // before they are scaled, so that neither an offset common to a row nor a mask of
 // the type's lowest value costs accuracy; maximum, sums and statistics are fp32.

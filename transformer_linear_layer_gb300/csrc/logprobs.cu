@@ -8,9 +8,10 @@
 // the few threads that can hold one of the top values.
 //
 // Measured (GB300): 8192 x 50257 bf16 without a top 150 us (5.5 TB/s), top 8 180 us;
-// 301 x 128001 fp32, top 32, 53 us; one row of 50257, top 20, 11 us. The large case
-// is bound by issue slots (packed fp32 arithmetic, one exponential a value), the
-// others by latency.
+// 301 x 128001 fp32, top 32, 53 us; one row of 50257, top 20, 11 us. 2048 rows
+// of the first issue in 63 % of the cycles with DRAM at 51 % (45 % with the top) of
+// its nominal rate: neither is full, the warps wait for memory and for the
+// instruction before. The small cases are bound by latency.
 #include "logits.cuh"
 
 namespace lin {
@@ -21,7 +22,8 @@ constexpr int kLpWarps = kLpThreads / 32;
 // Units a thread loads before it uses the first, and blocks an SM. fp32 units hold
 // half the elements, so more of them have to be on their way for the same time
 // (2048 x 50257 fp32, top 8: 82 us, with 4 and 10 96 us); bf16 has more to compute
-// and gains from more warps (8192 x 50257 bf16, top 8: 178 us, with 8 and 8 196 us).
+// and gains from more warps (8192 x 50257 bf16, top 8: 178 us, with 8 and 8 196 us;
+// without a top 156 and 150 in that run).
 constexpr int lp_batch(bool bf16) { return bf16 ? 4 : 8; }
 constexpr int lp_blocks(bool bf16) { return bf16 ? 10 : 8; }
 constexpr int kLpFolds = 16;   // maxima kept of a thread's batches (batch n in place n % 16)
