@@ -31,10 +31,10 @@
 // Longer ones: three kernels:
 //   attn_bwd_prep    delta and lse, a row of eight bf16 a query, padded to whole
 //                    blocks of 128 queries.
-//   attn_bwd_kernel  a persistent block per SM walks work items (sequence, head,
-//                    block of 128 keys); an item walks the query blocks that see
-//                    its keys, with dk and dv accumulating in TMEM. dq is summed
-//                    over the key blocks in fp32 in the workspace.
+//   attn_bwd_kernel  a persistent block per SM draws work items (sequence, head,
+//                    block of 128 keys) by a ticket; an item walks the query blocks
+//                    that see its keys, with dk and dv accumulating in TMEM. dq is
+//                    summed over the key blocks in fp32 in the workspace.
 //   attn_bwd_dq      the fp32 sums to bf16.
 //
 // attn_bwd_kernel's warps: 0 TMA; 1 tcgen05.mma issuer; 2 and 3 send what is staged
@@ -47,9 +47,9 @@
 // Order of the dq sums: the key blocks of a head form `chains` chains (block j in
 // chain j % chains), each with its own fp32 copy of dq; within a chain block j
 // adds to a tile after block j - chains has (a counter per tile, waited for). The
-// sums' order is thus fixed, results are repeatable bit for bit, and a wait is
-// only ever for an item that comes earlier in the walk. A tile is added by one bulk
-// reduction from shared memory, whose completion is looked for a step later.
+// sums' order is thus fixed, results are repeatable bit for bit whichever block has an
+// item, and a wait is only ever for an item that was drawn earlier, by a block that
+// runs. A tile is added by one bulk reduction from shared memory, whose completion is looked for a step later.
 // Every wait is bounded (about 1 s); a block that gives up sets the device status
 // word.
 //
@@ -79,11 +79,12 @@ constexpr uint32_t kAbStat = kAbB * 16;            // eight bf16 of 128 queries:
 constexpr uint32_t kAbOnes = 512;                  // the rows that meet them
 constexpr int kAbKStages = 2, kAbQStages = 3;      // (V has one)
 constexpr uint32_t kAbQStage = 2 * kAbTile + kAbStat;
+constexpr int kAbItems = 4;                        // work items between the ticket and the last role that takes them
 constexpr uint32_t kAbDs = kAbB * kAbB * 2;        // dS': two 64-query K-major blocks of 16 KiB
 constexpr uint32_t kAbDqTile = kAbB * kAbD * 4;    // fp32 dq of a query block: [column / 4][row][4]
-constexpr int kAbBars = 2 * kAbKStages + 2 + 2 * kAbQStages + 10;
-constexpr size_t kAbSmem =
-    1024 + (kAbKStages + 1) * kAbTile + kAbQStages * kAbQStage + kAbDs + kAbDqTile + kAbOnes + kAbBars * 8 + 16;
+constexpr int kAbBars = 2 * kAbKStages + 2 + 2 * kAbQStages + 10 + 2 * kAbItems;
+constexpr size_t kAbSmem = 1024 + (kAbKStages + 1) * kAbTile + kAbQStages * kAbQStage + kAbDs + kAbDqTile + kAbOnes +
+                           kAbBars * 8 + kAbItems * 8 + 16;
 static_assert(kAbSmem <= 227 * 1024, "shared memory");
 // TMEM columns
 constexpr uint32_t kAbS = 0, kAbDp = 128, kAbDv = 256, kAbDk = 320, kAbDq = 384, kAbP = 448, kAbTmem = 512;
@@ -105,8 +106,9 @@ struct AbArgs {
     int items;           // heads * nb
     int chains;
     int ahead;           // blocks that run at once (short kernel)
-    int causal, snake;
+    int causal;
     float scale, scale_log2, inv_scale;
+    unsigned* ticket;    // the next item, counted by the blocks that run
     const uint4* stats;  // heads x nb x 128
     unsigned* flags;     // heads x chains x nb
     float* dq;           // heads x chains x nb tiles
@@ -356,41 +358,24 @@ __device__ __forceinline__ void ab_mma_scores(uint32_t d_tmem, uint32_t a, uint3
     tc_mma<true>(d_tmem, ab_flat_desc(ones, 128, 0), ab_flat_desc(stat, 0, 128), kIdescS, 1u);
 }
 
-// The block's items: rounds of gridDim.x items. Items are ordered by key block, then
-// by head; their lengths fall along the walk when causal. With every other round in
-// reverse (`snake`) the sums of the lengths stay close, but an item may follow one of
-// its chain that starts after it: taken where there are chains for at least half of
-// a head's blocks that run together, when causal (24 heads of 4096 causal,
-// 2 chains: 256 us, 217 in plain rounds; 192 of 4096: 1836 and 1565; 96 of 1024,
-// 2 chains: 86 and 90).
+// A role's place in the block's items. The TMA warp draws them by a ticket and passes
+// them on through a ring in shared memory. Items are ordered by key block, then by head
+// (their lengths fall along the order when causal), and only a block that runs draws
+// one. So an item whose sums another one waits for has started and goes on, whichever
+// blocks are resident: with the items dealt out by block index, a block that another
+// stream's kernel keeps off its SM held up all the others.
 struct AbWalker {
-    int round, m;        // round, items so far
+    int m = -1;          // number of the item within the block
     int j, bh;           // key block, launch-local (sequence, head)
     int i, i0;           // query block, the item's first
-    bool valid;
-    __device__ __forceinline__ void place(const AbArgs& a) {
-        const int c = blockIdx.x, g = gridDim.x;
-        const long long idx = (long long)round * g + (a.snake && (round & 1) ? g - 1 - c : c);
-        valid = idx < a.items;
-        j = valid ? (int)(idx / a.heads) : 0;
-        bh = valid ? (int)(idx % a.heads) : 0;
+    bool valid = false;  // false past the last item
+    __device__ __forceinline__ void set(const AbArgs& a, int2 x) {
+        j = x.x;
+        bh = x.y;
+        valid = j >= 0;
         i = i0 = a.causal ? j : 0;
     }
-    __device__ __forceinline__ void init(const AbArgs& a) {
-        round = m = 0;
-        place(a);
-    }
-    __device__ __forceinline__ bool first() const { return i == i0; }
     __device__ __forceinline__ bool last(const AbArgs& a) const { return i == a.nb - 1; }
-    __device__ __forceinline__ void next(const AbArgs& a) {
-        if (++i < a.nb) return;
-        next_item(a);
-    }
-    __device__ __forceinline__ void next_item(const AbArgs& a) {
-        ++round;
-        ++m;
-        place(a);
-    }
 };
 
 __global__ void __launch_bounds__(kAbThreads, 1)
@@ -406,18 +391,20 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
     uint8_t* sOut = sDS + kAbDs;               // dq on its way out; dk and dv at an item's end
     uint8_t* sOnes = sOut + kAbDqTile;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sOnes + kAbOnes);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kAbBars);
+    int2* items = reinterpret_cast<int2*>(bars + kAbBars);  // key block (-1: no more) and head
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + kAbItems);
     int* s_abort = reinterpret_cast<int*>(tmem_slot + 1);
 
     // Full / empty of the stages; then, once a step: sfull, dpfull, done (the
     // products of S', of dV and dP', of dK and dQ), pready, dsready (the groups'
     // warps), dqfree, accfree (the four); outfull (the four; of even and of odd
-    // messages), outfree (a sender) once a message.
+    // messages), outfree (a sender) once a message; full / empty of the items' ring.
     const uint32_t kfull = smem_u32(bars), kempty = kfull + 8 * KS, vfull = kempty + 8 * KS, vempty = vfull + 8,
                    qfull = vempty + 8, qempty = qfull + 8 * QS, one_a_step = qempty + 8 * QS;
     const uint32_t sfull = one_a_step, dpfull = one_a_step + 8, done = one_a_step + 16, pready = one_a_step + 24,
                    dsready = one_a_step + 32, dqfree = one_a_step + 40, accfree = one_a_step + 48,
-                   outfull = one_a_step + 56, outfree = one_a_step + 72;
+                   outfull = one_a_step + 56, outfree = one_a_step + 72, ifull = outfree + 8,
+                   iempty = ifull + 8 * kAbItems;
 
     // (the same in every lane, and known to be: roles branch without divergence)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -442,6 +429,10 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         mbar_init(outfull, 4);
         mbar_init(outfull + 8, 4);
         mbar_init(outfree, 1);
+        for (int k = 0; k < kAbItems; ++k) {
+            mbar_init(ifull + 8 * k, 1);
+            mbar_init(iempty + 8 * k, 1 + 2 + 4 * kAbGroups + 4);  // issuer, senders, the groups' and the last warps
+        }
         *s_abort = 0;
         mbar_fence_init();
         tma_prefetch_map(&tmQkv);
@@ -468,15 +459,45 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
+    // The next item, by a whole warp and by one thread; false when the wait has run out.
+    auto take = [&](AbWalker& w) {
+        const uint32_t k = ++w.m % kAbItems;
+        if (!wait(ifull + 8 * k, (w.m / kAbItems) & 1)) return false;
+        w.set(a, items[k]);
+        arrive(iempty + 8 * k);
+        return true;
+    };
+    auto take_alone = [&](AbWalker& w) {
+        const uint32_t k = ++w.m % kAbItems;
+        if (!mbar_wait(ifull + 8 * k, (w.m / kAbItems) & 1)) return false;
+        w.set(a, items[k]);
+        mbar_arrive(iempty + 8 * k);
+        return true;
+    };
 
     if (warp < 4) regs_dec<kAbRegsIssue>();
     if (warp == 0) {
         // ---- TMA ----
-        pdl_wait();  // the statistics are the previous kernel's output
+        pdl_wait();  // the statistics and the ticket are the previous kernel's output
         uint32_t m = 0, n = 0;
         bool ok = true;
-        AbWalker w;
-        for (w.init(a); ok && w.valid; w.next_item(a), ++m) {
+        for (;; ++m) {
+            unsigned drawn = 0;
+            if (lane == 0) drawn = atomicAdd(a.ticket, 1u);
+            const unsigned idx = __shfl_sync(0xffffffffu, drawn, 0);
+            AbWalker w;
+            const bool more = idx < (unsigned)a.items;
+            w.set(a, more ? make_int2((int)(idx / a.heads), (int)(idx % a.heads)) : make_int2(-1, 0));
+            const uint32_t is = m % kAbItems;
+            if (aborted() || !wait(iempty + 8 * is, ((m / kAbItems) & 1) ^ 1)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                items[is] = make_int2(w.j, w.bh);
+                mbar_arrive(ifull + 8 * is);
+            }
+            if (!more) break;
             const int bh = a.bh0 + w.bh, b = bh / a.H, h = bh % a.H;
             const uint32_t ks = m % KS;
             if (aborted() || !wait(kempty + 8 * ks, ((m / KS) & 1) ^ 1)) {
@@ -534,7 +555,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         // groups'. Stages, phases and the steps left are kept, not computed.)
         if (elect_one()) {
             AbWalker lead;  // the item of the step whose scores are issued next
-            lead.init(a);
+            bool ok = take_alone(lead);
             const uint64_t k_desc = sw128_kmajor_desc(smem_u32(sK)), km_desc = sw128_mnmajor_desc(smem_u32(sK));
             const uint64_t v_desc = sw128_kmajor_desc(smem_u32(sV));
             const uint64_t q_desc = sw128_kmajor_desc(smem_u32(sQ)), qm_desc = sw128_mnmajor_desc(smem_u32(sQ));
@@ -547,7 +568,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
             uint32_t g_stage = 0;                  // and of the gradients
             uint32_t lead_k = 0, lead_kphase = 0, lead_vphase = 0, cur_k = 0, acc_phase = 1;
             int lead_left = lead.valid ? a.nb - lead.i0 : 0, cur_left = lead_left, lead_len = lead_left;
-            bool lead_first = true, first = true, ok = true, any = lead_left > 0;
+            bool lead_first = true, first = true, any = lead_left > 0;
             auto scores = [&](uint32_t d_tmem, uint64_t ad, uint64_t bd, uint64_t one_rows) {
 #pragma unroll
                 for (int kk = 0; kk < kAbD / 16; ++kk)
@@ -571,8 +592,8 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
                     s_phase ^= 1;
                 }
                 if (--lead_left == 0) {
-                    lead.next_item(a);
-                    lead_len = lead_left = lead.valid ? a.nb - lead.i0 : 0;
+                    ok = take_alone(lead);
+                    lead_len = lead_left = ok && lead.valid ? a.nb - lead.i0 : 0;
                     lead_first = true;
                     lead_vphase ^= 1;
                     if (++lead_k == KS) {
@@ -608,7 +629,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
                 const bool turn = lead_first && lead_left > 0;
                 if (lead_left > 0 && !turn) issue_dp();
                 // dS' of step n is written: dK += dS' Q, dQ = dS K
-                if (!mbar_wait(dsready, parity) || (n > 0 && !mbar_wait(dqfree, parity ^ 1))) {
+                if (!ok || !mbar_wait(dsready, parity) || (n > 0 && !mbar_wait(dqfree, parity ^ 1))) {
                     ok = false;
                     break;
                 }
@@ -630,6 +651,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
                     }
                     cur_left = lead_len + 1;  // (the item that follows)
                     issue_dp();
+                    if (!ok) break;
                 }
                 if (++g_stage == QS) g_stage = 0;
                 first = false;
@@ -655,9 +677,9 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         pdl_wait();
         if (elect_one()) {
             uint32_t msg = 0;
-            bool ok = true;
             AbWalker w;
-            for (w.init(a); ok && w.valid; w.next(a)) {
+            bool ok = take_alone(w);
+            for (; ok && w.valid; ok = ++w.i < a.nb || take_alone(w)) {
                 const int bh = a.bh0 + w.bh, b = bh / a.H, h = bh % a.H;
                 if (w.last(a) && (msg++ & 1) == (uint32_t)(warp & 1)) {
                     // dk and dv; tokens past T lie outside the map and are not written
@@ -721,9 +743,9 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         uint8_t* ds_row = sDS + (grp >> 1) * (kAbDs / 2) + r * 128;
         const uint64_t sl2 = ab_pack(a.scale_log2, a.scale_log2);
         uint32_t n = 0;
-        bool ok = true;
         AbWalker w;
-        for (w.init(a); w.valid; w.next(a), ++n) {
+        bool ok = take(w);
+        for (; ok && w.valid; ok = ++w.i < a.nb || take(w), ++n) {
             const bool diag = a.causal && w.i == w.j;
             const bool masked = diag || (w.j + 1) * kAbB > a.T;
             // query c of this group is visible to the thread's key from `from` on
@@ -765,9 +787,9 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         const int r = 32 * quad + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
         uint32_t n = 0, msg = 0;
-        bool ok = true;
         AbWalker w;
-        for (w.init(a); w.valid; w.next(a), ++n) {
+        bool ok = take(w);
+        for (; ok && w.valid; ok = ++w.i < a.nb || take(w), ++n) {
             const bool last = w.last(a);
             ok = wait(done, n & 1) && (msg == 0 || wait(outfree, (msg - 1) & 1));
             if (!ok) break;
@@ -986,16 +1008,17 @@ attn_bwd_short_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_co
     }
 }
 
-// The statistics of every query block, and its dq counters zeroed.
+// The statistics of every query block; its dq counters and the ticket zeroed.
 __global__ void __launch_bounds__(256) attn_bwd_prep(const uint16_t* out, const uint16_t* dout, const float* lse, int T,
                                                      int H, int nb, int bh0, int chains, float inv_scale,
-                                                     uint4* stats, unsigned* flags) {
+                                                     uint4* stats, unsigned* flags, unsigned* ticket) {
     pdl_wait();
     pdl_launch_dependents();
     const int local = blockIdx.x / nb, i = blockIdx.x % nb;
     const int bh = bh0 + local;
     ab_stats(out, dout, lse, T, H, bh / H, bh % H, i, inv_scale, stats + (size_t)blockIdx.x * kAbB);
     for (int g = threadIdx.x; g < chains; g += 256) flags[((size_t)local * chains + g) * nb + i] = 0u;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0u;
 }
 
 // dq of 128 queries of one head: the chains' fp32 sums added in order, scaled,
@@ -1110,8 +1133,9 @@ int launch_attention_backward(const AttnBwdProblem& p) {
         return cudaGetLastError() == cudaSuccess ? LIN_OK : LIN_ERR_CUDA;
     }
 
-    // Workspace after the counter block: statistics, counters, dq sums. Heads go
-    // in as many launches as it takes.
+    // Workspace after the counter block: ticket, statistics, counters, dq sums (a
+    // kilobyte stands for the first and for alignment). Heads go in as many launches
+    // as it takes.
     const size_t avail = p.workspace_bytes > kCounterBytes + 1024 ? p.workspace_bytes - kCounterBytes - 1024 : 0;
     const size_t stat = (size_t)nb * kAbStat;
     const size_t chain = (size_t)nb * (kAbDqTile + sizeof(unsigned));
@@ -1122,7 +1146,6 @@ int launch_attention_backward(const AttnBwdProblem& p) {
     const long long together = (p.sm_count + heads - 1) / heads;
     const long long room = (long long)((avail / heads - stat) / chain);
     a.chains = (int)std::max(1ll, std::min({together, room, (long long)nb}));
-    a.snake = p.causal && 2 * a.chains >= std::min(together, (long long)nb);
 
     static std::atomic<unsigned long long> attr_set{0};
     if (ensure_smem_attr(attr_set, attn_bwd_kernel, kAbSmem) != LIN_OK) return LIN_ERR_CUDA;
@@ -1133,7 +1156,8 @@ int launch_attention_backward(const AttnBwdProblem& p) {
         return cudaFuncGetAttributes(&fa, attn_bwd_kernel) == cudaSuccess ? fa.numRegs : 0;
     }();
     if (regs < kAbLaunchRegs) return LIN_ERR_UNSUPPORTED;
-    char* ws = static_cast<char*>(p.workspace) + kCounterBytes;
+    a.ticket = reinterpret_cast<unsigned*>(static_cast<char*>(p.workspace) + kCounterBytes);
+    char* ws = static_cast<char*>(p.workspace) + kCounterBytes + 256;
     for (long long bh0 = 0; bh0 < bh_all; bh0 += heads) {
         const int count = (int)std::min(heads, bh_all - bh0);
         a.bh0 = (int)bh0;
@@ -1148,7 +1172,7 @@ int launch_attention_backward(const AttnBwdProblem& p) {
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;
         if (cudaLaunchKernelEx(&cfg, attn_bwd_prep, out, dout, p.lse, p.T, p.H, nb, a.bh0, a.chains,
-                               a.inv_scale, stats, a.flags) !=
+                               a.inv_scale, stats, a.flags, a.ticket) !=
             cudaSuccess)
             return LIN_ERR_CUDA;
         cfg.gridDim = dim3((unsigned)std::min(a.items, p.sm_count));
