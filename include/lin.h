@@ -546,8 +546,12 @@ LIN_API int lin_distill_forward(lin_ctx* ctx, int R, int V, int K, const void* l
                                 float* loss, float* lse, void* stream);
 
 /* dlogits (R rows of V, ldd apart, in the logits' type, one rounding) from the
- * forward's lse and grad_loss (R fp32: g). dlogits may be the logits
- * themselves (in place, with ldd == ld). Fast when dlogits and logits start
+ * forward's lse of the same logits and tau, and grad_loss (R fp32: g). Where
+ * |lse| is at most 512 (bf16 logits) or 64 (fp32), p = exp(z / tau - lse): the
+ * rounding of lse moves the row's p by up to 2^-23 |lse| relative, 2^-14 and
+ * 2^-17 at most. Past that lse has lost the digits that p needs, and the row's
+ * maximum and sum are computed again, at the cost of another read of the row.
+ * dlogits may be the logits themselves (in place, with ldd == ld). Fast when dlogits and logits start
  * at the same offset within 16 bytes and (ld - ldd) * element size is a
  * multiple of 16; right for any. */
 LIN_API int lin_distill_backward(lin_ctx* ctx, int R, int V, int K, const void* logits, long long ld, int logits_type,

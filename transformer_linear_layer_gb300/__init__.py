@@ -741,8 +741,11 @@ def distill_forward(logits, ids, teacher, temperature: float = 1.0, ctx: Context
 
 def distill_backward(logits, ids, teacher, lse, grad_loss, temperature: float = 1.0, out=None,
                      ctx: Context | None = None, stream=None):
-    """The logits' gradient, from :func:`distill_forward`'s lse and the
-    gradient of each row's loss (R fp32). ``out`` may be ``logits``."""
+    """The logits' gradient, from :func:`distill_forward`'s lse (of the same
+    logits and temperature) and the gradient of each row's loss (R fp32).
+    ``out`` may be ``logits``. Rows whose lse is too large to carry the
+    probabilities' digits (above 512 for bf16 logits, 64 for fp32) are summed
+    again."""
     args = _distill_args(logits, ids, teacher, lse, grad_loss)
     out, ldd = _dlogits(logits, out, args)
     dev = logits.device.index if logits.device.index is not None else 0

@@ -286,7 +286,7 @@ struct Slice {
     }
 };
 
-// Statistics of the whole row in every computing thread of the cluster.
+// Statistics of the whole row in every computing thread of the cluster; `seq` counts the calls.
 template <bool BF16, int CL>
 __device__ __forceinline__ Stats dg_row_stats(const Slice<BF16, CL>& sl, Stats st, float c, uint32_t seq) {
     DgShared& sh = sl.sh;
@@ -341,6 +341,16 @@ template <bool BF16>
 __device__ __forceinline__ char* dg_row(const DistillArgs& a, long long r, const Row<BF16>& row) {
     return static_cast<char*>(a.dz) + (r * a.ldd - row.off) * Row<BF16>::SZ;
 }
+
+// The largest |lse| from which the gradient alone takes p = exp(z / tau - lse). A given
+// lse is right to half a step of fp32, and its product with tau to another: 2^-23 |lse|
+// relative on every p of the row, which is 1/64 of a bf16 half step (2^-8) at 512 and
+// 128 roundings of fp32 at 64. Past it (logits that lie far from zero, a mask of the
+// type's lowest value on all of them) lse has lost the digits that p needs, and the
+// row's maximum and sum are computed again (7959 rows of 50257 bf16, all of them past
+// it: 440 us against 288).
+template <bool BF16>
+constexpr float dg_lse_limit() { return BF16 ? 512.f : 64.f; }
 
 // FORWARD: the statistics (and the loss) are computed; else lse is given.
 template <bool BF16, bool FORWARD, int CL>
@@ -425,7 +435,7 @@ __global__ void __launch_bounds__(kDgAll, 2) distill_grad_kernel(const DistillAr
             now = next;
         }
     } else {
-        uint32_t seq = 0;
+        uint32_t seq = 0, renewed = 0;  // rows; those whose statistics are computed although lse is given
         for (long long r = r0; r < g.rows; r += step, ++seq) {
             const Row<BF16> row(a.z, r, a.ld, a.V);
             const int u0 = sl.begin(row), u1 = sl.end(row), b = seq % kDgRows;
@@ -450,8 +460,22 @@ __global__ void __launch_bounds__(kDgAll, 2) distill_grad_kernel(const DistillAr
                 logs = log2f(st.s);
                 inv_s = 1.0f / st.s;
             } else {
-                base = a.lse_in[r] * a.tau;
+                const float lse = a.lse_in[r];
+                base = lse * a.tau;
                 sl.wait(sh.teacher[b], (seq / kDgRows) & 1);
+                if (!(fabsf(lse) <= dg_lse_limit<BF16>())) {
+                    Stats st{-INFINITY, 0.f, 0.f, 0u};
+                    for (int c0 = u0; c0 < u1; c0 += g.chunk) {
+                        const int c1 = min(c0 + g.chunk, u1);
+                        uint4 raw[kDgBatch];
+                        sl.units(row, 0, c0, c1, raw, true);
+                        lg_accumulate<BF16, false>(st, raw, sl.count(c0, c1), a.c);
+                    }
+                    st = dg_row_stats<BF16, CL>(sl, st, a.c, renewed++);
+                    base = lg_base(st.m);
+                    logs = log2f(st.s);
+                    inv_s = 1.0f / st.s;
+                }
             }
             const float w = sh.weight[b], coef = w * inv_s;
             const uint32_t keep = w == 0.f ? 0u : ~0u;
