@@ -153,3 +153,34 @@ def test_clusters_with_rows_far_from_zero(dtype, R, V):
     z, ids, t, w = make(R, V, 8, dtype, seed=4)
     far(z, [0.0, -3e5, 0.0, "lowest", 1e4])
     check_all(z, ids, t, w, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("R,V", [(30, 777), (3, 50257)])
+@pytest.mark.parametrize("tau", [1.0, 0.3, 2.0])
+def test_loss_where_the_student_masks_a_teachers_token(R, V, dtype, tau):
+    """A mask of the type's lowest value costs its finite amount (inf only where the
+    loss itself passes fp32), one of -inf costs inf."""
+    tau = float(torch.tensor(tau, dtype=torch.float32))
+    z, ids, t, _ = make(R, V, 6, dtype, seed=9)
+    ids[:] = torch.arange(6, device="cuda") * (V // 7)
+    t[:] = torch.tensor([4.0, 1.0, 0.0, -2.0, 3.0, 2.0], device="cuda")
+    low = torch.finfo(dtype).min
+    z[:, ids[0, 2]] = low
+    z[1::3, ids[0, 3]] = low
+    z[2::3, ids[0, 1]] = -INF
+    d = z.double() / tau
+    d = d - d.amax(1, keepdim=True)
+    logp = (d - torch.log(torch.exp(d).sum(1, keepdim=True))).gather(1, ids)
+    logq = torch.log_softmax(t.double() / tau, 1)
+    loss = (tau * tau * (logq.exp() * (logq - logp)).sum(1)).float()  # (past fp32: inf)
+    rel = 2 * ref.sum_error(V) + 64 * ref.FP32_HALF
+    got, _ = tll.distill_forward(z, ids, t, temperature=tau)
+    both, dz = tll.distill_forward_backward(z, ids, t, temperature=tau)
+    assert torch.equal(got.isinf(), loss.isinf()) and bool(loss[2::3].isinf().all())
+    if tau <= 1:
+        assert bool(loss[::3].isfinite().all())
+    fine = loss.isfinite()
+    assert bool(((got - loss).abs() <= rel * loss.abs())[fine].all())
+    assert bool(((both - loss).abs() <= rel * loss.abs())[fine].all()) and torch.equal(both.isinf(), loss.isinf())
+    assert bool(dz.isfinite().all())

@@ -106,20 +106,24 @@ __device__ __forceinline__ TeacherSums lg_teacher(const DistillArgs& a, long lon
     return {m, sum, __any_sync(0xffffffffu, over) != 0};
 }
 
-// One warp: the loss from the row's statistics (p = 2^((z - base) c - logs)).
+// One warp: the loss from the row's statistics (p = 2^((z - base) c - logs)). With the
+// temperature drawn out of the logarithms, tau^2 (log q - log p) is tau times
+// (t - top) - (z - base) + tau ln 2 (logs - logt), where t and z are in their own units:
+// a teacher's token that the student masks with the type's lowest value then costs what
+// it costs, and does not overflow on the way.
 __device__ __forceinline__ float lg_loss(const DistillArgs& a, Teacher te, const TeacherSums& s, float base,
                                          float logs) {
     float part = 0.f;
-    const float logt = log2f(s.sum);
+    const float rest = a.tau * kLn2 * (logs - log2f(s.sum));
     for (int i = threadIdx.x & 31; i < a.K; i += 32) {
         if (te.id[i] < 0 || s.sum == 0.f) continue;
-        const float lq = (te.t[i] - s.top) * a.c;
-        const float q = exp2f(lq) / s.sum;
-        if (q != 0.f) part += q * ((lq - logt) - ((te.z[i] - base) * a.c - logs));
+        const float t = te.t[i] - s.top;
+        const float q = exp2f(t * a.c) / s.sum;
+        if (q != 0.f) part += q * (t - (te.z[i] - base) + rest);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-    return s.bad ? NAN : a.tau * a.tau * kLn2 * part;
+    return s.bad ? NAN : a.tau * part;
 }
 
 // ------------------------------------------------------------------ loss alone
