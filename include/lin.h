@@ -130,10 +130,10 @@ LIN_API int lin_destroy(lin_ctx* ctx);
  * workspace): use one context per stream.
  * Back-to-back calls: with LIN_OPT_EARLY_START at 2 (off by default; see
  * that option for when it is safe), a call whose inputs (X, W, bias) overlap
- * none of the previous call's output on the same stream is launched as a
- * programmatic dependent of that call, reads its inputs before the previous
- * kernel has finished and writes Y only after it. For such a call the built-in
- * plan may also drop its K split (the skinny kernel's cluster split, the
+ * none of the outputs that earlier calls on the same stream may still write is
+ * launched as a programmatic dependent of the previous call, reads its inputs
+ * before that call's kernel has finished and writes Y only after it. For such a
+ * call the built-in plan may also drop its K split (the skinny kernel's cluster split, the
  * tensor-core K split, an FFMA split over a short K), so that consecutive
  * independent calls fill the SMs together; see LIN_OPT_ADAPTIVE_PLANS.
  * lin_plan_query returns the plan of an isolated call. */
@@ -296,7 +296,8 @@ LIN_API int lin_check_device(lin_ctx* ctx, void* stream);
  *   2: as 1, and X may be read early too.
  *   The library only sees its own calls: it drops the early reads of W / bias
  *   (and X) by itself when they overlap the previous library call's output on
- *   that stream, but it cannot see other work. Use 1 only when no other work on
+ *   that stream, and a call whose early reads would touch what an older call may
+ *   still be writing is launched in plain stream order. It cannot see other work. Use 1 only when no other work on
  *   the stream writes the next call's W or bias between two library calls (an
  *   optimizer step does), and 2 only when nothing but library calls write its X
  *   either (a framework kernel that produces X, such as a layernorm, does).

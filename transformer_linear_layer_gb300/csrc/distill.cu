@@ -377,8 +377,8 @@ __global__ void __launch_bounds__(kDgAll, 2) distill_grad_kernel(const DistillAr
     }
     if constexpr (CL > 1) cluster_sync_all();  // the peers' barriers are ready
     else __syncthreads();
+    pdl_wait();  // first, so that a call after this one never runs beside one before it
     pdl_launch_dependents();
-    pdl_wait();
     Slice<BF16, CL> sl(sh, g, smem, rank);
     void* entries = smem + (size_t)g.slots * g.chunk * 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

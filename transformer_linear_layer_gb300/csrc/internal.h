@@ -133,6 +133,11 @@ int ensure_smem_attr(std::atomic<unsigned long long>& done, Kernel kern, size_t 
     return LIN_OK;
 }
 
+// A call on `st` that was launched in plain stream order, or whose kernels wait for what
+// is before them before they let others start: [p, p + bytes) is all that may still be
+// written there.
+void note_ordered_output(cudaStream_t st, const void* p, size_t bytes);
+
 // Launchers (return LIN_OK or LIN_ERR_*). They assume the plan was validated.
 int launch_fill(const Problem& p);
 int launch_skinny(const Problem& p, const lin_plan& plan);

@@ -329,66 +329,119 @@ struct DeviceGuard {
     }
 };
 
-// Output range of the last launch on each stream (process-wide): a kernel
-// that starts before its predecessor finishes may prefetch W only when W does
-// not overlap what that predecessor writes.
-struct LastOut {
-    cudaStream_t stream;
-    uintptr_t lo, hi;
-};
-std::mutex g_last_mu;
-LastOut g_last[64];
-int g_last_n = 0;
-
 struct Range {
     const void* p;
     size_t bytes;
 };
 
-// Which inputs may be read before the dependency wait: *w_ok for W and bias,
-// *x_ok for X (each false when it overlaps the previous output on `st`).
-// Records Y as this stream's newest output.
-void early_reads_ok(cudaStream_t st, Range w, Range bias, Range x, Range y, bool* w_ok, bool* x_ok, bool* known) {
-    auto hits = [](const LastOut& o, Range r) {
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(r.p), hi = lo + r.bytes;
-        return r.p && r.bytes && lo < o.hi && o.lo < hi;
-    };
-    std::lock_guard<std::mutex> lk(g_last_mu);
-    *w_ok = *x_ok = true;
-    *known = false;
-    int slot = -1;
-    for (int i = 0; i < g_last_n; ++i)
-        if (g_last[i].stream == st) {
-            *w_ok = !hits(g_last[i], w) && !hits(g_last[i], bias);
-            *x_ok = !hits(g_last[i], x);
+// What the calls on each stream (process-wide) may still be writing. A kernel that
+// lets its successor start before its own dependency wait is behind it while the call
+// before both still runs, so a call's inputs are compared with the outputs of all calls
+// since the last one that is known to start, or to let others start, only when
+// everything before it has finished. Such a call begins the list anew.
+constexpr int kOutputs = 64;
+struct StreamOutputs {
+    cudaStream_t stream;
+    int n;
+    bool more;  // there are outputs that the list has no place for
+    uintptr_t lo[kOutputs], hi[kOutputs];
+};
+std::mutex g_outputs_mu;
+StreamOutputs g_outputs[64];
+int g_streams = 0;
+
+// The stream's list, under the mutex. A new one is empty; once the table has been full,
+// it may be one that had to make room for another.
+StreamOutputs& outputs_of(cudaStream_t st, bool* known) {
+    for (int i = 0; i < std::min(g_streams, 64); ++i)
+        if (g_outputs[i].stream == st) {
             *known = true;
-            slot = i;
-            break;
+            return g_outputs[i];
         }
-    if (slot < 0) {
-        if (g_last_n < 64) {
-            slot = g_last_n++;
-        } else {
-            slot = 0;  // table full: forget the oldest entry's stream, stay safe for this one
-            *w_ok = *x_ok = false;
-        }
-    }
-    g_last[slot].stream = st;
-    g_last[slot].lo = reinterpret_cast<uintptr_t>(y.p);
-    g_last[slot].hi = g_last[slot].lo + y.bytes;
+    *known = false;
+    StreamOutputs& o = g_outputs[g_streams % 64];
+    o.stream = st;
+    o.n = 0;
+    o.more = g_streams >= 64;
+    if (++g_streams == 128) g_streams = 64;
+    return o;
 }
 
-// Record `y` as the last output on stream `st` (for a call whose last kernel
-// writes a different range than its main output).
-void note_output(cudaStream_t st, Range y) {
-    std::lock_guard<std::mutex> lk(g_last_mu);
-    for (int i = 0; i < g_last_n; ++i)
-        if (g_last[i].stream == st) {
-            g_last[i].lo = reinterpret_cast<uintptr_t>(y.p);
-            g_last[i].hi = g_last[i].lo + y.bytes;
+void add_output(StreamOutputs& o, Range y) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(y.p), hi = lo + y.bytes;
+    for (int i = 0; i < o.n; ++i)
+        if (o.lo[i] <= lo && hi <= o.hi[i]) {  // there already: now the newest
+            std::swap(o.lo[i], o.lo[o.n - 1]);
+            std::swap(o.hi[i], o.hi[o.n - 1]);
             return;
         }
+    if (o.n == kOutputs) {
+        o.more = true;
+        return;
+    }
+    o.lo[o.n] = lo;
+    o.hi[o.n++] = hi;
 }
+
+struct EarlyReads {
+    bool w = false;        // W and bias may be read before the dependency wait
+    bool x = false;        // and X
+    bool known = false;    // the stream has had a call
+    bool ordered = false;  // the call has to be launched in plain stream order
+};
+
+// Which inputs a call may read early, at the context's level; records Y. An input that
+// the newest call writes is read after the wait, which is for that call. One that
+// an older call writes, or that cannot be told from one, makes the call an ordered one.
+EarlyReads early_reads(cudaStream_t st, int level, Range w, Range bias, Range x, Range y) {
+    std::lock_guard<std::mutex> lk(g_outputs_mu);
+    EarlyReads r;
+    StreamOutputs& o = outputs_of(st, &r.known);
+    if (level >= 1) {
+        bool older = o.more || o.n == kOutputs;
+        auto hits = [&](Range in) {
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(in.p), hi = lo + in.bytes;
+            bool hit = false;
+            for (int i = 0; in.p && in.bytes && i < o.n; ++i)
+                if (lo < o.hi[i] && o.lo[i] < hi) {
+                    hit = true;
+                    older = older || i != o.n - 1;
+                }
+            return hit;
+        };
+        const bool bias_hit = hits(bias);
+        r.w = !hits(w) && !bias_hit;
+        r.x = level >= 2 && r.w && !hits(x);
+        if (older) {
+            r.w = r.x = false;
+            r.ordered = true;
+            o.n = 0;
+            o.more = false;
+        }
+    }
+    add_output(o, y);
+    return r;
+}
+
+// Record another output of a call on `st`.
+void note_output(cudaStream_t st, Range y) {
+    std::lock_guard<std::mutex> lk(g_outputs_mu);
+    bool known;
+    add_output(outputs_of(st, &known), y);
+}
+
+}  // namespace
+
+void note_ordered_output(cudaStream_t st, const void* p, size_t bytes) {
+    std::lock_guard<std::mutex> lk(g_outputs_mu);
+    bool known;
+    StreamOutputs& o = outputs_of(st, &known);
+    o.n = 0;
+    o.more = false;
+    add_output(o, Range{p, bytes});
+}
+
+namespace {
 
 int check_plan_fits(const lin_plan& p, int M, int N, int K, int precision) {
     switch (p.kernel) {
@@ -484,12 +537,13 @@ int run(lin_ctx* ctx, const lin_plan& plan_in, int M, int N, int K, const void* 
     p.workspace_bytes = ctx->workspace_bytes;
     p.dev_status = ctx->dev_status;
     p.sm_count = ctx->sm_count;
-    bool w_ok = false, x_ok = false, known = false;
-    early_reads_ok(p.stream, Range{W, (size_t)N * K * ein}, Range{bias, bias ? (size_t)N * 4 : 0},
-                   Range{X, (size_t)M * K * ein}, Range{Y, ybytes}, &w_ok, &x_ok, &known);
-    p.early_start = ctx->programmatic;
-    p.early_w = p.early_start && ctx->early_level >= 1 && w_ok;
-    p.early_x = p.early_w && ctx->early_level >= 2 && x_ok;
+    const EarlyReads early = early_reads(p.stream, ctx->early_level, Range{W, (size_t)N * K * ein},
+                                         Range{bias, bias ? (size_t)N * 4 : 0}, Range{X, (size_t)M * K * ein},
+                                         Range{Y, ybytes});
+    const bool known = early.known;
+    p.early_start = ctx->programmatic && !early.ordered;
+    p.early_w = p.early_start && early.w;
+    p.early_x = p.early_w && early.x;
     // An independent call right after another call on this stream overlaps it:
     // the skinny stream then needs no K split to fill the SMs (the concurrent
     // calls do), and skipping the split saves its reduction.
@@ -796,16 +850,15 @@ int backward_setup(lin_ctx* ctx, int which, int M, int N, int K, const void* dZ,
     q->stream = static_cast<cudaStream_t>(stream);
     q->dev_status = ctx->dev_status;
     q->sm_count = ctx->sm_count;
-    bool w_ok = false, x_ok = false, known = false;
-    early_reads_ok(q->stream, Range{B, b_bytes}, Range{nullptr, 0}, Range{dZ, dz_bytes}, Range{out, out_bytes}, &w_ok,
-                   &x_ok, &known);
-    q->early_start = ctx->programmatic;
-    q->early_x = q->early_start && ctx->early_level >= 1 && w_ok && ctx->early_level >= 2 && x_ok;
+    const EarlyReads early = early_reads(q->stream, ctx->early_level, Range{B, b_bytes}, Range{nullptr, 0},
+                                         Range{dZ, dz_bytes}, Range{out, out_bytes});
+    q->early_start = ctx->programmatic && !early.ordered;
+    q->early_x = q->early_start && early.x;
     q->workspace = ctx->workspace;
     q->workspace_bytes = ctx->workspace_bytes;
     // Right after an independent call the two overlap (early start) and fill
     // the SMs together: a K split would only add its round trip.
-    q->ksplit_ok = !(ctx->adaptive && known && q->early_x);
+    q->ksplit_ok = !(ctx->adaptive && early.known && q->early_x);
     q->aux = nullptr;
     return LIN_OK;
 }
@@ -899,8 +952,7 @@ int lin_gelu_backward(lin_ctx* ctx, long long count, const void* dY, const void*
     DeviceGuard guard(ctx->device);
     if (!guard.ok) return LIN_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    bool w_ok = false, x_ok = false, known = false;
-    early_reads_ok(st, Range{Z, bytes}, Range{nullptr, 0}, Range{dY, bytes}, Range{dZ, bytes}, &w_ok, &x_ok, &known);
+    note_output(st, Range{dZ, bytes});
     return launch_gelu_backward(count, dY, Z, dZ, precision == LIN_PREC_BF16, ctx->sm_count, st,
                                 ctx->programmatic);
 }
@@ -984,9 +1036,8 @@ int lin_attention_forward(lin_ctx* ctx, int B, int T, int H, int D, const void* 
     p.sm_count = ctx->sm_count;
     p.early_start = ctx->programmatic;
     // Its output is a later call's input: note it for the early-read checks.
-    bool w_ok = false, x_ok = false, known = false;
-    early_reads_ok(p.stream, Range{nullptr, 0}, Range{nullptr, 0}, Range{qkv, in_bytes}, Range{out, out_bytes}, &w_ok,
-                   &x_ok, &known);
+    note_output(p.stream, Range{out, out_bytes});
+    if (lse) note_output(p.stream, Range{lse, lse_bytes});
     return launch_attention(p);
 }
 
@@ -1004,9 +1055,9 @@ struct Operand {
     bool written;
 };
 
-// Alignment, and no output over another operand. Records the outputs' hull as
-// the stream's newest output.
-int check_operands(const Operand* o, int N, cudaStream_t st) {
+// Alignment, and no output over another operand. Records the outputs of the call on the
+// stream; *hull is where they all lie.
+int check_operands(const Operand* o, int N, cudaStream_t st, lin::Range* hull) {
     using namespace lin;
     for (int i = 0; i < N; ++i)
         for (int j = 0; j < N; ++j)
@@ -1021,10 +1072,15 @@ int check_operands(const Operand* o, int N, cudaStream_t st) {
         if (a < lo) lo = a;
         if (a + o[i].bytes > hi) hi = a + o[i].bytes;
     }
-    bool w_ok = false, x_ok = false, known = false;
-    early_reads_ok(st, Range{nullptr, 0}, Range{nullptr, 0}, Range{nullptr, 0},
-                   Range{reinterpret_cast<const void*>(lo), hi - lo}, &w_ok, &x_ok, &known);
+    *hull = Range{reinterpret_cast<const void*>(lo), hi - lo};
+    note_output(st, *hull);
     return LIN_OK;
+}
+
+// These calls' kernels wait for what is before them before they let others start.
+int launched(int rc, cudaStream_t st, const lin::Range& hull) {
+    if (rc == LIN_OK) lin::note_ordered_output(st, hull.p, hull.bytes);
+    return rc;
 }
 
 int logits_setup(lin_ctx* ctx, int R, int V, const void* logits, long long ld, int type, float tau, void* stream,
@@ -1070,7 +1126,8 @@ int distill_run(lin_ctx* ctx, int R, int V, int K, const void* logits, long long
         {lse, r4, 4, true},
         {grad ? dz : nullptr, grad ? row_bytes(R, V, ldd, esz) : 0, esz, true},
     };
-    const int ok = check_operands(ops, (int)(sizeof(ops) / sizeof(ops[0])), p.stream);
+    lin::Range hull;
+    const int ok = check_operands(ops, (int)(sizeof(ops) / sizeof(ops[0])), p.stream, &hull);
     if (ok != LIN_OK) return ok;
     lin::DeviceGuard guard(ctx->device);
     if (!guard.ok) return LIN_ERR_CUDA;
@@ -1085,7 +1142,7 @@ int distill_run(lin_ctx* ctx, int R, int V, int K, const void* logits, long long
     p.lse = lse;
     p.dz = grad ? dz : nullptr;
     p.ldd = ldd;
-    return lin::launch_distill(p);
+    return launched(lin::launch_distill(p), p.stream, hull);
 }
 
 }  // namespace
@@ -1108,7 +1165,8 @@ int lin_attention_backward(lin_ctx* ctx, int B, int T, int H, int D, const void*
         {qkv, 3 * bytes, 16, false}, {out, bytes, 16, false},      {lse, (size_t)B * H * T * 4, 4, false},
         {dout, bytes, 16, false},    {dqkv, 3 * bytes, 16, true},
     };
-    const int ok = check_operands(ops, (int)(sizeof(ops) / sizeof(ops[0])), static_cast<cudaStream_t>(stream));
+    Range hull;
+    const int ok = check_operands(ops, (int)(sizeof(ops) / sizeof(ops[0])), static_cast<cudaStream_t>(stream), &hull);
     if (ok != LIN_OK) return ok;
     DeviceGuard guard(ctx->device);
     if (!guard.ok) return LIN_ERR_CUDA;
@@ -1129,7 +1187,7 @@ int lin_attention_backward(lin_ctx* ctx, int B, int T, int H, int D, const void*
     p.dev_status = ctx->dev_status;
     p.sm_count = ctx->sm_count;
     p.early_start = ctx->programmatic;
-    return launch_attention_backward(p);
+    return launched(launch_attention_backward(p), p.stream, hull);
 }
 
 int lin_token_logprobs(lin_ctx* ctx, int R, int V, const void* logits, long long ld, int logits_type,
@@ -1158,7 +1216,8 @@ int lin_token_logprobs(lin_ctx* ctx, int R, int V, const void* logits, long long
         {top_logprob, r4 * top, 4, true},
         {top_ids, r4 * top, 4, true},
     };
-    const int ok = check_operands(ops, (int)(sizeof(ops) / sizeof(ops[0])), p.stream);
+    lin::Range hull;
+    const int ok = check_operands(ops, (int)(sizeof(ops) / sizeof(ops[0])), p.stream, &hull);
     if (ok != LIN_OK) return ok;
     lin::DeviceGuard guard(ctx->device);
     if (!guard.ok) return LIN_ERR_CUDA;
@@ -1170,7 +1229,7 @@ int lin_token_logprobs(lin_ctx* ctx, int R, int V, const void* logits, long long
     p.lse = lse;
     p.top_logprob = top_logprob;
     p.top_ids = top_ids;
-    return lin::launch_logprobs(p);
+    return launched(lin::launch_logprobs(p), p.stream, hull);
 }
 
 int lin_distill_forward(lin_ctx* ctx, int R, int V, int K, const void* logits, long long ld, int logits_type,

@@ -136,6 +136,7 @@ extern "C" int lin_forward_fp32_static(int M, int N, int K, const float* X, cons
     p.sm_count = sm;
     p.early_start = false;
     p.early_x = false;
+    note_ordered_output(p.stream, Y, ybytes);
     if (plan.kernel == LIN_KERNEL_FILL) return launch_fill(p);
     if (plan.kernel == LIN_KERNEL_GEMV) return launch_gemv(p, plan);  // no scratch
     if (plan.kernel != LIN_KERNEL_FFMA) return LIN_ERR_UNSUPPORTED;
