@@ -466,8 +466,8 @@ LIN_API int lin_attention_forward(lin_ctx* ctx, int B, int T, int H, int D, cons
  *          (-inf marks a query that sees no key: it contributes nothing).
  *   dout : (B*T) x C bf16, the gradient of out.
  *   dqkv : (B*T) x 3C bf16, written whole; must not overlap the inputs.
- *   B, T, H, D, causal, scale as in the forward; a scale whose reciprocal is not
- *   finite in fp32 is refused (LIN_ERR_ARG).
+ *   B, T, H, D, causal, scale as in the forward; a scale below 2^-100 or above
+ *   2^100 is refused (LIN_ERR_ARG): lse / scale has to be finite in fp32.
  * Arithmetic: bf16 products accumulated in fp32 on the tensor cores; p and ds
  * in fp32, each rounded once to bf16 for the products that take it; sums in
  * fp32, each gradient rounded once. The sums' order is fixed by the sizes, the

@@ -109,3 +109,24 @@ def test_blocks_that_cannot_run_hold_up_no_other(hold, B, T, H, causal, left):
     torch.cuda.synchronize()
     ctx.check()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T", [100, 300])
+@pytest.mark.parametrize("scale", [2.0 ** -98, 2.0 ** -100])
+def test_queries_that_see_no_key_at_tiny_scales(T, scale):
+    """lse = -inf takes no part in dv at a scale where the scores hardly differ."""
+    B, H, C = 2, 2, 128
+    qkv, out, lse, dout = inputs(B, T, H, False)
+    out, lse = tll.attention_forward(qkv, B, T, H, causal=False, scale=scale, with_lse=True)
+    lse[:, :, ::3] = -torch.inf
+    got = tll.attention_backward(qkv, out, lse, dout, B, T, H, causal=False, scale=scale)
+    tll.default_context(0).check()
+    assert bool(got.isfinite().all())
+    p = torch.exp(-lse.double())
+    p[:, :, ::3] = 0
+    do = dout.double().view(B, T, H, 64).transpose(1, 2)
+    want = torch.einsum("bhi,bhid->bhd", p, do)  # every key's dv
+    bound = torch.einsum("bhi,bhid->bhd", p * (ref.BF16_HALF + 2.0 ** -16), do.abs())
+    bound = 1.02 * (bound + ref.BF16_HALF * (want.abs() + bound)) + 1e-30
+    dv = got[:, 2 * C:].double().view(B, T, H, 64).transpose(1, 2)
+    assert bool(((dv - want[:, :, None]).abs() <= bound[:, :, None]).all())

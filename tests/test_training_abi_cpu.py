@@ -139,3 +139,15 @@ def test_the_binding_takes_gpu_tensors_only():
     with pytest.raises(ValueError):
         tll.attention_backward(torch.zeros(2, 192).bfloat16(), torch.zeros(2, 64).bfloat16(), torch.zeros(1, 1, 2),
                                torch.zeros(2, 64).bfloat16(), 1, 2, 1)
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-35, 7.8e-31, 1.3e30, 3e38])
+def test_attention_backward_scales_that_fp32_statistics_cannot_carry(ctx, scale):
+    """lse / scale and the score that stands for "sees no key" have to be finite."""
+    assert attention(ctx, scale=scale) == tll.ERR_ARG
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** 100])
+def test_attention_backward_takes_scales_up_to_that(ctx, scale):
+    assert attention(ctx, scale=scale) == tll.ERR_CUDA

@@ -319,7 +319,8 @@ __device__ __forceinline__ void ab_stats(const uint16_t* out, const uint16_t* do
     }
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     if (half == 0) {
-        const float far = -1e30f;  // finite, so that it is 0 where it meets a 0
+        // finite, so that it is 0 where it meets a 0, and 0 as a probability: e scale <= -256
+        const float far = -fmaxf(1e30f, 256.f * inv_scale);
         const float l = t < T ? lse[((size_t)b * H + h) * T + t] : -INFINITY;
         const float e = l == -INFINITY || l == INFINITY ? far : -l * inv_scale;
         const float e0 = bf16_bits_to_f32(f32_to_bf16_bits(e)), e1 = bf16_bits_to_f32(f32_to_bf16_bits(e - e0));

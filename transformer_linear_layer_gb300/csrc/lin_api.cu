@@ -1159,7 +1159,8 @@ int lin_attention_backward(lin_ctx* ctx, int B, int T, int H, int D, const void*
         (long long)B * H * nb > INT_MAX)
         return LIN_ERR_UNSUPPORTED;
     if (!qkv || !out || !lse || !dout || !dqkv) return LIN_ERR_ARG;
-    if (scale > 0.f && isinf(1.0f / scale)) return LIN_ERR_ARG;
+    // lse / scale, and what stands for no key, are fp32
+    if (scale > 0.f && !(scale >= 0x1p-100f && scale <= 0x1p100f)) return LIN_ERR_ARG;
     const size_t bytes = (size_t)rows * H * D * 2;
     const Operand ops[] = {
         {qkv, 3 * bytes, 16, false}, {out, bytes, 16, false},      {lse, (size_t)B * H * T * 4, 4, false},
