@@ -151,3 +151,11 @@ def test_attention_backward_scales_that_fp32_statistics_cannot_carry(ctx, scale)
 @pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** 100])
 def test_attention_backward_takes_scales_up_to_that(ctx, scale):
     assert attention(ctx, scale=scale) == tll.ERR_CUDA
+
+
+@pytest.mark.parametrize("tau", [3e-39, 4.2e-39])
+def test_temperatures_whose_base_2_factor_overflows(ctx, tau):
+    """1 / tau is finite, log2(e) / tau is not."""
+    assert logprobs(ctx, tau=tau) == tll.ERR_ARG
+    for form in ("forward", "backward", "both"):
+        assert distill(ctx, form, tau=tau) == tll.ERR_ARG

@@ -1085,7 +1085,9 @@ int launched(int rc, cudaStream_t st, const lin::Range& hull) {
 
 int logits_setup(lin_ctx* ctx, int R, int V, const void* logits, long long ld, int type, float tau, void* stream,
                  lin::LogitsProblem* p) {
-    if (!ctx || R < 0 || V < 0 || !float_type(type) || !(tau > 0.f) || isinf(tau) || isinf(1.0f / tau))
+    // log2(e) / tau has to be finite in fp32 too
+    if (!ctx || R < 0 || V < 0 || !float_type(type) || !(tau > 0.f) || isinf(tau) ||
+        isinf((float)(1.4426950408889634 / tau)))
         return LIN_ERR_ARG;
     if (R == 0) return LIN_OK;
     if (V == 0 || ld < V || !logits) return LIN_ERR_ARG;
