@@ -31,10 +31,15 @@ constexpr int kDgWarps = kDgThreads / 32;
 constexpr int kDgHelpers = 4;     // (32768 x 8000 bf16, gradient: 283 us with 2, 200 with 4; loss and gradient of
                                   // 8192 x 50257 348 and 354)
 constexpr int kDgAll = kDgThreads + 32 + 32 * kDgHelpers;
-// Units of a thread in a chunk, at most: a row of 50257 bf16 is five chunks of five
-// (loss and gradient of 8192 rows 354 us back to back, 393 with 8, 399 with 4; 4 is
-// ahead at other widths: 32768 x 8000 314 against 329, 2000 x 128001 297 against 312).
-constexpr int kDgBatch = 5;
+// Units of a thread in a chunk, at most. A slice goes in as few chunks as that allows,
+// all of about one size, which often is less than the limit: the kernel is there for
+// chunks of up to four units, whose code is shorter, and for five. Loss and gradient, in
+// us, with a limit of 4 and of 5: where five means fewer chunks, 7959 x 50257 bf16 388
+// and 347, 3999 x 100003 bf16 427 and 377, 32768 x 5003 fp32 509 and 407, 19989 x 20011
+// bf16 522 and 540; where it does not, code for 4 and for 5, 32768 x 8000 bf16 313 and
+// 329, 12498 x 32003 bf16 409 and 427, 3124 x 128001 bf16 451 and 478. (Eight, at 8192 x
+// 50257: 393 against 354.)
+constexpr int kDgBatch = 5, kDgSmallBatch = 4;
 constexpr int kDgRing = 32;       // chunks of the ring, at most
 constexpr int kDgRows = 2 * kDgHelpers;  // rows between their teacher's entries and their loss
 // Shared memory of a block when two share an SM (228 KB, 1 KB of it reserved for each block).
@@ -185,7 +190,7 @@ struct DgRing {
 
 // A block's slice of its cluster's rows. Chunks are numbered in the order in
 // which they pass through the ring; `slot` and `phase` follow that order.
-template <bool BF16, int CL>
+template <bool BF16, int CL, int BATCH>
 struct Slice {
     DgShared& sh;
     const DgRing& g;
@@ -225,19 +230,19 @@ struct Slice {
         return (c1 - c0 - (int)(threadIdx.x & ~31u) + kDgThreads - 1) / kDgThreads;
     }
     // This thread's units of a chunk; units past its end read as -inf. `again`: from memory.
-    __device__ __forceinline__ void units(const Row<BF16>& row, int which, int c0, int c1, uint4 (&r)[kDgBatch],
+    __device__ __forceinline__ void units(const Row<BF16>& row, int which, int c0, int c1, uint4 (&r)[BATCH],
                                           bool again = false) const {
         const int n = c1 - c0 - (int)threadIdx.x;
         if (!again) {
             const uint32_t at = smem_u32(ring) + ((uint32_t)which * g.chunk + threadIdx.x) * 16u;
 #pragma unroll
-            for (int k = 0; k < kDgBatch; ++k) {
+            for (int k = 0; k < BATCH; ++k) {
                 r[k] = Row<BF16>::nothing();
                 lg_lds16_if(r[k], n > k * kDgThreads, at + k * (kDgThreads * 16u));
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < kDgBatch; ++k) {
+            for (int k = 0; k < BATCH; ++k) {
                 const int u = c0 + threadIdx.x + k * kDgThreads;
                 r[k] = Row<BF16>::nothing();
                 lg_ldg16_if(r[k], n > k * kDgThreads && row.whole(u), row.a0 + (long long)u * 16);
@@ -245,7 +250,7 @@ struct Slice {
         }
         if (c0 > 0 && c1 < row.units) return;  // (as most chunks) no unit sticks out
 #pragma unroll
-        for (int k = 0; k < kDgBatch; ++k) {
+        for (int k = 0; k < BATCH; ++k) {
             const int u = c0 + threadIdx.x + k * kDgThreads;
             if (u < c1 && !row.whole(u)) r[k] = row.load_edge(u);
         }
@@ -291,8 +296,8 @@ struct Slice {
 };
 
 // Statistics of the whole row in every computing thread of the cluster; `seq` counts the calls.
-template <bool BF16, int CL>
-__device__ __forceinline__ Stats dg_row_stats(const Slice<BF16, CL>& sl, Stats st, float c, uint32_t seq) {
+template <bool BF16, int CL, int BATCH>
+__device__ __forceinline__ Stats dg_row_stats(const Slice<BF16, CL, BATCH>& sl, Stats st, float c, uint32_t seq) {
     DgShared& sh = sl.sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Stats* parts = sh.warp[seq & 1];
@@ -357,7 +362,7 @@ template <bool BF16>
 constexpr float dg_lse_limit() { return BF16 ? 512.f : 64.f; }
 
 // FORWARD: the statistics (and the loss) are computed; else lse is given.
-template <bool BF16, bool FORWARD, int CL>
+template <bool BF16, bool FORWARD, int CL, int BATCH>
 __global__ void __launch_bounds__(kDgAll, 2) distill_grad_kernel(const DistillArgs a, const DgRing g) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ DgShared sh;
@@ -379,7 +384,7 @@ __global__ void __launch_bounds__(kDgAll, 2) distill_grad_kernel(const DistillAr
     else __syncthreads();
     pdl_wait();  // first, so that a call after this one never runs beside one before it
     pdl_launch_dependents();
-    Slice<BF16, CL> sl(sh, g, smem, rank);
+    Slice<BF16, CL, BATCH> sl(sh, g, smem, rank);
     void* entries = smem + (size_t)g.slots * g.chunk * 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long r0 = blockIdx.x / CL, step = gridDim.x / CL;
@@ -450,7 +455,7 @@ __global__ void __launch_bounds__(kDgAll, 2) distill_grad_kernel(const DistillAr
                 for (int c0 = u0; c0 < u1; c0 += g.chunk) {
                     const int c1 = min(c0 + g.chunk, u1);
                     sl.wait(sh.full[sl.slot], sl.phase);
-                    uint4 raw[kDgBatch];
+                    uint4 raw[BATCH];
                     sl.units(row, sl.slot, c0, c1, raw);
                     if (!g.whole) sl.arrive(sh.empty[sl.slot]);
                     lg_accumulate<BF16, false>(st, raw, sl.count(c0, c1), a.c);
@@ -459,7 +464,7 @@ __global__ void __launch_bounds__(kDgAll, 2) distill_grad_kernel(const DistillAr
                 // The teacher's warp has read the row's logits in this block, so that
                 // the statistics tell the peers that they may write to it.
                 sl.wait(sh.teacher[b], (seq / kDgRows) & 1);
-                st = dg_row_stats<BF16, CL>(sl, st, a.c, seq);
+                st = dg_row_stats(sl, st, a.c, seq);
                 base = lg_base(st.m);
                 logs = log2f(st.s);
                 inv_s = 1.0f / st.s;
@@ -471,11 +476,11 @@ __global__ void __launch_bounds__(kDgAll, 2) distill_grad_kernel(const DistillAr
                     Stats st{-INFINITY, 0.f, 0.f, 0u};
                     for (int c0 = u0; c0 < u1; c0 += g.chunk) {
                         const int c1 = min(c0 + g.chunk, u1);
-                        uint4 raw[kDgBatch];
+                        uint4 raw[BATCH];
                         sl.units(row, 0, c0, c1, raw, true);
                         lg_accumulate<BF16, false>(st, raw, sl.count(c0, c1), a.c);
                     }
-                    st = dg_row_stats<BF16, CL>(sl, st, a.c, renewed++);
+                    st = dg_row_stats(sl, st, a.c, renewed++);
                     base = lg_base(st.m);
                     logs = log2f(st.s);
                     inv_s = 1.0f / st.s;
@@ -492,13 +497,13 @@ __global__ void __launch_bounds__(kDgAll, 2) distill_grad_kernel(const DistillAr
             for (int c0 = u0; c0 < u1; c0 += g.chunk) {
                 const int c1 = min(c0 + g.chunk, u1);
                 if constexpr (!FORWARD) sl.wait(sh.full[sl.slot], sl.phase);
-                uint4 raw[kDgBatch];
+                uint4 raw[BATCH];
                 sl.units(row, slot, c0, c1, raw, FORWARD && !g.whole);
                 if (!FORWARD || g.whole) sl.arrive(sh.empty[slot]);
                 const bool plain = vec && c0 > 0 && c1 < row.units;
                 const int n = sl.count(c0, c1);
 #pragma unroll
-                for (int k = 0; k < kDgBatch; ++k) {
+                for (int k = 0; k < BATCH; ++k) {
                     if (k >= n) break;
                     const int u = c0 + threadIdx.x + k * kDgThreads;
                     const uint4 o = dg_unit<BF16>(raw[k], base, a.c, coef, keep);
@@ -563,10 +568,10 @@ struct DgKernelState {
     std::atomic<unsigned long long> fits{0};  // dynamic shared memory << 32 | clusters
 };
 
-template <bool BF16, bool FORWARD, int CL>
+template <bool BF16, bool FORWARD, int CL, int BATCH>
 int launch_grad(const LogitsProblem& p, const DistillArgs& a, const DgPlan& q) {
     static DgKernelState state;
-    const auto kern = distill_grad_kernel<BF16, FORWARD, CL>;
+    const auto kern = distill_grad_kernel<BF16, FORWARD, CL, BATCH>;
     if (ensure_smem_attr(state.attr_set, kern, kDgSmem) != LIN_OK) return LIN_ERR_CUDA;
     long long clusters = std::max(1, 2 * p.sm_count / CL);
     if (CL > 1 && p.R > 1) {
@@ -592,6 +597,14 @@ int launch_grad(const LogitsProblem& p, const DistillArgs& a, const DgPlan& q) {
         clusters = std::min(clusters, (long long)std::max(1, fit));
     }
     return lg_launch(kern, std::min(clusters, p.R) * CL, kDgAll, q.smem, CL, p, a, q.ring);
+}
+
+template <int CL, int BATCH>
+int launch_grad_of(const LogitsProblem& p, const DistillArgs& a, const DgPlan& q) {
+    const bool forward = p.lse_in == nullptr;
+    if (p.bf16)
+        return forward ? launch_grad<true, true, CL, BATCH>(p, a, q) : launch_grad<true, false, CL, BATCH>(p, a, q);
+    return forward ? launch_grad<false, true, CL, BATCH>(p, a, q) : launch_grad<false, false, CL, BATCH>(p, a, q);
 }
 
 }  // namespace
@@ -622,12 +635,11 @@ int launch_distill(const LogitsProblem& p) {
             return p.bf16 ? lg_launch(distill_loss_kernel<true, CL>, p.R * CL, kDfThreads, entries, CL, p, a)
                           : lg_launch(distill_loss_kernel<false, CL>, p.R * CL, kDfThreads, entries, CL, p, a);
         });
-    const bool forward = p.lse_in == nullptr;
-    const DgPlan q = dg_plan(p, forward, kDgRows * entries);
+    const DgPlan q = dg_plan(p, p.lse_in == nullptr, kDgRows * entries);
     return lg_by_cluster(q.cl, [&](auto cl) {
         constexpr int CL = decltype(cl)::value;
-        if (p.bf16) return forward ? launch_grad<true, true, CL>(p, a, q) : launch_grad<true, false, CL>(p, a, q);
-        return forward ? launch_grad<false, true, CL>(p, a, q) : launch_grad<false, false, CL>(p, a, q);
+        return q.ring.chunk <= kDgSmallBatch * kDgThreads ? launch_grad_of<CL, kDgSmallBatch>(p, a, q)
+                                                          : launch_grad_of<CL, kDgBatch>(p, a, q);
     });
 }
 
