@@ -561,11 +561,12 @@ DgPlan dg_plan(const LogitsProblem& p, bool whole, size_t extra) {
     return q;
 }
 
-// What a kernel has been told about the device: its shared-memory limit, and
-// how many clusters of a configuration fit at once (the last one asked for).
+// What a kernel has been told about the devices: its shared-memory limit, and
+// how many clusters of a configuration fit at once (the last one asked for, on a
+// device).
 struct DgKernelState {
     std::atomic<unsigned long long> attr_set{0};
-    std::atomic<unsigned long long> fits{0};  // dynamic shared memory << 32 | clusters
+    std::atomic<unsigned long long> fits{0};  // dynamic shared memory << 32 | device << 16 | clusters
 };
 
 template <bool BF16, bool FORWARD, int CL, int BATCH>
@@ -577,9 +578,12 @@ int launch_grad(const LogitsProblem& p, const DistillArgs& a, const DgPlan& q) {
     if (CL > 1 && p.R > 1) {
         // Clusters stay within a part of the SMs, so fewer may fit: a block of a
         // second wave would take its share of the rows after all others are done.
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return LIN_ERR_CUDA;
+        const unsigned long long asked = ((unsigned long long)q.smem << 16 | (unsigned)(dev & 0xFFFF)) << 16;
         const unsigned long long known = state.fits.load(std::memory_order_relaxed);
-        int fit = (int)(known & 0xFFFFFFFFu);
-        if (known >> 32 != q.smem) {
+        int fit = (int)(known & 0xFFFFu);
+        if ((known ^ asked) >> 16 != 0) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3((unsigned)(clusters * CL));
             cfg.blockDim = dim3(kDgAll);
@@ -592,7 +596,8 @@ int launch_grad(const LogitsProblem& p, const DistillArgs& a, const DgPlan& q) {
             cfg.attrs = &attr;
             cfg.numAttrs = 1;
             if (cudaOccupancyMaxActiveClusters(&fit, kern, &cfg) != cudaSuccess) return LIN_ERR_CUDA;
-            state.fits.store((unsigned long long)q.smem << 32 | (unsigned)fit, std::memory_order_relaxed);
+            fit = std::min(fit, 0xFFFF);
+            state.fits.store(asked | (unsigned)fit, std::memory_order_relaxed);
         }
         clusters = std::min(clusters, (long long)std::max(1, fit));
     }
