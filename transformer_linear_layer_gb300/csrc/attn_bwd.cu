@@ -359,6 +359,15 @@ __device__ __forceinline__ void ab_mma_scores(uint32_t d_tmem, uint32_t a, uint3
     tc_mma<true>(d_tmem, ab_flat_desc(ones, 128, 0), ab_flat_desc(stat, 0, 128), kIdescS, 1u);
 }
 
+__device__ __forceinline__ int2 ab_lds_item(uint32_t addr) {
+    int2 x;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ void ab_sts_item(uint32_t addr, int j, int bh) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(j), "r"(bh) : "memory");
+}
+
 // A role's place in the block's items. The TMA warp draws them by a ticket and passes
 // them on through a ring in shared memory. Items are ordered by key block, then by head
 // (their lengths fall along the order when causal), and only a block that runs draws
@@ -366,16 +375,16 @@ __device__ __forceinline__ void ab_mma_scores(uint32_t d_tmem, uint32_t a, uint3
 // blocks are resident: with the items dealt out by block index, a block that another
 // stream's kernel keeps off its SM held up all the others.
 struct AbWalker {
-    int m = -1;          // number of the item within the block
-    int j, bh;           // key block, launch-local (sequence, head)
-    int i, i0;           // query block, the item's first
-    bool valid = false;  // false past the last item
+    unsigned m = ~0u;  // number of the item within the block
+    int j = -1, bh;    // key block (-1 past the last item), launch-local (sequence, head)
+    int i;             // query block
     __device__ __forceinline__ void set(const AbArgs& a, int2 x) {
         j = x.x;
         bh = x.y;
-        valid = j >= 0;
-        i = i0 = a.causal ? j : 0;
+        i = first(a);
     }
+    __device__ __forceinline__ bool valid() const { return j >= 0; }
+    __device__ __forceinline__ int first(const AbArgs& a) const { return a.causal ? j : 0; }
     __device__ __forceinline__ bool last(const AbArgs& a) const { return i == a.nb - 1; }
 };
 
@@ -392,8 +401,8 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
     uint8_t* sOut = sDS + kAbDs;               // dq on its way out; dk and dv at an item's end
     uint8_t* sOnes = sOut + kAbDqTile;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sOnes + kAbOnes);
-    int2* items = reinterpret_cast<int2*>(bars + kAbBars);  // key block (-1: no more) and head
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + kAbItems);
+    // (the items' ring lies behind the barriers: key block, -1 for no more, and head)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kAbBars + kAbItems);
     int* s_abort = reinterpret_cast<int*>(tmem_slot + 1);
 
     // Full / empty of the stages; then, once a step: sfull, dpfull, done (the
@@ -405,7 +414,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
     const uint32_t sfull = one_a_step, dpfull = one_a_step + 8, done = one_a_step + 16, pready = one_a_step + 24,
                    dsready = one_a_step + 32, dqfree = one_a_step + 40, accfree = one_a_step + 48,
                    outfull = one_a_step + 56, outfree = one_a_step + 72, ifull = outfree + 8,
-                   iempty = ifull + 8 * kAbItems;
+                   iempty = ifull + 8 * kAbItems, items = iempty + 8 * kAbItems;
 
     // (the same in every lane, and known to be: roles branch without divergence)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -464,14 +473,14 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
     auto take = [&](AbWalker& w) {
         const uint32_t k = ++w.m % kAbItems;
         if (!wait(ifull + 8 * k, (w.m / kAbItems) & 1)) return false;
-        w.set(a, items[k]);
+        w.set(a, ab_lds_item(items + 8 * k));
         arrive(iempty + 8 * k);
         return true;
     };
     auto take_alone = [&](AbWalker& w) {
         const uint32_t k = ++w.m % kAbItems;
         if (!mbar_wait(ifull + 8 * k, (w.m / kAbItems) & 1)) return false;
-        w.set(a, items[k]);
+        w.set(a, ab_lds_item(items + 8 * k));
         mbar_arrive(iempty + 8 * k);
         return true;
     };
@@ -495,7 +504,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
                 break;
             }
             if (lane == 0) {
-                items[is] = make_int2(w.j, w.bh);
+                ab_sts_item(items + 8 * is, w.j, w.bh);
                 mbar_arrive(ifull + 8 * is);
             }
             if (!more) break;
@@ -509,7 +518,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
                 mbar_expect_tx(kfull + 8 * ks, kAbTile);
                 tma_load_3d(smem_u32(sK + ks * kAbTile), &tmQkv, kfull + 8 * ks, a.C + h * kAbD, w.j * kAbB, b);
             }
-            for (int i = w.i0; i < a.nb; ++i, ++n) {
+            for (int i = w.first(a); i < a.nb; ++i, ++n) {
                 const uint32_t qs = n % QS;
                 if (aborted() || !wait(qempty + 8 * qs, ((n / QS) & 1) ^ 1)) {
                     ok = false;
@@ -523,7 +532,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
                     bulk_load(smem_u32(q + 2 * kAbTile), a.stats + ((size_t)w.bh * a.nb + i) * kAbB, kAbStat,
                               qfull + 8 * qs);
                 }
-                if (i == w.i0) {  // V's one stage frees when the item before has its last dP'
+                if (i == w.first(a)) {  // V's one stage frees when the item before has its last dP'
                     if (!wait(vempty, (m & 1) ^ 1)) {
                         ++n;
                         ok = false;
@@ -568,7 +577,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
             uint32_t s_stage = 0, s_phase = 0;     // Q stage of the next scores
             uint32_t g_stage = 0;                  // and of the gradients
             uint32_t lead_k = 0, lead_kphase = 0, lead_vphase = 0, cur_k = 0, acc_phase = 1;
-            int lead_left = lead.valid ? a.nb - lead.i0 : 0, cur_left = lead_left, lead_len = lead_left;
+            int lead_left = lead.valid() ? a.nb - lead.first(a) : 0, cur_left = lead_left, lead_len = lead_left;
             bool lead_first = true, first = true, any = lead_left > 0;
             auto scores = [&](uint32_t d_tmem, uint64_t ad, uint64_t bd, uint64_t one_rows) {
 #pragma unroll
@@ -594,7 +603,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
                 }
                 if (--lead_left == 0) {
                     ok = take_alone(lead);
-                    lead_len = lead_left = ok && lead.valid ? a.nb - lead.i0 : 0;
+                    lead_len = lead_left = ok && lead.valid() ? a.nb - lead.first(a) : 0;
                     lead_first = true;
                     lead_vphase ^= 1;
                     if (++lead_k == KS) {
@@ -680,7 +689,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
             uint32_t msg = 0;
             AbWalker w;
             bool ok = take_alone(w);
-            for (; ok && w.valid; ok = ++w.i < a.nb || take_alone(w)) {
+            for (; ok && w.valid(); ok = ++w.i < a.nb || take_alone(w)) {
                 const int bh = a.bh0 + w.bh, b = bh / a.H, h = bh % a.H;
                 if (w.last(a) && (msg++ & 1) == (uint32_t)(warp & 1)) {
                     // dk and dv; tokens past T lie outside the map and are not written
@@ -746,7 +755,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         uint32_t n = 0;
         AbWalker w;
         bool ok = take(w);
-        for (; ok && w.valid; ok = ++w.i < a.nb || take(w), ++n) {
+        for (; ok && w.valid(); ok = ++w.i < a.nb || take(w), ++n) {
             const bool diag = a.causal && w.i == w.j;
             const bool masked = diag || (w.j + 1) * kAbB > a.T;
             // query c of this group is visible to the thread's key from `from` on
@@ -790,7 +799,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQkv, const __grid_constant
         uint32_t n = 0, msg = 0;
         AbWalker w;
         bool ok = take(w);
-        for (; ok && w.valid; ok = ++w.i < a.nb || take(w), ++n) {
+        for (; ok && w.valid(); ok = ++w.i < a.nb || take(w), ++n) {
             const bool last = w.last(a);
             ok = wait(done, n & 1) && (msg == 0 || wait(outfree, (msg - 1) & 1));
             if (!ok) break;

@@ -279,9 +279,8 @@ __device__ __forceinline__ Stats lg_warp_join(Stats st, float c) {
     return st;
 }
 
-// Statistics of a whole row read straight from memory by a cluster of CL blocks
-// of NT threads, which take its units in turn.
-// seen(largest value) is called after every N units of the thread.
+// A thread's share of a row's statistics, read straight from memory: the units u0,
+// u0 + stride, ... in batches of N. seen(largest value) is called after every batch.
 template <bool BF16, bool ENTROPY, int N, class Seen>
 __device__ __forceinline__ Stats lg_stream(const Row<BF16>& row, int u0, int stride, float c, Seen seen) {
     Stats st{-INFINITY, 0.f, 0.f, 0u};
