@@ -130,3 +130,15 @@ def test_queries_that_see_no_key_at_tiny_scales(T, scale):
     bound = 1.02 * (bound + ref.BF16_HALF * (want.abs() + bound)) + 1e-30
     dv = got[:, 2 * C:].double().view(B, T, H, 64).transpose(1, 2)
     assert bool(((dv - want[:, :, None]).abs() <= bound[:, :, None]).all())
+
+
+@pytest.mark.parametrize("T", [100, 300])
+def test_the_output_of_a_query_that_sees_no_key_does_not_matter(T):
+    """lse = -inf: its out may be 0 / 0, and reaches no gradient."""
+    qkv, out, lse, dout = inputs(2, T, 2, False)
+    lse[:, :, ::3] = -torch.inf
+    want = tll.attention_backward(qkv, out, lse, dout, 2, T, 2, causal=False)
+    out.view(2, T, 128)[:, ::3] = float("nan")
+    got = tll.attention_backward(qkv, out, lse, dout, 2, T, 2, causal=False)
+    tll.default_context(0).check()
+    assert bool(got.isfinite().all()) and torch.equal(got, want)

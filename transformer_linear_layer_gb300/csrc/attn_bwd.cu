@@ -324,8 +324,9 @@ __device__ __forceinline__ void ab_stats(const uint16_t* out, const uint16_t* do
         const float l = t < T ? lse[((size_t)b * H + h) * T + t] : -INFINITY;
         const float e = l == -INFINITY || l == INFINITY ? far : -l * inv_scale;
         const float e0 = bf16_bits_to_f32(f32_to_bf16_bits(e)), e1 = bf16_bits_to_f32(f32_to_bf16_bits(e - e0));
-        const float d0 = bf16_bits_to_f32(f32_to_bf16_bits(-sum)), d1 = bf16_bits_to_f32(f32_to_bf16_bits(-sum - d0));
         const bool cut = e == far;
+        if (cut) sum = 0.f;  // its out may be anything, a 0 / 0 as well
+        const float d0 = bf16_bits_to_f32(f32_to_bf16_bits(-sum)), d1 = bf16_bits_to_f32(f32_to_bf16_bits(-sum - d0));
         st[row] = make_uint4(pack_bf16x2(e0, cut ? 0.f : e1), pack_bf16x2(cut ? 0.f : (e - e0) - e1, d0),
                              pack_bf16x2(d1, (-sum - d0) - d1), 0u);
     }
