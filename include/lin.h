@@ -474,9 +474,17 @@ LIN_API int lin_attention_forward(lin_ctx* ctx, int B, int T, int H, int D, cons
  * SM count and the workspace, so results repeat bit for bit. Uses the context
  * workspace (up to about 256 bytes a head and token per partial sum of dq;
  * heads that do not fit at once go in several launches; LIN_ERR_WORKSPACE
- * when not even one head fits). qkv, out, dout and dqkv must be 16-byte aligned
- * (LIN_ERR_ALIGN), lse 4-byte aligned. Asynchronous on `stream`; reads and
- * writes only after the previous kernel on the stream has finished. */
+ * when not even one head fits: the default workspace holds one of 246000
+ * tokens). Key blocks add to a partial sum of dq in turn; a larger workspace
+ * gives more partial sums, and less waiting, up to one for every key block of a
+ * head that runs at the same time. A wait is only for a block that runs already,
+ * whatever SMs other streams hold. A NaN or infinity in a token's row of qkv may
+ * reach the gradients of all tokens in its block of 128 of the sequence, also
+ * across the causal mask (0 times NaN in the products); one in dout their dk and
+ * dv. out of a query that sees no key is not used. qkv, out, dout and dqkv must
+ * be 16-byte aligned (LIN_ERR_ALIGN), lse 4-byte aligned. Asynchronous on
+ * `stream`; reads and writes only after the previous kernel on the stream has
+ * finished. */
 LIN_API int lin_attention_backward(lin_ctx* ctx, int B, int T, int H, int D, const void* qkv, const void* out,
                                    const float* lse, const void* dout, void* dqkv, int causal, float scale,
                                    void* stream);
@@ -486,14 +494,16 @@ LIN_API int lin_attention_backward(lin_ctx* ctx, int B, int T, int H, int D, con
  * vocabulary's columns are neither read nor written), z_rj below. Element
  * types are named by lin_dtype. tau > 0 is a temperature: probabilities are
  * softmax(z / tau). Maxima, sums and statistics are held in fp32, the
- * differences from a row's maximum are formed before they are scaled, and
- * results do not depend on the order in which blocks run (identical inputs
- * give identical bits). A NaN or +inf among a row's logits makes that row's
- * results NaN; -inf is a token that cannot occur (probability 0).
+ * differences from a row's maximum are formed before they are scaled (but see
+ * lin_distill_backward, which is given lse), and results do not depend on the
+ * order in which blocks run (identical inputs give identical bits). A NaN or
+ * +inf among a row's logits makes that row's results NaN; -inf is a token that
+ * cannot occur (probability 0).
  * Pointers are DEVICE pointers aligned to their elements (LIN_ERR_ALIGN).
  * LIN_ERR_ARG: a NULL that is not allowed, a negative size, ld < V, an
- * unknown type, tau not positive and finite, or an output that overlaps an
- * input or another output (except as said). LIN_ERR_UNSUPPORTED: V > 2^30 or
+ * unknown type, tau not positive and finite (or so small that log2(e) / tau is
+ * not finite in fp32), or an output that overlaps an input or another output
+ * (except as said). LIN_ERR_UNSUPPORTED: V > 2^30 or
  * R > 2^27. R == 0 does nothing; V == 0 with rows is LIN_ERR_ARG. No
  * workspace. Launched like lin_forward, as a programmatic dependent that reads
  * and writes only after the previous kernel on the stream has finished. */
@@ -536,7 +546,8 @@ LIN_API int lin_token_logprobs(lin_ctx* ctx, int R, int V, const void* logits, l
  * g_r being the gradient that reaches loss_r. Entries may repeat a token. A
  * row without entries (or whose teacher logits are all -inf) has loss 0 and
  * gradient 0, and so has the gradient where g_r = 0, whatever the logits are.
- * An id >= V makes its row's loss and gradient NaN.
+ * An id >= V makes its row's loss and gradient NaN. Logits that are all -inf
+ * leave p undefined: NaN, in a row with entries (the gradient: and weight).
  *   ids     : R x K, LIN_TYPE_INT32 or LIN_TYPE_INT64 (ids_type), 0 <= K <= 256.
  *   teacher : R x K, LIN_TYPE_FP32 or LIN_TYPE_BF16 (teacher_type). */
 

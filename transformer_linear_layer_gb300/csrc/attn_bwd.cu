@@ -40,23 +40,24 @@
 // attn_bwd_kernel's warps: 0 TMA; 1 tcgen05.mma issuer; 2 and 3 send what is staged
 // for memory; 4-19 four groups that turn S' and dP' into P' and dS' (a thread has one
 // key and 32 of the block's queries); 20-23 dQ out of TMEM, and dK and dV at an
-// item's end. S'(n+1) and dP'(n+1) are issued while step n is turned into P' and
-// dS', so the exponentials overlap the products. A step has three commits (S', dV with the next dP', dK with
-// dQ); what else waits for products is told by the warps that saw them.
+// item's end. When P'(n) is written, S'(n+1), dV and dP'(n+1) are issued and run while
+// dS'(n) is formed; dK and dQ of step n run under the exponentials of step n+1. A step
+// has three commits (S', dV with the next dP', dK with dQ); what else waits for products
+// is told by the warps that saw them.
 //
 // Order of the dq sums: the key blocks of a head form `chains` chains (block j in
 // chain j % chains), each with its own fp32 copy of dq; within a chain block j
 // adds to a tile after block j - chains has (a counter per tile, waited for). The
 // sums' order is thus fixed, results are repeatable bit for bit whichever block has an
 // item, and a wait is only ever for an item that was drawn earlier, by a block that
-// runs. A tile is added by one bulk reduction from shared memory, whose completion is looked for a step later.
-// Every wait is bounded (about 1 s); a block that gives up sets the device status
-// word.
+// runs. A tile is added by one bulk reduction from shared memory, whose completion is
+// looked for a step later. Every wait is bounded (about 1 s); a block that gives up sets
+// the device status word.
 //
 // Measured (GB300): 64 sequences of 128, 12 heads, causal 29 us (3.5 TB/s of
-// operands); 2 of 4096 211 us (610 TF/s of the visible pairs' products), of which
-// attn_bwd_kernel about 180 (profiled alone); a step takes 2700 cycles when nothing
-// waits, 1660 of them products. Tensor pipe 36 % active, DRAM 6 %: bound by the
+// operands); 2 of 4096 202 us (640 TF/s of the visible pairs' products), of which
+// attn_bwd_kernel about 170 (profiled alone); a step takes 2700 cycles when nothing
+// waits, 1660 of them products. Tensor pipe 37 % active, DRAM 6 %: bound by the
 // steps' chain of products, exponentials and additions. T <= 128: DRAM 28 %, tensor
 // pipe 15 %: bound by the latency of a block's own chain, two blocks an SM.
 #include <math.h>
@@ -374,7 +375,11 @@ __device__ __forceinline__ void ab_sts_item(uint32_t addr, int j, int bh) {
 // (their lengths fall along the order when causal), and only a block that runs draws
 // one. So an item whose sums another one waits for has started and goes on, whichever
 // blocks are resident: with the items dealt out by block index, a block that another
-// stream's kernel keeps off its SM held up all the others.
+// stream's kernel keeps off its SM held up all the others. Against dealing them out,
+// every second round in reverse where chains were many (calls in a CUDA graph): 2 x 4096
+// x 12 heads causal 211 -> 200 us, 16 x 4096 x 12 1562 -> 1494, 40 x 256 x 12 61.0 -> 59.4,
+// 3 x 777 x 5 full 25.3 both, and 8 x 200 x 12, 192 items of one or two steps whose
+// reversed round was even, 17.4 -> 19.8.
 struct AbWalker {
     unsigned m = ~0u;  // number of the item within the block
     int j = -1, bh;    // key block (-1 past the last item), launch-local (sequence, head)

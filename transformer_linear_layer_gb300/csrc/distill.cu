@@ -15,10 +15,13 @@
 // (about 1 s); a block that gives up sets the device status word.
 //
 // Measured (GB300, 8192 x 50257 bf16, 32 entries): loss 138 us (6.0 TB/s), loss and
-// gradient 344 us (4.8 TB/s), gradient 293 us (5.6 TB/s). Of 2048 rows the gradient
-// kernel issues in 47 % of the cycles (58 % with the loss) with DRAM at 60 % (47 %)
-// of its nominal rate: neither is full. Its warps wait, for memory and for the
-// instruction before, and the rows in shared memory leave room for 26 of them an SM.
+// gradient 345 us (4.8 TB/s), gradient 292 us (5.6 TB/s); 2048 x 50257 fp32, 64
+// entries: gradient 161 us, loss and gradient 176 us (5.1 and 4.7 TB/s). Of 2048 bf16
+// rows the gradient kernel issues in 46 % of the cycles (58 % with the loss) with DRAM
+// at 61 % (48 %) of its nominal rate: neither is full. Its warps wait, for memory and
+// for the instruction before, and the ring in shared memory leaves room for 26 of them
+// an SM. That ring is what the loss and gradient together need; the gradient from a
+// given lse shares the kernel, and has not been built as a stream through registers.
 #include "logits.cuh"
 
 namespace lin {

@@ -33,8 +33,9 @@ struct Problem {
     // early_start: launch as a programmatic dependent of the previous kernel on
     // the stream (the CTAs may start before it finishes; nothing is read before
     // griddepcontrol.wait unless early_w / early_x say so; L2 prefetches of the
-    // operands may be issued before it). early_w: W and bias do not overlap that
-    // kernel's output and may be read before the wait; early_x: neither does X.
+    // operands may be issued before it). early_w: W and bias overlap no output that
+    // a call before this one may still write, and may be read before the wait;
+    // early_x: neither does X.
     // Y is written only after the wait.
     bool early_start = false;
     bool early_w = false;

@@ -5,7 +5,9 @@
 // and what is kept of it is a running maximum m and the sum
 // s = sum exp((z - m) / tau) of a softmax. The differences z - m are formed
 // before they are scaled, so that neither an offset common to a row nor a mask of
-// the type's lowest value costs accuracy; maximum, sums and statistics are fp32.
+// the type's lowest value costs accuracy (a gradient from a given lse keeps to that
+// by computing the two again where lse is too large to stand for them); maximum, sums
+// and statistics are fp32.
 //
 // A row is cut into 16-byte units on the address grid, since rows of an odd
 // vocabulary start anywhere: whole units move as one 16-byte access, the (at

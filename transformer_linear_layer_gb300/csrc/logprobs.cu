@@ -9,7 +9,7 @@
 //
 // Measured (GB300): 8192 x 50257 bf16 without a top 150 us (5.5 TB/s), top 8 180 us;
 // 301 x 128001 fp32, top 32, 53 us; one row of 50257, top 20, 11 us. 2048 rows
-// of the first issue in 63 % of the cycles with DRAM at 51 % (45 % with the top) of
+// of the first issue in 64 % of the cycles with DRAM at 52 % (45 % with the top) of
 // its nominal rate: neither is full, the warps wait for memory and for the
 // instruction before. The small cases are bound by latency.
 #include "logits.cuh"
