@@ -136,9 +136,13 @@ extern "C" int lin_forward_fp32_static(int M, int N, int K, const float* X, cons
     p.sm_count = sm;
     p.early_start = false;
     p.early_x = false;
-    note_ordered_output(p.stream, Y, ybytes);
-    if (plan.kernel == LIN_KERNEL_FILL) return launch_fill(p);
-    if (plan.kernel == LIN_KERNEL_GEMV) return launch_gemv(p, plan);  // no scratch
+    // (all in plain stream order: what came before is done when they start)
+    const auto launched = [&](int rc) {
+        if (rc == LIN_OK) note_ordered_output(p.stream, Y, ybytes);
+        return rc;
+    };
+    if (plan.kernel == LIN_KERNEL_FILL) return launched(launch_fill(p));
+    if (plan.kernel == LIN_KERNEL_GEMV) return launched(launch_gemv(p, plan));  // no scratch
     if (plan.kernel != LIN_KERNEL_FFMA) return LIN_ERR_UNSUPPORTED;
     if (plan.splits > 1) {
         // The array keeps the previous call's contents: zero the counters this
@@ -146,5 +150,5 @@ extern "C" int lin_forward_fp32_static(int M, int N, int K, const float* X, cons
         const size_t counter_bytes = (size_t)plan.grid_x * plan.grid_y * sizeof(unsigned);
         if (cudaMemsetAsync(splitk_counters(scratch), 0, counter_bytes, p.stream) != cudaSuccess) return LIN_ERR_CUDA;
     }
-    return launch_ffma(p, plan);
+    return launched(launch_ffma(p, plan));
 }
