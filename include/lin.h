@@ -579,6 +579,98 @@ LIN_API int lin_distill_forward_backward(lin_ctx* ctx, int R, int V, int K, cons
                                          int teacher_type, float tau, const float* weight, float* loss,
                                          void* dlogits, long long ldd, void* stream);
 
+/* ---- Rotary positions, and serving from a paged cache ---- */
+
+/* Rotary positions of (part of) a head: pair i < dim / 2 of a token at position p
+ * turns by the angle p f_i. Pairs are elements (i, i + dim / 2) or (2i, 2i + 1) of
+ * the head's first dim elements; the rest of the head does not rotate. */
+typedef enum {
+    LIN_ROTARY_HALF = 0,         /* element i with i + dim / 2 */
+    LIN_ROTARY_INTERLEAVED = 1   /* element 2i with 2i + 1 */
+} lin_rotary_layout;
+
+typedef struct {
+    int dim;                           /* elements that rotate: even, 0 to the head's width */
+    int layout;                        /* lin_rotary_layout */
+    float scale;                       /* factor on the rotated elements (1 = none): finite */
+    const unsigned long long* turns;   /* DEVICE, dim / 2: f_i / (2 pi) mod 1 in units of 2^-64 */
+} lin_rotary;
+
+/* turns[i] (host) from frequencies[i] (host, radians per position, finite): the
+ * fixed-point form that lin_rotary holds on the device. The kernels multiply it by
+ * the position modulo 2^64, which is the angle modulo one turn, without
+ * rounding, for any 64-bit position. */
+LIN_API int lin_rotary_turns(const double* frequencies, int n, unsigned long long* turns);
+
+/* y = x with every head rotated by its row's position. Row n, head h at
+ * x + n * ldx + h * D and y + n * ldy + h * D (elements; ldx, ldy >= H * D).
+ *   x, y      : LIN_TYPE_FP32 or LIN_TYPE_BF16 (type), DEVICE. y may be x (with ldy == ldx);
+ *               otherwise no row's heads of y may lie over x's. Rows of equal stride may
+ *               interleave (column ranges of one matrix).
+ *   positions : N of LIN_TYPE_INT32 or LIN_TYPE_INT64 (positions_type), any value.
+ *   D         : 1 to 1024.
+ * Angles, cosines and products in fp32 (the angle itself is exact), one rounding to
+ * the type. A NaN or infinity reaches its own pair only. Fast when addresses and
+ * strides are multiples of 16 bytes and the pairs fill them; right for any. No workspace. Reads and writes only
+ * after the previous kernel on the stream has finished. */
+LIN_API int lin_rotary_forward(lin_ctx* ctx, int N, int H, int D, const void* x, long long ldx, void* y, long long ldy,
+                               int type, const void* positions, int positions_type, const lin_rotary* rotary,
+                               void* stream);
+
+/* Its gradient: dx from dy, the rotation by the negative angle (and the same scale). */
+LIN_API int lin_rotary_backward(lin_ctx* ctx, int N, int H, int D, const void* dy, long long lddy, void* dx,
+                                long long lddx, int type, const void* positions, int positions_type,
+                                const lin_rotary* rotary, void* stream);
+
+/* A paged cache of keys and values, bf16. Slot s of head h of page g starts at element
+ * g * page_stride + h * head_stride + s * token_stride of k, and of v, head_dim
+ * consecutive elements. */
+typedef struct {
+    void* k;                  /* DEVICE, 16-byte aligned */
+    void* v;
+    int pages;
+    int page_size;            /* tokens a page holds: a power of two, 8 to 4096 */
+    int heads;                /* key (and value) heads */
+    int head_dim;             /* 64 or 128 */
+    long long page_stride;    /* elements; multiples of 8 (16 bytes), each head's row of a slot apart */
+    long long head_stride;
+    long long token_stride;
+} lin_kv_cache;
+
+/* A batch of sequences whose new tokens are rows of packed matrices, one sequence
+ * after the other. The arrays are on the DEVICE and are read when the kernels run, so a captured graph
+ * follows them. */
+typedef struct {
+    int sequences;
+    int tokens;               /* rows of the packed matrices */
+    const int* q_start;       /* sequences + 1: sequence b's new tokens are rows q_start[b] to q_start[b + 1] - 1; ascending */
+    const int* kv_len;        /* sequences: tokens that sequence b has in the cache, the new ones included */
+    const int* block_table;   /* sequence b's tokens i * page_size .. lie in page block_table[b * table_stride + i] */
+    int table_pages;          /* entries of a sequence that may be read */
+    long long table_stride;   /* >= table_pages */
+} lin_kv_batch;
+
+/* Write the new tokens' keys and values into the cache. Row n, the i-th new token of
+ * sequence b (i = n - q_start[b]), goes to the place of position
+ *   p = kv_len[b] - (q_start[b + 1] - q_start[b]) + i.
+ * With a rotary plan (not NULL) keys are rotated on the way, by p or by
+ * positions[n], and queries too: q_out = q rotated.
+ *   q, q_out : tokens x H heads of head_dim, bf16, rows ldq and ldqo elements apart; q_out
+ *              may be q (ldqo == ldq). Both NULL (H 0): keys and values only. Without a
+ *              rotary plan they must be.
+ *   k, v     : tokens x cache->heads heads of head_dim, bf16, rows ldk and ldv apart.
+ *   positions: NULL, or one per row (LIN_TYPE_INT32 or LIN_TYPE_INT64), used for the rotation only.
+ * Rows of no sequence are left out: nothing is written for them. A token whose
+ * position lies outside the table, or whose table entry is not a page of the cache, is not
+ * stored (its q_out is written). Two tokens with the same place: one of them
+ * is stored. q_start has to ascend; whatever the arrays hold, nothing outside the
+ * operands is read or written. Columns of one matrix (a qkv
+ * projection's output) are fine as q, k, v and q_out; nothing else may overlap an output. */
+LIN_API int lin_cache_append(lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_batch* batch, int H, const void* q,
+                             long long ldq, void* q_out, long long ldqo, const void* k, long long ldk, const void* v,
+                             long long ldv, const void* positions, int positions_type, const lin_rotary* rotary,
+                             void* stream);
+
 #ifdef __cplusplus
 }
 #endif

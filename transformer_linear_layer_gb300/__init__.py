@@ -24,6 +24,7 @@ __all__ = [
     "LinError", "Context", "Plan", "forward", "forward_plan", "plan_query", "plan_make", "build",
     "backward_data", "backward_weight", "gelu_backward", "attention_forward", "attention_backward",
     "TokenLogprobs", "token_logprobs", "distill_forward", "distill_backward", "distill_forward_backward",
+    "Rotary", "rotary_forward", "rotary_backward", "KVCache", "KVBatch", "cache_append",
     "library", "PREC_FP32", "PREC_TF32", "PREC_BF16", "EPI_NONE", "EPI_GELU_TANH",
     "KERNEL_NONE", "KERNEL_FILL", "KERNEL_SKINNY", "KERNEL_FFMA", "KERNEL_TC", "KERNEL_GEMV",
 ]
@@ -42,6 +43,8 @@ EARLY_NONE, EARLY_WEIGHTS, EARLY_ALL = 0, 1, 2
 OK, ERR_ARG, ERR_ALIGN, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_TIMEOUT, ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
 # lin_dtype
 TYPE_FP32, TYPE_BF16, TYPE_INT32, TYPE_INT64 = 0, 1, 2, 3
+# lin_rotary_layout
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
 # LIN_STATIC_SCRATCH_BYTES: the fixed device array behind lin_forward_fp32_static.
 STATIC_SCRATCH_BYTES = 8 << 20
 
@@ -66,6 +69,29 @@ class Plan(ctypes.Structure):
 
     def __repr__(self):
         return f"Plan({self.as_dict()})"
+
+
+class RotaryPlan(ctypes.Structure):
+    """Mirror of ``lin_rotary``."""
+
+    _fields_ = [("dim", ctypes.c_int), ("layout", ctypes.c_int), ("scale", ctypes.c_float),
+                ("turns", ctypes.c_void_p)]
+
+
+class KVCachePlan(ctypes.Structure):
+    """Mirror of ``lin_kv_cache``."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("token_stride", ctypes.c_longlong)]
+
+
+class KVBatchPlan(ctypes.Structure):
+    """Mirror of ``lin_kv_batch``."""
+
+    _fields_ = [("sequences", ctypes.c_int), ("tokens", ctypes.c_int), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("table_pages", ctypes.c_int),
+                ("table_stride", ctypes.c_longlong)]
 
 
 class LinError(RuntimeError):
@@ -121,6 +147,10 @@ def library() -> ctypes.CDLL:
                 "lin_distill_forward": ([P, I, I, I, P, L, I, P, I, P, I, F, P, P, P], I),
                 "lin_distill_backward": ([P, I, I, I, P, L, I, P, I, P, I, F, P, P, P, L, P], I),
                 "lin_distill_forward_backward": ([P, I, I, I, P, L, I, P, I, P, I, F, P, P, P, L, P], I),
+                "lin_rotary_turns": ([P, I, P], I),
+                "lin_rotary_forward": ([P, I, I, I, P, L, P, L, I, P, I, P, P], I),
+                "lin_rotary_backward": ([P, I, I, I, P, L, P, L, I, P, I, P, P], I),
+                "lin_cache_append": ([P, P, P, I, P, L, P, L, P, L, P, L, P, I, P, P], I),
                 "lin_strerror": ([I], ctypes.c_char_p),
                 "lin_abi_version": ([], I),
             }
@@ -774,3 +804,236 @@ def distill_forward_backward(logits, ids, teacher, weight=None, temperature: flo
     if rc != OK:
         raise LinError(rc, "lin_distill_forward_backward")
     return loss, out
+
+
+# ---------------------------------------------------------------- rotary positions
+
+class Rotary:
+    """The plan of rotary positions: which elements of a head turn, and how fast.
+
+    dim: elements of each head that rotate (even; the rest of the head does not).
+    interleaved: pairs are neighbours (2i, 2i + 1) instead of halves (i, i + dim/2).
+    Pair i turns by base ** (-2 i / dim) radians per position, scaled for longer
+    contexts by ``scaling``:
+
+      None      as trained
+      "linear"  all frequencies divided by ``factor``
+      "ntk"     the base times factor ** (dim / (dim - 2)): the slowest pair is
+                divided by the factor, the fastest kept
+      "yarn"    by parts: pairs that turn at most ``slow`` times in
+                ``original_length`` positions are divided by the factor, those that
+                turn ``fast`` times or more are kept, with a ramp between; the rotated
+                elements are multiplied by 0.1 ln(factor) + 1 (Peng et al., "YaRN:
+                Efficient Context Window Extension of Large Language Models")
+
+    or by ``frequencies`` (dim/2 radians per position) in place of all of these.
+    ``scale`` replaces the factor on the rotated elements. The plan holds its
+    table on ``device``; positions may be any 64-bit integers."""
+
+    def __init__(self, dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str | None = None,
+                 factor: float = 1.0, original_length: int | None = None, fast: float = 32.0, slow: float = 1.0,
+                 frequencies=None, scale: float | None = None, device="cuda"):
+        import math
+
+        import torch
+
+        if dim < 0 or dim % 2:
+            raise ValueError(f"dim must be even and not negative, got {dim}")
+        if scaling not in (None, "linear", "ntk", "yarn"):
+            raise ValueError(f"unknown scaling {scaling!r}")
+        if not (math.isfinite(factor) and factor >= 1.0):
+            raise ValueError(f"factor must be at least 1, got {factor}")
+        if not (math.isfinite(base) and base > 0):
+            raise ValueError(f"base must be positive, got {base}")
+        own_scale = 1.0
+        if frequencies is None:
+            if scaling == "ntk" and dim > 2:
+                base = base * factor ** (dim / (dim - 2))
+            frequencies = [base ** (-2.0 * i / dim) for i in range(dim // 2)]
+            if scaling == "linear":
+                frequencies = [f / factor for f in frequencies]
+            elif scaling == "yarn":
+                if not original_length or original_length < 1 or not fast > slow:
+                    raise ValueError("yarn needs original_length, and fast above slow")
+                held = []
+                for f in frequencies:
+                    keep = (original_length * f / (2 * math.pi) - slow) / (fast - slow)
+                    keep = min(1.0, max(0.0, keep))
+                    held.append(f * keep + f / factor * (1.0 - keep))
+                frequencies = held
+                own_scale = 0.1 * math.log(factor) + 1.0
+        self.frequencies = [float(f) for f in frequencies]
+        n = dim // 2
+        if len(self.frequencies) != n:
+            raise ValueError(f"{n} frequencies are needed, got {len(self.frequencies)}")
+        self.dim, self.interleaved = dim, bool(interleaved)
+        self.scale = own_scale if scale is None else float(scale)
+        turns = (ctypes.c_ulonglong * max(n, 1))()
+        rc = library().lin_rotary_turns((ctypes.c_double * max(n, 1))(*self.frequencies), n, turns)
+        if rc != OK:
+            raise LinError(rc, "lin_rotary_turns")
+        signed = [t - (1 << 64) if t >> 63 else t for t in turns]
+        self.turns = torch.tensor(signed[:n] or [0], dtype=torch.int64, device=device)
+        self._plan = RotaryPlan(dim, ROTARY_INTERLEAVED if self.interleaved else ROTARY_HALF, self.scale,
+                                self.turns.data_ptr())
+        self._ref = ctypes.byref(self._plan)
+
+
+def _check_heads(t, dtype, what):
+    """(rows, heads, width, row stride) of an N x H x D tensor whose rows hold their
+    heads one after the other, any distance apart."""
+    if not t.is_cuda or t.dim() != 3 or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} must be an N x heads x width CUDA tensor" + (f" of {dtype}" if dtype else ""))
+    N, H, D = t.shape
+    s0, s1, s2 = t.stride()
+    if (D > 1 and s2 != 1) or (H > 1 and s1 != D):
+        raise ValueError(f"{what}: a row must hold its heads one after the other")
+    ld = s0 if N > 1 else H * D
+    if ld < H * D:
+        raise ValueError(f"{what}: rows overlap")
+    return N, H, D, ld
+
+
+def _rotary(call, x, positions, rotary, out, ctx, stream):
+    import torch
+
+    N, H, D, ldx = _check_heads(x, None, "x")
+    kind = _float_type(x, "x")
+    ptype = _index_type(positions, "positions")
+    _check(positions, positions.dtype, (N,), "positions")
+    if out is None:
+        out = torch.empty((N, H, D), dtype=x.dtype, device=x.device)
+    No, Ho, Do, ldy = _check_heads(out, x.dtype, "out")
+    if (No, Ho, Do) != (N, H, D):
+        raise ValueError(f"out must have shape {(N, H, D)}, got {tuple(out.shape)}")
+    _same_device(x, positions, out, rotary.turns)
+    dev = x.device.index if x.device.index is not None else 0
+    ctx = ctx or default_context(dev)
+    rc = getattr(library(), call)(ctx._h, N, H, D, x.data_ptr(), ldx, out.data_ptr(), ldy, kind,
+                                  positions.data_ptr(), ptype, rotary._ref, _stream_ptr(stream, dev))
+    if rc != OK:
+        raise LinError(rc, call)
+    return out
+
+
+def rotary_forward(x, positions, rotary: Rotary, out=None, ctx: Context | None = None, stream=None):
+    """Heads turned by their row's position.
+
+    x: N x H x D, fp32 or bf16, the heads of a row one after the other and rows any
+    distance apart: the query and key heads of a qkv projection's output are
+    ``qkv[:, :2 * C].unflatten(1, (2 * H, D))``. positions: N, int32 or int64.
+    Returns N x H x D; ``out`` may be ``x`` (in place)."""
+    return _rotary("lin_rotary_forward", x, positions, rotary, out, ctx, stream)
+
+
+def rotary_backward(dy, positions, rotary: Rotary, out=None, ctx: Context | None = None, stream=None):
+    """The gradient of :func:`rotary_forward`'s input from its output's (``out`` may be ``dy``)."""
+    return _rotary("lin_rotary_backward", dy, positions, rotary, out, ctx, stream)
+
+
+# ---------------------------------------------------------------- paged cache
+
+class KVCache:
+    """A paged cache of keys and values: ``k`` and ``v`` bf16 of pages x heads x
+    page_size x head width (64 or 128; page_size a power of two from 8 to 4096), of the same
+    strides. The last dimension is contiguous, the others may have any
+    strides (multiples of 8): token-major pages are passed as
+    ``pages.transpose(1, 2)``, halves of one tensor as ``kv[:, 0]``, ``kv[:, 1]``."""
+
+    def __init__(self, k, v):
+        import torch
+
+        for what, t in (("k", k), ("v", v)):
+            if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1:
+                raise ValueError(f"{what} must be a bf16 CUDA tensor of pages x heads x page_size x width")
+        if k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("k and v must have the same shape and strides")
+        _same_device(k, v)
+        self.k, self.v = k, v
+        self.pages, self.heads, self.page_size, self.head_dim = k.shape
+        self.device = k.device
+        self._plan = KVCachePlan(k.data_ptr(), v.data_ptr(), *(k.shape[i] for i in (0, 2, 1, 3)), *k.stride()[:3])
+        self._ref = ctypes.byref(self._plan)
+
+
+class KVBatch:
+    """Sequences whose new tokens are rows of packed tensors (int32, on the GPU; the
+    kernels read them when they run).
+
+    q_start: B + 1, sequence b's new tokens are rows q_start[b] to q_start[b + 1] - 1.
+    kv_len: B, tokens of each sequence in the cache, the new ones included.
+    block_table: B x pages of a sequence, rows contiguous: its tokens i * page_size
+    and on lie in page block_table[b, i]."""
+
+    def __init__(self, q_start, kv_len, block_table):
+        import torch
+
+        B = kv_len.shape[0] if kv_len.dim() == 1 else -1
+        _check(kv_len, torch.int32, (B,), "kv_len")
+        _check(q_start, torch.int32, (B + 1,), "q_start")
+        if (not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or
+                block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+            raise ValueError(f"block_table must be an int32 CUDA tensor of {B} rows, each contiguous")
+        _same_device(kv_len, q_start, block_table)
+        self.q_start, self.kv_len, self.block_table = q_start, kv_len, block_table
+        self.sequences = B
+        self.device = kv_len.device
+        self._plans: dict = {}
+
+    def _ref(self, tokens: int):
+        ref = self._plans.get(tokens)
+        if ref is None:
+            t = self.block_table
+            ref = ctypes.byref(KVBatchPlan(self.sequences, tokens, self.q_start.data_ptr(), self.kv_len.data_ptr(),
+                                           t.data_ptr(), t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]))
+            if len(self._plans) > 64:
+                self._plans.clear()
+            self._plans[tokens] = ref
+        return ref
+
+
+def cache_append(q, k, v, cache: KVCache, batch: KVBatch, rotary: Rotary | None = None, positions=None, q_out=None,
+                 ctx: Context | None = None, stream=None):
+    """Write new keys and values (tokens x heads x width, bf16) into the cache's pages, row by
+    row to the places that ``batch`` gives them.
+
+    With ``rotary``, keys are rotated on the way by their place in the sequence (or by
+    ``positions``, one per row), and so is ``q`` (tokens x query heads x width, or None):
+    returns it rotated, in ``q_out`` or a new tensor (``q_out`` may be ``q``). Without ``rotary`` q must be None.
+    Rows that belong to no sequence are left out."""
+    import torch
+
+    D, dev = cache.head_dim, cache.device
+    N, Hk, Dk, ldk = _check_heads(k, torch.bfloat16, "k")
+    Nv, Hv, Dv, ldv = _check_heads(v, torch.bfloat16, "v")
+    if (Hk, Dk) != (cache.heads, D) or (Nv, Hv, Dv) != (N, Hk, Dk):
+        raise ValueError(f"k and v must be tokens x {cache.heads} x {D}, got {tuple(k.shape)} and {tuple(v.shape)}")
+    H = ldq = ldo = 0
+    if q is not None:
+        Nq, H, Dq, ldq = _check_heads(q, torch.bfloat16, "q")
+        if (Nq, Dq) != (N, D):
+            raise ValueError(f"q must be {N} x heads x {D}, got {tuple(q.shape)}")
+        if rotary is None:
+            raise ValueError("q is only rotated: without a rotary plan it must be None")
+        if q_out is None:
+            q_out = torch.empty((N, H, D), dtype=torch.bfloat16, device=dev)
+        No, Ho, Do, ldo = _check_heads(q_out, torch.bfloat16, "q_out")
+        if (No, Ho, Do) != (N, H, D):
+            raise ValueError(f"q_out must have shape {(N, H, D)}, got {tuple(q_out.shape)}")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    ptype = TYPE_INT64
+    if positions is not None:
+        ptype = _index_type(positions, "positions")
+        _check(positions, positions.dtype, (N,), "positions")
+    for t in (q, q_out, k, v, batch, positions, None if rotary is None else rotary.turns):
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+    index = dev.index if dev.index is not None else 0
+    ctx = ctx or default_context(index)
+    rc = library().lin_cache_append(ctx._h, cache._ref, batch._ref(N), H, _ptr(q), ldq, _ptr(q_out), ldo,
+                                    k.data_ptr(), ldk, v.data_ptr(), ldv, _ptr(positions), ptype,
+                                    None if rotary is None else rotary._ref, _stream_ptr(stream, index))
+    if rc != OK:
+        raise LinError(rc, "lin_cache_append")
+    return q_out

@@ -238,6 +238,36 @@ struct LogitsProblem {
 int launch_logprobs(const LogitsProblem& p);
 int launch_distill(const LogitsProblem& p);
 
+// Rotary positions (rotary.cu): up to three groups of heads of D elements, head h of
+// row n at src + n * ld_src + h * D. Without `append` only part 0 is used. With it, part 0
+// is q (to part 0's dst; no heads when there is no rotation), part 1 k and part 2 v
+// (copied); they go to the cache's pages, and positions, unless given, follow from
+// the batch.
+struct RotaryPart {
+    const void* src = nullptr;
+    void* dst = nullptr;
+    long long ld_src = 0, ld_dst = 0;
+    int heads = 0;
+};
+struct RotaryProblem {
+    long long N = 0;
+    int D = 0, rot = 0;            // rot: elements of a head that rotate (even)
+    bool interleaved = false, inverse = false;
+    bool bf16 = true;
+    bool append = false;
+    RotaryPart part[3];
+    const void* positions = nullptr;
+    bool wide = false;             // 64-bit positions
+    const unsigned long long* turns = nullptr;
+    float scale = 1.f;
+    lin_kv_cache cache = {};
+    lin_kv_batch batch = {};
+    cudaStream_t stream = nullptr;
+    int sm_count = 0;
+    bool early_start = false;      // programmatic launch (nothing is read before the dependency wait)
+};
+int launch_rotary(const RotaryProblem& p);
+
 // Kernel timelines (timeline build only, see timeline.cuh): copy up to `bytes`
 // of the stamp array to host memory at `dst` (if not null), then zero it (if
 // `clear`). LIN_ERR_UNSUPPORTED in the library build.

@@ -12,11 +12,13 @@
 //                           tiles cannot fill the SMs
 //   K == 0               -> fill Y = act(bias)
 #include <climits>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
 #include <vector>
 #include <new>
+#include <utility>
 
 #include "internal.h"
 #include "device_common.cuh"
@@ -1256,6 +1258,237 @@ int lin_distill_forward_backward(lin_ctx* ctx, int R, int V, int K, const void* 
                                  const float* weight, float* loss, void* dlogits, long long ldd, void* stream) {
     return distill_run(ctx, R, V, K, logits, ld, logits_type, ids, ids_type, teacher, teacher_type, tau, weight,
                        nullptr, loss, nullptr, dlogits, ldd, true, stream);
+}
+
+// ---- rotary positions and the paged cache ----
+
+int lin_rotary_turns(const double* frequencies, int n, unsigned long long* turns) {
+    if (n < 0 || (n > 0 && (!frequencies || !turns))) return LIN_ERR_ARG;
+    for (int i = 0; i < n; ++i)
+        if (!std::isfinite(frequencies[i])) return LIN_ERR_ARG;
+    for (int i = 0; i < n; ++i) {
+        const double t = frequencies[i] / 6.283185307179586476925;
+        double part = t - std::floor(t);  // [0, 1], 1 when a tiny negative rounds up
+        if (part >= 1.0) part = 0.0;
+        turns[i] = static_cast<unsigned long long>(std::ldexp(part, 64));
+    }
+    return LIN_OK;
+}
+
+namespace {
+
+constexpr int kMaxHeadDim = 1024;
+
+// N rows of `width` elements of `esz` bytes, `ld` elements apart.
+struct Rows {
+    const void* p;
+    long long N, width, ld;
+    size_t esz;
+};
+
+size_t rows_extent(const Rows& r) { return r.p && r.N > 0 && r.width > 0 ? ((size_t)(r.N - 1) * r.ld + r.width) * r.esz : 0; }
+
+// Whether two sets of rows share an element. Rows of the same stride may interleave
+// (columns of one matrix); others overlap when their extents do.
+bool rows_overlap(const Rows& a, const Rows& b) {
+    if (!lin::overlaps(a.p, rows_extent(a), b.p, rows_extent(b))) return false;
+    const long long la = a.ld * (long long)a.esz, lb = b.ld * (long long)b.esz;
+    const bool same = la == lb || a.N == 1 || b.N == 1;
+    if (!same) return true;
+    const long long ld = a.N == 1 ? lb : la;
+    if (a.N == 1 && b.N == 1) return true;
+    const long long wa = a.width * (long long)a.esz, wb = b.width * (long long)b.esz;
+    long long d = (long long)(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p)) % ld;
+    if (d < 0) d += ld;
+    return !(d >= wa && ld - d >= wb);
+}
+
+int rotary_ok(const lin_rotary* r, int D) {
+    if (!r || r->dim < 0 || r->dim > D || r->dim % 2 != 0 || (r->dim > 0 && !r->turns) || !std::isfinite(r->scale) ||
+        (r->layout != LIN_ROTARY_HALF && r->layout != LIN_ROTARY_INTERLEAVED))
+        return LIN_ERR_ARG;
+    return (uintptr_t)r->turns % 8 != 0 ? LIN_ERR_ALIGN : LIN_OK;
+}
+
+// Largest row stride that is taken, and extent of a cache (elements).
+constexpr long long kMaxStride = 1ll << 30, kMaxCache = 1ll << 46;
+
+int rotary_run(lin_ctx* ctx, int N, int H, int D, const void* x, long long ldx, void* y, long long ldy, int type,
+               const void* positions, int positions_type, const lin_rotary* rotary, bool inverse, void* stream) {
+    using namespace lin;
+    if (!ctx || N < 0 || H < 0 || D < 0 || !float_type(type) || !index_type(positions_type)) return LIN_ERR_ARG;
+    if (D > kMaxHeadDim) return LIN_ERR_UNSUPPORTED;
+    const int ok = rotary_ok(rotary, D);
+    if (ok != LIN_OK) return ok;
+    if (N == 0 || H == 0 || D == 0) return LIN_OK;
+    const long long width = (long long)H * D;
+    if (!x || !y || !positions || ldx < width || ldy < width) return LIN_ERR_ARG;
+    if (width > (1 << 27) || ldx > kMaxStride || ldy > kMaxStride) return LIN_ERR_UNSUPPORTED;
+    const size_t esz = type_bytes(type), psz = type_bytes(positions_type);
+    const Rows in{x, N, width, ldx, esz}, out{y, N, width, ldy, esz};
+    const bool in_place = x == y && (ldx == ldy || N == 1);
+    if (!in_place && rows_overlap(out, in)) return LIN_ERR_ARG;
+    const size_t turn_bytes = (size_t)rotary->dim / 2 * 8;
+    if (rows_overlap(out, Rows{positions, 1, N, N, psz}) ||
+        rows_overlap(out, Rows{rotary->turns, 1, (long long)turn_bytes, (long long)turn_bytes, 1}))
+        return LIN_ERR_ARG;
+    if (((uintptr_t)x | (uintptr_t)y) % esz != 0 || (uintptr_t)positions % psz != 0) return LIN_ERR_ALIGN;
+    DeviceGuard guard(ctx->device);
+    if (!guard.ok) return LIN_ERR_CUDA;
+    RotaryProblem p;
+    p.N = N;
+    p.D = D;
+    p.rot = rotary->dim;
+    p.interleaved = rotary->layout == LIN_ROTARY_INTERLEAVED;
+    p.inverse = inverse;
+    p.bf16 = type == LIN_TYPE_BF16;
+    p.part[0] = RotaryPart{x, y, ldx, ldy, H};
+    p.positions = positions;
+    p.wide = positions_type == LIN_TYPE_INT64;
+    p.turns = rotary->turns;
+    p.scale = rotary->scale;
+    p.stream = static_cast<cudaStream_t>(stream);
+    p.sm_count = ctx->sm_count;
+    p.early_start = ctx->programmatic;
+    const Range hull{y, rows_extent(out)};
+    note_output(p.stream, hull);
+    return launched(launch_rotary(p), p.stream, hull);
+}
+
+// Elements from a cache's first to its last.
+size_t cache_extent(const lin_kv_cache& c) {
+    return ((size_t)(c.pages - 1) * c.page_stride + (size_t)(c.heads - 1) * c.head_stride +
+            (size_t)(c.page_size - 1) * c.token_stride + c.head_dim) * 2;
+}
+
+// Whether the cache's rows of head_dim elements, k's and v's, lie apart: strides taken
+// from the smallest, each at least the extent of those below it. Strides of a
+// single page, head or slot do not count; v is a second copy at its distance from k.
+bool cache_rows_apart(const lin_kv_cache& c) {
+    const uintptr_t k = reinterpret_cast<uintptr_t>(c.k), v = reinterpret_cast<uintptr_t>(c.v);
+    const uintptr_t apart = (k < v ? v - k : k - v) / 2;
+    long long n[4] = {c.pages, c.heads, c.page_size, 2};
+    long long s[4] = {c.page_stride, c.head_stride, c.token_stride, (long long)(apart > (uintptr_t)kMaxCache * 4 ? kMaxCache * 4 : apart)};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 4; ++j)
+            if (s[j] < s[i]) {
+                std::swap(s[i], s[j]);
+                std::swap(n[i], n[j]);
+            }
+    long long extent = c.head_dim;
+    for (int i = 0; i < 4; ++i) {
+        if (n[i] == 1) continue;
+        if (s[i] < extent) return false;
+        extent = (n[i] - 1) * s[i] + extent;
+    }
+    return true;
+}
+
+int cache_ok(const lin_kv_cache* c, const lin_kv_batch* b) {
+    if (!c || !b || c->pages < 0 || c->heads < 1 || c->page_size < 1 || c->head_dim < 1 || b->sequences < 0 ||
+        b->tokens < 0 || b->table_pages < 0 || b->table_stride < b->table_pages)
+        return LIN_ERR_ARG;
+    if ((c->page_size & (c->page_size - 1)) != 0 || c->page_size < 8 || c->page_size > 4096 ||
+        (c->head_dim != 64 && c->head_dim != 128) || c->heads > 65535 || b->table_stride > kMaxStride ||
+        (long long)b->table_pages * c->page_size > INT_MAX)
+        return LIN_ERR_UNSUPPORTED;
+    if (b->tokens > 0 && b->sequences > 0 && (!b->q_start || !b->kv_len || (b->table_pages > 0 && !b->block_table)))
+        return LIN_ERR_ARG;
+    if (((uintptr_t)b->q_start | (uintptr_t)b->kv_len | (uintptr_t)b->block_table) % 4 != 0) return LIN_ERR_ALIGN;
+    if (c->pages == 0) return LIN_OK;
+    if (!c->k || !c->v) return LIN_ERR_ARG;
+    const long long strides[] = {c->page_stride, c->head_stride, c->token_stride};
+    const int counts[] = {c->pages, c->heads, c->page_size};
+    for (int i = 0; i < 3; ++i) {
+        if (strides[i] < 0) return LIN_ERR_ARG;
+        if (strides[i] > kMaxCache / counts[i]) return LIN_ERR_UNSUPPORTED;
+    }
+    if (!cache_rows_apart(*c)) return LIN_ERR_ARG;
+    if (((uintptr_t)c->k | (uintptr_t)c->v) % 16 != 0 || c->token_stride % 8 != 0 ||
+        (c->heads > 1 && c->head_stride % 8 != 0) || (c->pages > 1 && c->page_stride % 8 != 0))
+        return LIN_ERR_ALIGN;
+    return LIN_OK;
+}
+
+// Rows of table entries as an operand of the overlap checks.
+Rows table_rows(const lin_kv_batch& b) {
+    return Rows{b.block_table, b.sequences, b.table_pages, b.table_stride, 4};
+}
+
+}  // namespace
+
+int lin_rotary_forward(lin_ctx* ctx, int N, int H, int D, const void* x, long long ldx, void* y, long long ldy,
+                       int type, const void* positions, int positions_type, const lin_rotary* rotary, void* stream) {
+    return rotary_run(ctx, N, H, D, x, ldx, y, ldy, type, positions, positions_type, rotary, false, stream);
+}
+
+int lin_rotary_backward(lin_ctx* ctx, int N, int H, int D, const void* dy, long long lddy, void* dx, long long lddx,
+                        int type, const void* positions, int positions_type, const lin_rotary* rotary, void* stream) {
+    return rotary_run(ctx, N, H, D, dy, lddy, dx, lddx, type, positions, positions_type, rotary, true, stream);
+}
+
+int lin_cache_append(lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_batch* batch, int H, const void* q,
+                     long long ldq, void* q_out, long long ldqo, const void* k, long long ldk, const void* v,
+                     long long ldv, const void* positions, int positions_type, const lin_rotary* rotary,
+                     void* stream) {
+    using namespace lin;
+    if (!ctx || H < 0 || (positions && !index_type(positions_type))) return LIN_ERR_ARG;
+    int ok = cache_ok(cache, batch);
+    if (ok != LIN_OK) return ok;
+    const int D = cache->head_dim;
+    if (rotary && (ok = rotary_ok(rotary, D)) != LIN_OK) return ok;
+    if (H > 0 ? !rotary : (q || q_out)) return LIN_ERR_ARG;
+    if (batch->tokens == 0 || batch->sequences == 0) return LIN_OK;
+    const long long N = batch->tokens, wq = (long long)H * D, wk = (long long)cache->heads * D;
+    if (!k || !v || ldk < wk || ldv < wk || (H > 0 && (!q || !q_out || ldq < wq || ldqo < wq))) return LIN_ERR_ARG;
+    if (wq > (1 << 27) || ldk > kMaxStride || ldv > kMaxStride || (H > 0 && (ldq > kMaxStride || ldqo > kMaxStride)))
+        return LIN_ERR_UNSUPPORTED;
+    const size_t psz = positions ? type_bytes(positions_type) : 4;
+    const size_t held = cache->pages > 0 ? cache_extent(*cache) : 0;
+    auto flat = [](const void* p, size_t bytes) { return Rows{p, 1, (long long)bytes, (long long)bytes, 1}; };
+    const Rows rq{H > 0 ? q : nullptr, N, wq, ldq, 2}, rqo{H > 0 ? q_out : nullptr, N, wq, ldqo, 2};
+    const Rows rk{k, N, wk, ldk, 2}, rv{v, N, wk, ldv, 2};
+    const Rows kc = flat(cache->k, held), vc = flat(cache->v, held);
+    const Rows inputs[] = {rk, rv, table_rows(*batch), flat(batch->q_start, 4 * ((size_t)batch->sequences + 1)),
+                           flat(batch->kv_len, 4 * (size_t)batch->sequences), flat(positions, positions ? N * psz : 0),
+                           flat(rotary ? rotary->turns : nullptr, rotary ? (size_t)rotary->dim / 2 * 8 : 0)};
+    for (const Rows& r : inputs)
+        if (rows_overlap(rqo, r) || rows_overlap(kc, r) || rows_overlap(vc, r)) return LIN_ERR_ARG;
+    if (!(q == q_out && (ldq == ldqo || N == 1)) && rows_overlap(rqo, rq)) return LIN_ERR_ARG;
+    if (rows_overlap(kc, rq) || rows_overlap(vc, rq) || rows_overlap(kc, rqo) || rows_overlap(vc, rqo)) return LIN_ERR_ARG;
+    if (((uintptr_t)k | (uintptr_t)v | (uintptr_t)q | (uintptr_t)q_out) % 2 != 0 || (uintptr_t)positions % psz != 0)
+        return LIN_ERR_ALIGN;
+    DeviceGuard guard(ctx->device);
+    if (!guard.ok) return LIN_ERR_CUDA;
+    RotaryProblem p;
+    p.N = N;
+    p.D = D;
+    p.rot = rotary ? rotary->dim : 0;
+    p.interleaved = rotary && rotary->layout == LIN_ROTARY_INTERLEAVED;
+    p.append = true;
+    p.part[0] = RotaryPart{q, q_out, ldq, ldqo, H};
+    p.part[1] = RotaryPart{k, cache->k, ldk, cache->token_stride, cache->heads};
+    p.part[2] = RotaryPart{v, cache->v, ldv, cache->token_stride, cache->heads};
+    p.positions = positions;
+    p.wide = positions_type == LIN_TYPE_INT64;
+    p.turns = rotary ? rotary->turns : nullptr;
+    p.scale = rotary ? rotary->scale : 1.f;
+    p.cache = *cache;
+    p.batch = *batch;
+    p.stream = static_cast<cudaStream_t>(stream);
+    p.sm_count = ctx->sm_count;
+    p.early_start = ctx->programmatic;
+    uintptr_t lo = UINTPTR_MAX, hi = 0;
+    for (const Rows& r : {rqo, kc, vc}) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(r.p);
+        const size_t n = rows_extent(r);
+        if (n == 0) continue;
+        lo = a < lo ? a : lo;
+        hi = a + n > hi ? a + n : hi;
+    }
+    const Range hull{hi ? reinterpret_cast<const void*>(lo) : nullptr, hi ? hi - lo : 0};
+    note_output(p.stream, hull);
+    return launched(launch_rotary(p), p.stream, hull);
 }
 
 int lin_check_device(lin_ctx* ctx, void* stream) {
