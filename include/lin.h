@@ -628,7 +628,7 @@ LIN_API int lin_rotary_backward(lin_ctx* ctx, int N, int H, int D, const void* d
 typedef struct {
     void* k;                  /* DEVICE, 16-byte aligned */
     void* v;
-    int pages;
+    int pages;                /* at least 1 */
     int page_size;            /* tokens a page holds: a power of two, 8 to 4096 */
     int heads;                /* key (and value) heads */
     int head_dim;             /* 64 or 128 */
@@ -670,6 +670,39 @@ LIN_API int lin_cache_append(lin_ctx* ctx, const lin_kv_cache* cache, const lin_
                              long long ldq, void* q_out, long long ldqo, const void* k, long long ldk, const void* v,
                              long long ldv, const void* positions, int positions_type, const lin_rotary* rotary,
                              void* stream);
+
+/* Attention of the batch's new tokens over the paged cache (which holds their own keys
+ * and values already, see lin_cache_append). Row n, the i-th of the n_b new tokens of sequence b, at
+ * position p = kv_len[b] - n_b + i, query head h, reading key head g = h / (H / heads):
+ *   s_j = (q_nh . K_bgj) scale   for the keys j that it sees: j <= p when causal, else all
+ *         j < kv_len[b]           (a cross attention's encoder states)
+ *   out[n * ldo + h * head_dim ..] = sum_j exp(s_j - m) V_bgj / sum_j exp(s_j - m),  m = max_j s_j
+ *   lse[n * H + h] = log sum_j exp(s_j)            (when lse is not NULL)
+ * A row that sees no key (an empty sequence, or one that holds fewer keys than it has new tokens)
+ * has out 0 and lse -inf; so has one whose scores are all -inf. Rows of no sequence are
+ * left as they were. kv_len is taken as 0 below 0, and up to table_pages * page_size; what lies on a page that is
+ * none of the cache's reads as zeros. Whatever the arrays hold, nothing outside the
+ * operands is read or written.
+ *   q, out : tokens x H heads of head_dim, bf16, 16-byte aligned, rows ldq and ldo apart (multiples of 8).
+ *   H      : a multiple of cache->heads, at most 32 times as many.
+ *   scale  : > 0; 0 selects 1/sqrt(head_dim).
+ *   max_new: about how many new tokens the longest sequence has (0: as many as the average); it picks the
+ *            kernel, and any value gives right results.
+ *   workspace: DEVICE, 16-byte aligned, of lin_paged_attention_workspace's size for the same max_new: parts of
+ *            items that several blocks share. NULL: the context's own (LIN_ERR_WORKSPACE when it is too
+ *            small); calls that may run at the same time, captured ones included, need one each.
+ * Arithmetic: bf16 products summed in fp32, softmax in fp32, probabilities rounded to bf16 for the product with V,
+ * one rounding of the output. Sums are split by the lengths and the device alone: results repeat bit
+ * for bit. A NaN or infinity in a key or value that some row of a sequence's new tokens sees may
+ * reach all of that sequence's rows; slots that no row sees may hold anything. Reads and writes
+ * only after the previous kernel on the stream has finished. */
+LIN_API int lin_paged_attention(lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_batch* batch, int H, const void* q,
+                                long long ldq, void* out, long long ldo, float* lse, int causal, float scale,
+                                int max_new, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that such a call needs (host only; batch may be NULL when max_new is given). */
+LIN_API int lin_paged_attention_workspace(const lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_batch* batch,
+                                          int H, int max_new, size_t* bytes);
 
 #ifdef __cplusplus
 }

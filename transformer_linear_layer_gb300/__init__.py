@@ -24,7 +24,7 @@ __all__ = [
     "LinError", "Context", "Plan", "forward", "forward_plan", "plan_query", "plan_make", "build",
     "backward_data", "backward_weight", "gelu_backward", "attention_forward", "attention_backward",
     "TokenLogprobs", "token_logprobs", "distill_forward", "distill_backward", "distill_forward_backward",
-    "Rotary", "rotary_forward", "rotary_backward", "KVCache", "KVBatch", "cache_append",
+    "Rotary", "rotary_forward", "rotary_backward", "KVCache", "KVBatch", "cache_append", "paged_attention",
     "library", "PREC_FP32", "PREC_TF32", "PREC_BF16", "EPI_NONE", "EPI_GELU_TANH",
     "KERNEL_NONE", "KERNEL_FILL", "KERNEL_SKINNY", "KERNEL_FFMA", "KERNEL_TC", "KERNEL_GEMV",
 ]
@@ -151,6 +151,8 @@ def library() -> ctypes.CDLL:
                 "lin_rotary_forward": ([P, I, I, I, P, L, P, L, I, P, I, P, P], I),
                 "lin_rotary_backward": ([P, I, I, I, P, L, P, L, I, P, I, P, P], I),
                 "lin_cache_append": ([P, P, P, I, P, L, P, L, P, L, P, L, P, I, P, P], I),
+                "lin_paged_attention": ([P, P, P, I, P, L, P, L, P, I, F, I, P, Z, P], I),
+                "lin_paged_attention_workspace": ([P, P, P, I, I, ctypes.POINTER(Z)], I),
                 "lin_strerror": ([I], ctypes.c_char_p),
                 "lin_abi_version": ([], I),
             }
@@ -1037,3 +1039,74 @@ def cache_append(q, k, v, cache: KVCache, batch: KVBatch, rotary: Rotary | None 
     if rc != OK:
         raise LinError(rc, "lin_cache_append")
     return q_out
+
+
+def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scale: float | None = None,
+                    max_new: int | None = None, out=None, lse=None, with_lse: bool = False, workspace=None,
+                    ctx: Context | None = None, stream=None):
+    """Attention of the batch's new tokens over the cache, which holds their own keys and values already
+    (:func:`cache_append`).
+
+    q: tokens x query heads x width, bf16, rows any multiple of 8 elements apart; query heads a multiple
+    (at most 32) of the cache's. causal: each token sees the keys up to its own place; otherwise all of its
+    sequence's (a cross attention over an encoder's states). max_new: about how many new
+    tokens the longest sequence has (default: the average), which picks the kernel; any value is
+    right. Returns out (like q, contiguous), or (out, lse) with lse tokens x heads fp32 when ``with_lse`` or an lse
+    tensor is given. Rows that belong to no sequence are not written. workspace: a uint8 tensor of
+    :func:`paged_attention_workspace` bytes (default: from torch's allocator, for this call)."""
+    import torch
+
+    N, H, D, ldq = _check_heads(q, torch.bfloat16, "q")
+    dev = cache.device
+    if D != cache.head_dim:
+        raise ValueError(f"q must be tokens x heads x {cache.head_dim}, got {tuple(q.shape)}")
+    if out is None:
+        out = torch.empty((N, H, D), dtype=torch.bfloat16, device=dev)
+    No, Ho, Do, ldo = _check_heads(out, torch.bfloat16, "out")
+    if (No, Ho, Do) != (N, H, D):
+        raise ValueError(f"out must have shape {(N, H, D)}, got {tuple(out.shape)}")
+    if lse is None and with_lse:
+        lse = torch.empty((N, H), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _check(lse, torch.float32, (N, H), "lse")
+    for t in (q, out, lse, batch, workspace):
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+    index = dev.index if dev.index is not None else 0
+    ctx = ctx or default_context(index)
+    hint = 0 if max_new is None else int(max_new)
+    raw = _stream_ptr(stream, index)
+    if workspace is None:
+        workspace = _scratch(paged_attention_workspace(cache, batch, N, H, hint, ctx), dev, stream)
+    rc = library().lin_paged_attention(ctx._h, cache._ref, batch._ref(N), H, q.data_ptr(), ldq, out.data_ptr(), ldo,
+                                       _ptr(lse), int(bool(causal)), 0.0 if scale is None else float(scale), hint,
+                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
+    if rc != OK:
+        raise LinError(rc, "lin_paged_attention")
+    return (out, lse) if lse is not None else out
+
+
+def paged_attention_workspace(cache: KVCache, batch: KVBatch, tokens: int, heads: int, max_new: int = 0,
+                              ctx: Context | None = None) -> int:
+    """Bytes of workspace that :func:`paged_attention` needs for such a call."""
+    ctx = ctx or default_context(cache.device.index or 0)
+    size = ctypes.c_size_t()
+    rc = library().lin_paged_attention_workspace(ctx._h, cache._ref, batch._ref(tokens), heads, max_new,
+                                                 ctypes.byref(size))
+    if rc != OK:
+        raise LinError(rc, "lin_paged_attention_workspace")
+    return size.value
+
+
+def _scratch(size, device, stream):
+    """Bytes from torch's allocator for one call's kernels, taken on the stream that they
+    run on (the memory may still be in use by earlier work of any other)."""
+    import torch
+
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
+                                           device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device=device)

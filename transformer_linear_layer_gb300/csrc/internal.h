@@ -268,6 +268,29 @@ struct RotaryProblem {
 };
 int launch_rotary(const RotaryProblem& p);
 
+// Attention of new tokens over a paged cache, for tiles of at most 16 or 32 rows (paged_rows.cu).
+struct PagedProblem {
+    lin_kv_cache cache = {};
+    lin_kv_batch batch = {};
+    int H = 0;                     // query heads
+    const void* q = nullptr;
+    long long ldq = 0;
+    void* out = nullptr;
+    long long ldo = 0;
+    float* lse = nullptr;
+    bool causal = true;
+    float scale = 0.f;             // softmax scale (> 0)
+    cudaStream_t stream = nullptr;
+    void* workspace = nullptr;
+    size_t workspace_bytes = 0;
+    int* dev_status = nullptr;
+    int sm_count = 0;
+    bool early_start = false;      // programmatic launch (nothing is read before the dependency wait)
+};
+constexpr int kPagedRowsMax = 32;  // rows of a tile, at least a key head's query heads
+size_t paged_rows_workspace(int sm_count, int rows, int D);
+int launch_paged_rows(const PagedProblem& p, int rows);
+
 // Kernel timelines (timeline build only, see timeline.cuh): copy up to `bytes`
 // of the stamp array to host memory at `dst` (if not null), then zero it (if
 // `clear`). LIN_ERR_UNSUPPORTED in the library build.

@@ -11,6 +11,7 @@
 //   FP32                 -> FFMA kernel; 64x64 tiles + split-K when 128x128
 //                           tiles cannot fill the SMs
 //   K == 0               -> fill Y = act(bias)
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdio>
@@ -1385,7 +1386,7 @@ bool cache_rows_apart(const lin_kv_cache& c) {
 }
 
 int cache_ok(const lin_kv_cache* c, const lin_kv_batch* b) {
-    if (!c || !b || c->pages < 0 || c->heads < 1 || c->page_size < 1 || c->head_dim < 1 || b->sequences < 0 ||
+    if (!c || !b || c->pages < 1 || c->heads < 1 || c->page_size < 1 || c->head_dim < 1 || b->sequences < 0 ||
         b->tokens < 0 || b->table_pages < 0 || b->table_stride < b->table_pages)
         return LIN_ERR_ARG;
     if ((c->page_size & (c->page_size - 1)) != 0 || c->page_size < 8 || c->page_size > 4096 ||
@@ -1395,7 +1396,6 @@ int cache_ok(const lin_kv_cache* c, const lin_kv_batch* b) {
     if (b->tokens > 0 && b->sequences > 0 && (!b->q_start || !b->kv_len || (b->table_pages > 0 && !b->block_table)))
         return LIN_ERR_ARG;
     if (((uintptr_t)b->q_start | (uintptr_t)b->kv_len | (uintptr_t)b->block_table) % 4 != 0) return LIN_ERR_ALIGN;
-    if (c->pages == 0) return LIN_OK;
     if (!c->k || !c->v) return LIN_ERR_ARG;
     const long long strides[] = {c->page_stride, c->head_stride, c->token_stride};
     const int counts[] = {c->pages, c->heads, c->page_size};
@@ -1444,7 +1444,7 @@ int lin_cache_append(lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_batch
     if (wq > (1 << 27) || ldk > kMaxStride || ldv > kMaxStride || (H > 0 && (ldq > kMaxStride || ldqo > kMaxStride)))
         return LIN_ERR_UNSUPPORTED;
     const size_t psz = positions ? type_bytes(positions_type) : 4;
-    const size_t held = cache->pages > 0 ? cache_extent(*cache) : 0;
+    const size_t held = cache_extent(*cache);
     auto flat = [](const void* p, size_t bytes) { return Rows{p, 1, (long long)bytes, (long long)bytes, 1}; };
     const Rows rq{H > 0 ? q : nullptr, N, wq, ldq, 2}, rqo{H > 0 ? q_out : nullptr, N, wq, ldqo, 2};
     const Rows rk{k, N, wk, ldk, 2}, rv{v, N, wk, ldv, 2};
@@ -1489,6 +1489,95 @@ int lin_cache_append(lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_batch
     const Range hull{hi ? reinterpret_cast<const void*>(lo) : nullptr, hi ? hi - lo : 0};
     note_output(p.stream, hull);
     return launched(launch_rotary(p), p.stream, hull);
+}
+
+namespace {
+
+// Rows of a tile that the call is made for: the new tokens of a sequence with
+// the query heads of a key head.
+int paged_rows(const lin_kv_cache& cache, const lin_kv_batch* batch, int H, int max_new) {
+    long long n = max_new;
+    if (n == 0 && batch && batch->sequences > 0)
+        n = ((long long)batch->tokens + batch->sequences - 1) / batch->sequences;
+    const long long rows = (n < 1 ? 1 : n) * (H / cache.heads);
+    return rows > INT_MAX ? INT_MAX : (int)rows;
+}
+
+int paged_heads_ok(const lin_kv_cache* c, int H, int max_new) {
+    if (!c || H < 1 || c->heads < 1 || max_new < 0 || H % c->heads != 0) return LIN_ERR_ARG;
+    if ((c->head_dim != 64 && c->head_dim != 128) || H / c->heads > lin::kPagedRowsMax || H > 65535)
+        return LIN_ERR_UNSUPPORTED;
+    return LIN_OK;
+}
+
+}  // namespace
+
+int lin_paged_attention_workspace(const lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_batch* batch, int H,
+                                  int max_new, size_t* bytes) {
+    if (!ctx || !bytes || (max_new == 0 && !batch)) return LIN_ERR_ARG;
+    const int ok = paged_heads_ok(cache, H, max_new);
+    if (ok != LIN_OK) return ok;
+    *bytes = lin::paged_rows_workspace(ctx->sm_count, paged_rows(*cache, batch, H, max_new), cache->head_dim);
+    return LIN_OK;
+}
+
+int lin_paged_attention(lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_batch* batch, int H, const void* q,
+                        long long ldq, void* out, long long ldo, float* lse, int causal, float scale, int max_new,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+    using namespace lin;
+    if (!ctx || (causal != 0 && causal != 1) || !(scale >= 0.f) || std::isinf(scale) || H < 0) return LIN_ERR_ARG;
+    int ok = cache_ok(cache, batch);
+    if (ok != LIN_OK) return ok;
+    if (H == 0 || batch->tokens == 0 || batch->sequences == 0) return LIN_OK;
+    if ((ok = paged_heads_ok(cache, H, max_new)) != LIN_OK) return ok;
+    const long long N = batch->tokens, width = (long long)H * cache->head_dim;
+    if (!q || !out || ldq < width || ldo < width) return LIN_ERR_ARG;
+    if (ldq > kMaxStride || ldo > kMaxStride || batch->sequences > (1 << 24)) return LIN_ERR_UNSUPPORTED;
+    if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) % 16 != 0 || ldq % 8 != 0 || ldo % 8 != 0 ||
+        (uintptr_t)lse % 4 != 0)
+        return LIN_ERR_ALIGN;
+    if (!workspace) {
+        workspace_bytes = ctx->workspace_bytes > kCounterBytes ? ctx->workspace_bytes - kCounterBytes : 0;
+        workspace = static_cast<char*>(ctx->workspace) + kCounterBytes;
+    }
+    const int rows = paged_rows(*cache, batch, H, max_new);
+    if (workspace_bytes < paged_rows_workspace(ctx->sm_count, rows, cache->head_dim)) return LIN_ERR_WORKSPACE;
+    auto flat = [](const void* p, size_t bytes) { return Rows{p, 1, (long long)bytes, (long long)bytes, 1}; };
+    const size_t held = cache_extent(*cache), lse_bytes = lse ? (size_t)N * H * 4 : 0;
+    const Rows ro{out, N, width, ldo, 2}, rl = flat(lse, lse_bytes), rw = flat(workspace, workspace_bytes);
+    const Rows inputs[] = {Rows{q, N, width, ldq, 2}, flat(cache->k, held), flat(cache->v, held), table_rows(*batch),
+                           flat(batch->q_start, 4 * ((size_t)batch->sequences + 1)),
+                           flat(batch->kv_len, 4 * (size_t)batch->sequences)};
+    for (const Rows& r : inputs)
+        if (rows_overlap(ro, r) || rows_overlap(rl, r) || rows_overlap(rw, r)) return LIN_ERR_ARG;
+    if (rows_overlap(ro, rl) || rows_overlap(ro, rw) || rows_overlap(rl, rw)) return LIN_ERR_ARG;
+    DeviceGuard guard(ctx->device);
+    if (!guard.ok) return LIN_ERR_CUDA;
+    PagedProblem p;
+    p.cache = *cache;
+    p.batch = *batch;
+    p.H = H;
+    p.q = q;
+    p.ldq = ldq;
+    p.out = out;
+    p.ldo = ldo;
+    p.lse = lse;
+    p.causal = causal != 0;
+    p.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)cache->head_dim);
+    p.stream = static_cast<cudaStream_t>(stream);
+    p.workspace = workspace;
+    p.workspace_bytes = workspace_bytes;
+    p.dev_status = ctx->dev_status;
+    p.sm_count = ctx->sm_count;
+    p.early_start = ctx->programmatic;
+    Range hull{out, rows_extent(ro)};
+    if (lse) {
+        const char* lo = std::min(static_cast<const char*>(out), reinterpret_cast<const char*>(lse));
+        const char* hi = std::max(static_cast<const char*>(out) + hull.bytes, reinterpret_cast<const char*>(lse) + lse_bytes);
+        hull = Range{lo, (size_t)(hi - lo)};
+    }
+    note_output(p.stream, hull);
+    return launched(launch_paged_rows(p, rows), p.stream, hull);
 }
 
 int lin_check_device(lin_ctx* ctx, void* stream) {

@@ -1,8 +1,25 @@
-// Shared by the kernels of the paged cache.
+// Shared by the kernels of the paged cache: finding a row's sequence, the division of
+// attention's work over the blocks of a persistent grid, and the joining of
+// what several of them computed of one item.
+//
+// Work. A tile is up to TQ = R / G new tokens of a sequence with the G query heads
+// that share a key head: R or fewer rows (token, head) of one product with the key head's keys.
+// An item is a tile of one key head, a unit is KB keys of an item. The units of
+// the call, sequence by sequence, tile by tile, head by head, key block by key block, form
+// one line, and each block of the grid takes an equal stretch of it. Lengths lie
+// on the device, so every block adds up the sequences' units itself. An item that a
+// stretch's end cuts is computed in parts: each block leaves its rows' sums (not
+// divided), maxima and totals in the workspace, and a second kernel joins them in the order of
+// the blocks. Which block has which units depends on the lengths and the grid alone, so
+// results repeat bit for bit, and no block waits for another.
 #pragma once
 
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include "device_common.cuh"
+#include "internal.h"
+#include "tc_common.cuh"
 
 namespace lin {
 
@@ -20,6 +37,239 @@ __device__ __forceinline__ int find_sequence(const int* q_start, int B, int n) {
     }
     const int c = __popc(__ballot_sync(0xffffffffu, lo + lane < hi && q_start[lo + lane] <= n));
     return c == 0 ? -1 : lo + c - 1;
+}
+
+// What a block leaves of an item that starts in its stretch and ends in a later
+// block's: the combining kernel's work list.
+struct PagedCut {
+    int row0, tokens;  // the tile's rows of q
+    int h;             // key head
+    int last;          // the block that ends it; 0 when the block cuts no item
+};
+
+struct PagedArgs {
+    lin_kv_batch batch;
+    int pages, page_size;
+    int Hkv, G, TQ;            // key heads, query heads of each, tokens of a tile
+    int causal;
+    float scale_log2;          // softmax scale times log2(e)
+    uint16_t* out;             // row n, head h at n * ldo + h * D
+    long long ldo;
+    float* lse;                // N x H, or null
+    PagedCut* cuts;            // one a block
+    float2* stats;             // slots x R: maximum (of the scores in base-2 units) and total
+    float* sums;               // slots x R x D; block c has slot 2c for an item that it continues, 2c + 1 for one that it starts
+    int* status;
+};
+
+// A sequence's new rows and what they see.
+struct PagedSeq {
+    int row0, n;   // rows of q
+    int held;      // keys that can be read
+    int pos0;      // position of the first new token
+};
+__device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
+    const int s = a.batch.q_start[b], e = a.batch.q_start[b + 1], kv = a.batch.kv_len[b];
+    PagedSeq q;
+    q.row0 = min(max(s, 0), a.batch.tokens);
+    q.n = max(min(e, a.batch.tokens) - q.row0, 0);
+    const int room = a.batch.table_pages * a.page_size;  // at most INT_MAX
+    q.held = min(max(kv, 0), room);
+    const long long pos = (long long)kv - e + q.row0;
+    q.pos0 = (int)max(min(pos, (1ll << 30) + (1ll << 29)), -(1ll << 30));
+    return q;
+}
+// Keys that some row of tile t sees, and its units (at least one: rows that see
+// nothing are written too).
+__device__ __forceinline__ int tile_seen(const PagedArgs& a, const PagedSeq& q, int t) {
+    const int end = min((t + 1) * a.TQ, q.n);
+    return a.causal ? max(min(q.held, q.pos0 + end), 0) : q.held;
+}
+template <int KB>
+__device__ __forceinline__ int tile_units(const PagedArgs& a, const PagedSeq& q, int t) {
+    return max((tile_seen(a, q, t) + KB - 1) / KB, 1);
+}
+
+// This block's stretch [lo, hi) of the line, and where it starts: unit `off` of
+// sequence b. By all THREADS threads of the block.
+struct PagedStretch {
+    long long lo, hi, per;
+    int b;
+    long long off;
+};
+template <int KB, int THREADS>
+__device__ __forceinline__ PagedStretch paged_stretch(const PagedArgs& a) {
+    static_assert(THREADS % 32 == 0, "whole warps");
+    constexpr int W = THREADS / 32;
+    __shared__ long long s_sum[W];
+    __shared__ long long s_off;
+    __shared__ int s_b;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int B = a.batch.sequences, each = (B + THREADS - 1) / THREADS;
+    const int b0 = min((int)threadIdx.x * each, B), b1 = min(b0 + each, B);
+    auto units = [&](int b) {
+        const PagedSeq q = paged_seq(a, b);
+        long long n = 0;
+        for (int t = 0; t * a.TQ < q.n; ++t) n += tile_units<KB>(a, q, t);
+        return n * a.Hkv;
+    };
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += units(b);
+    long long upto = mine;  // inclusive over the threads
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += v;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < W; ++w) {
+        if (w < warp) upto += s_sum[w];
+        total += s_sum[w];
+    }
+    PagedStretch r;
+    r.per = (total + gridDim.x - 1) / gridDim.x;
+    r.lo = min((long long)blockIdx.x * r.per, total);
+    r.hi = min(r.lo + r.per, total);
+    long long at = upto - mine;
+    if (r.lo < r.hi && at <= r.lo && r.lo < upto) {
+        int b = b0;
+        for (long long u; b + 1 < b1 && at + (u = units(b)) <= r.lo; ++b) at += u;
+        s_b = b;
+        s_off = r.lo - at;
+    }
+    __syncthreads();
+    r.b = s_b;
+    r.off = s_off;
+    return r;
+}
+
+// Walks a stretch item by item.
+template <int KB>
+struct PagedWalk {
+    PagedSeq q;
+    int b, t, h, n;   // sequence, tile, key head, units of the item
+    long long u;      // unit of the line
+    int j;            // unit of the item
+    __device__ __forceinline__ void start(const PagedArgs& a, const PagedStretch& r) {
+        b = r.b;
+        u = r.lo;
+        q = paged_seq(a, b);
+        long long off = r.off;
+        for (t = 0;; ++t) {
+            n = tile_units<KB>(a, q, t);
+            if (off < (long long)n * a.Hkv) break;
+            off -= (long long)n * a.Hkv;
+        }
+        h = (int)(off / n);
+        j = (int)(off - (long long)h * n);
+    }
+    // To the next item's first unit, `k` units on. Only when there is one.
+    __device__ __forceinline__ void next(const PagedArgs& a, int k) {
+        u += k;
+        j = 0;
+        if (++h < a.Hkv) return;
+        h = 0;
+        if ((++t) * a.TQ >= q.n) {
+            t = 0;
+            do {
+                q = paged_seq(a, ++b);
+            } while (q.n == 0 && b + 1 < a.batch.sequences);
+        }
+        n = tile_units<KB>(a, q, t);
+    }
+};
+
+// A row's result: sums over its maximum's scale divided by the total; a row that saw
+// no key (total 0) is zero, with lse -inf.
+__device__ __forceinline__ float row_lse(float m, float l) {
+    return l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+}
+
+// Joins the parts of the items that stretches' ends cut: block c those of the item that
+// block c of the attention kernel started and did not end. A warp a row: maxima of up
+// to 32 parts at once, then the weighted sums, part after part.
+template <int D, int R>
+__global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int c = blockIdx.x;
+    const PagedCut cut = a.cuts[c];
+    if (cut.last <= c) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int parts = cut.last - c + 1;
+    auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+    for (int row = blockIdx.y * 4 + warp; row < cut.tokens * a.G; row += gridDim.y * 4) {
+        float m = -INFINITY;
+        for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.stats[(size_t)slot(i) * R + row].x);
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float base = m == -INFINITY ? 0.f : m;
+        float acc[D / 32] = {}, total = 0.f;
+        for (int i0 = 0; i0 < parts; i0 += 32) {
+            float w = 0.f, l = 0.f;
+            if (i0 + lane < parts) {
+                const float2 s = a.stats[(size_t)slot(i0 + lane) * R + row];
+                w = exp2f(s.x - base);
+                l = s.y * w;
+            }
+            const int k = min(parts - i0, 32);
+#pragma unroll 4
+            for (int i = 0; i < k; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                total += __shfl_sync(0xffffffffu, l, i);
+                const float* src = a.sums + ((size_t)slot(i0 + i) * R + row) * D + lane * (D / 32);
+                if constexpr (D == 64) {
+                    const float2 v = *reinterpret_cast<const float2*>(src);
+                    acc[0] = fmaf(v.x, wi, acc[0]);
+                    acc[1] = fmaf(v.y, wi, acc[1]);
+                } else {
+                    const float4 v = *reinterpret_cast<const float4*>(src);
+                    acc[0] = fmaf(v.x, wi, acc[0]);
+                    acc[1] = fmaf(v.y, wi, acc[1]);
+                    acc[2] = fmaf(v.z, wi, acc[2]);
+                    acc[3] = fmaf(v.w, wi, acc[3]);
+                }
+            }
+        }
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        const int tok = row / a.G, head = cut.h * a.G + row % a.G;
+        uint16_t* dst = a.out + (size_t)(cut.row0 + tok) * a.ldo + (size_t)head * D + lane * (D / 32);
+        if constexpr (D == 64)
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+        else
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+        if (a.lse && lane == 0) a.lse[(size_t)(cut.row0 + tok) * (a.Hkv * a.G) + head] = row_lse(m, total);
+    }
+}
+
+// The workspace of a grid of C blocks whose tiles have R rows.
+inline size_t paged_workspace(int C, int R, int D) {
+    return align_up(sizeof(PagedCut) * (size_t)C, 256) + (size_t)C * 2 * R * (sizeof(float2) + (size_t)D * sizeof(float));
+}
+
+// Host side (paged_rows.cu). Maps of the pages of `base` (box: 64 elements x a page's tokens,
+// at most `keys`) and of q (box: 64 elements x the heads of a key head x `tokens`), 128-byte
+// swizzle, what lies outside reads as zeros; and the kernels' arguments for a grid whose tiles have
+// R rows (false: the workspace is too small).
+bool paged_kv_map(CUtensorMap* map, const PagedProblem& p, const void* base, int keys);
+bool paged_q_map(CUtensorMap* map, const PagedProblem& p, int tokens);
+bool paged_args(const PagedProblem& p, int grid, int R, PagedArgs* a);
+
+// 4-D TMA load of a box at (element, slot, head, page), 3-D at (element, head, row).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
 }
 
 }  // namespace lin
