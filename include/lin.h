@@ -684,7 +684,7 @@ LIN_API int lin_cache_append(lin_ctx* ctx, const lin_kv_cache* cache, const lin_
  * none of the cache's reads as zeros. Whatever the arrays hold, nothing outside the
  * operands is read or written.
  *   q, out : tokens x H heads of head_dim, bf16, 16-byte aligned, rows ldq and ldo apart (multiples of 8).
- *   H      : a multiple of cache->heads, at most 32 times as many.
+ *   H      : a multiple of cache->heads, at most 128 times as many.
  *   scale  : > 0; 0 selects 1/sqrt(head_dim).
  *   max_new: about how many new tokens the longest sequence has (0: as many as the average); it picks the
  *            kernel, and any value gives right results.

@@ -65,7 +65,8 @@ CASES = [
     ([16], [130], 2, 2, 64, 16), ([7, 33], [64, 33], 10, 2, 64, 16), ([1, 65, 1, 130], [70, 65, 1, 400], 8, 4, 128, 16),
     ([200], [200], 3, 3, 64, 32), ([129, 5], [1000, 5], 5, 1, 128, 64), ([1], [64], 32, 1, 64, 8),
     ([2, 1], [65, 128], 32, 1, 128, 16), ([300], [301], 7, 1, 64, 16), ([257], [700], 4, 2, 128, 8),
-    ([1] * 3, [2000, 3, 1], 2, 1, 64, 4096),
+    ([1] * 3, [2000, 3, 1], 2, 1, 64, 4096), ([1, 3], [70, 400], 128, 1, 128, 16), ([2], [300], 96, 2, 64, 32),
+    ([500, 3, 256], [1500, 3, 256], 2, 1, 128, 32), ([255, 1], [300, 4000], 6, 2, 64, 16),
 ]
 
 

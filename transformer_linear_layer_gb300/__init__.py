@@ -1048,7 +1048,7 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     (:func:`cache_append`).
 
     q: tokens x query heads x width, bf16, rows any multiple of 8 elements apart; query heads a multiple
-    (at most 32) of the cache's. causal: each token sees the keys up to its own place; otherwise all of its
+    (at most 128) of the cache's. causal: each token sees the keys up to its own place; otherwise all of its
     sequence's (a cross attention over an encoder's states). max_new: about how many new
     tokens the longest sequence has (default: the average), which picks the kernel; any value is
     right. Returns out (like q, contiguous), or (out, lse) with lse tokens x heads fp32 when ``with_lse`` or an lse

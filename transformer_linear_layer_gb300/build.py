@@ -30,7 +30,7 @@ TIMELINE_LIB = os.path.join(BUILD, "liblin_timeline.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ("lin_api.cu", "skinny.cu", "ffma.cu", "tc.cu", "gemv.cu", "backward.cu", "noalloc.cu", "fold.cu", "probe.cu", "attn.cu",
            "attn_bwd.cu", "logprobs.cu", "distill.cu", "rotary.cu",
-           "paged_rows.cu")
+           "paged_rows.cu", "paged_tiles.cu", "paged_join.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr", f"-I{INCLUDE}"]

@@ -268,7 +268,7 @@ struct RotaryProblem {
 };
 int launch_rotary(const RotaryProblem& p);
 
-// Attention of new tokens over a paged cache, for tiles of at most 16 or 32 rows (paged_rows.cu).
+// Attention of new tokens over a paged cache.
 struct PagedProblem {
     lin_kv_cache cache = {};
     lin_kv_batch batch = {};
@@ -287,9 +287,13 @@ struct PagedProblem {
     int sm_count = 0;
     bool early_start = false;      // programmatic launch (nothing is read before the dependency wait)
 };
-constexpr int kPagedRowsMax = 32;  // rows of a tile, at least a key head's query heads
+// kPagedRowsMax rows (tokens of a sequence with the query heads of a key head) and fewer go
+// to paged_rows.cu, more to paged_tiles.cu, whose tiles hold at least kPagedGroupMax query heads.
+constexpr int kPagedRowsMax = 32, kPagedGroupMax = 128;
 size_t paged_rows_workspace(int sm_count, int rows, int D);
+size_t paged_tiles_workspace(int sm_count, int D);
 int launch_paged_rows(const PagedProblem& p, int rows);
+int launch_paged_tiles(const PagedProblem& p);
 
 // Kernel timelines (timeline build only, see timeline.cuh): copy up to `bytes`
 // of the stamp array to host memory at `dst` (if not null), then zero it (if

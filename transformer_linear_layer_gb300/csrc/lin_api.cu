@@ -1503,9 +1503,14 @@ int paged_rows(const lin_kv_cache& cache, const lin_kv_batch* batch, int H, int 
     return rows > INT_MAX ? INT_MAX : (int)rows;
 }
 
+size_t paged_bytes(const lin_ctx& ctx, const lin_kv_cache& cache, int rows) {
+    return rows <= lin::kPagedRowsMax ? lin::paged_rows_workspace(ctx.sm_count, rows, cache.head_dim)
+                                      : lin::paged_tiles_workspace(ctx.sm_count, cache.head_dim);
+}
+
 int paged_heads_ok(const lin_kv_cache* c, int H, int max_new) {
     if (!c || H < 1 || c->heads < 1 || max_new < 0 || H % c->heads != 0) return LIN_ERR_ARG;
-    if ((c->head_dim != 64 && c->head_dim != 128) || H / c->heads > lin::kPagedRowsMax || H > 65535)
+    if ((c->head_dim != 64 && c->head_dim != 128) || H / c->heads > lin::kPagedGroupMax || H > 65535)
         return LIN_ERR_UNSUPPORTED;
     return LIN_OK;
 }
@@ -1517,7 +1522,7 @@ int lin_paged_attention_workspace(const lin_ctx* ctx, const lin_kv_cache* cache,
     if (!ctx || !bytes || (max_new == 0 && !batch)) return LIN_ERR_ARG;
     const int ok = paged_heads_ok(cache, H, max_new);
     if (ok != LIN_OK) return ok;
-    *bytes = lin::paged_rows_workspace(ctx->sm_count, paged_rows(*cache, batch, H, max_new), cache->head_dim);
+    *bytes = paged_bytes(*ctx, *cache, paged_rows(*cache, batch, H, max_new));
     return LIN_OK;
 }
 
@@ -1541,7 +1546,7 @@ int lin_paged_attention(lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_ba
         workspace = static_cast<char*>(ctx->workspace) + kCounterBytes;
     }
     const int rows = paged_rows(*cache, batch, H, max_new);
-    if (workspace_bytes < paged_rows_workspace(ctx->sm_count, rows, cache->head_dim)) return LIN_ERR_WORKSPACE;
+    if (workspace_bytes < paged_bytes(*ctx, *cache, rows)) return LIN_ERR_WORKSPACE;
     auto flat = [](const void* p, size_t bytes) { return Rows{p, 1, (long long)bytes, (long long)bytes, 1}; };
     const size_t held = cache_extent(*cache), lse_bytes = lse ? (size_t)N * H * 4 : 0;
     const Rows ro{out, N, width, ldo, 2}, rl = flat(lse, lse_bytes), rw = flat(workspace, workspace_bytes);
@@ -1577,7 +1582,7 @@ int lin_paged_attention(lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_ba
         hull = Range{lo, (size_t)(hi - lo)};
     }
     note_output(p.stream, hull);
-    return launched(launch_paged_rows(p, rows), p.stream, hull);
+    return launched(rows <= kPagedRowsMax ? launch_paged_rows(p, rows) : launch_paged_tiles(p), p.stream, hull);
 }
 
 int lin_check_device(lin_ctx* ctx, void* stream) {

@@ -187,64 +187,6 @@ __device__ __forceinline__ float row_lse(float m, float l) {
     return l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
 }
 
-// Joins the parts of the items that stretches' ends cut: block c those of the item that
-// block c of the attention kernel started and did not end. A warp a row: maxima of up
-// to 32 parts at once, then the weighted sums, part after part.
-template <int D, int R>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int c = blockIdx.x;
-    const PagedCut cut = a.cuts[c];
-    if (cut.last <= c) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int parts = cut.last - c + 1;
-    auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
-    for (int row = blockIdx.y * 4 + warp; row < cut.tokens * a.G; row += gridDim.y * 4) {
-        float m = -INFINITY;
-        for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.stats[(size_t)slot(i) * R + row].x);
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float base = m == -INFINITY ? 0.f : m;
-        float acc[D / 32] = {}, total = 0.f;
-        for (int i0 = 0; i0 < parts; i0 += 32) {
-            float w = 0.f, l = 0.f;
-            if (i0 + lane < parts) {
-                const float2 s = a.stats[(size_t)slot(i0 + lane) * R + row];
-                w = exp2f(s.x - base);
-                l = s.y * w;
-            }
-            const int k = min(parts - i0, 32);
-#pragma unroll 4
-            for (int i = 0; i < k; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, i);
-                total += __shfl_sync(0xffffffffu, l, i);
-                const float* src = a.sums + ((size_t)slot(i0 + i) * R + row) * D + lane * (D / 32);
-                if constexpr (D == 64) {
-                    const float2 v = *reinterpret_cast<const float2*>(src);
-                    acc[0] = fmaf(v.x, wi, acc[0]);
-                    acc[1] = fmaf(v.y, wi, acc[1]);
-                } else {
-                    const float4 v = *reinterpret_cast<const float4*>(src);
-                    acc[0] = fmaf(v.x, wi, acc[0]);
-                    acc[1] = fmaf(v.y, wi, acc[1]);
-                    acc[2] = fmaf(v.z, wi, acc[2]);
-                    acc[3] = fmaf(v.w, wi, acc[3]);
-                }
-            }
-        }
-        const float inv = total == 0.f ? 0.f : 1.f / total;
-        const int tok = row / a.G, head = cut.h * a.G + row % a.G;
-        uint16_t* dst = a.out + (size_t)(cut.row0 + tok) * a.ldo + (size_t)head * D + lane * (D / 32);
-        if constexpr (D == 64)
-            *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-        else
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-        if (a.lse && lane == 0) a.lse[(size_t)(cut.row0 + tok) * (a.Hkv * a.G) + head] = row_lse(m, total);
-    }
-}
-
 // The workspace of a grid of C blocks whose tiles have R rows.
 inline size_t paged_workspace(int C, int R, int D) {
     return align_up(sizeof(PagedCut) * (size_t)C, 256) + (size_t)C * 2 * R * (sizeof(float2) + (size_t)D * sizeof(float));
@@ -257,6 +199,8 @@ inline size_t paged_workspace(int C, int R, int D) {
 bool paged_kv_map(CUtensorMap* map, const PagedProblem& p, const void* base, int keys);
 bool paged_q_map(CUtensorMap* map, const PagedProblem& p, int tokens);
 bool paged_args(const PagedProblem& p, int grid, int R, PagedArgs* a);
+// The joining kernel, behind an attention kernel of `grid` blocks (paged_join.cu).
+int launch_paged_join(const PagedProblem& p, const PagedArgs& a, int grid, int R);
 
 // 4-D TMA load of a box at (element, slot, head, page), 3-D at (element, head, row).
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {

@@ -407,11 +407,8 @@ int start(const PagedProblem& p) {
     cfg.attrs = &attr;
     cfg.numAttrs = p.early_start ? 1 : 0;
     if (cudaLaunchKernelEx(&cfg, paged_rows_kernel<D, MT>, tq, tk, tv, a) != cudaSuccess) return LIN_ERR_CUDA;
-    cfg.gridDim = dim3(grid - 1, R / 16);
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, paged_join_kernel<D, R>, a) != cudaSuccess) return LIN_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? LIN_OK : LIN_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) return LIN_ERR_CUDA;
+    return launch_paged_join(p, a, grid, R);
 }
 
 template <int D, int MT>

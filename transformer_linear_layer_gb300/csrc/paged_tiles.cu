@@ -1,0 +1,571 @@
+// Attention of many new tokens (chunks of prompts, whole prompts, the queries of a
+// cross attention) over a paged cache, on the tensor cores: tiles of two groups of up
+// to 128 rows (token, query head of one key head).
+//
+//   s_rj = (q_r . k_j) scale,  out_r = sum_j exp(s_rj - m) v_j / sum_j exp(s_rj - m)
+//
+// 4 D flops a row and key against 4 D bytes a key: with 256 rows a tile the products and the
+// exponentials bound it, not memory. Both groups work on the same keys, so that
+// a block of 128 keys, brought in once, serves 256 rows (two tiles apart would ask the
+// L2 for 60 bytes a cycle and SM); and one group's softmax runs under the other's products.
+//   warp 0      TMA. K and V of 128 keys are tiles of one ring (K, V, K, V, ...),
+//               a box per page and 64 columns, each lane its own; Q per group.
+//   warps 1, 2  tcgen05.mma, a thread per group: S = Q K^T (128 x 128) into the
+//               group's 128 TMEM columns, then O += P V with P (bf16) as the TMEM operand, in
+//               the columns that S had: nothing of the scores passes through shared memory.
+//   warps 4-7,  softmax of group 0 and 1, a thread per row: scores out of TMEM, scaled to
+//   warps 8-11  base-2 units by a packed FMA, exponentiated, rounded to bf16, back into TMEM.
+//               A commit of S also says that the product before it is done, so that O can
+//               be scaled when the reference for the exponents moves. That need not be the maximum: it stays
+//               where it is while no row of the warp has risen by more than 2^8, which keeps sums and
+//               probabilities in range (bf16 keeps its relative precision) and nearly always saves
+//               the trip of O through the registers.
+// Keys past the last one that a row of the tile sees are not loaded where they fill a box, and their
+// values are set to zero in shared memory where they do not: a probability of 0 must not meet a
+// NaN in slots that were never written.
+// Every wait is bounded (about 1 s); a block that gives up sets the status word.
+#include <math.h>
+
+#include "paged.cuh"
+
+namespace lin {
+namespace {
+
+constexpr int kPtThreads = 384;
+constexpr int kPtKeys = 128;            // keys of a block, and rows of a group
+// Registers: launched at kPtLaunch a thread; warps 0-3 go down to kPtLow and the softmax
+// warps up to kPtHigh (128 * 72 + 256 * 216 = 384 * 168). The host refuses a kernel
+// compiled to fewer than kPtLaunch: the increase could not be granted.
+constexpr int kPtLaunch = 168, kPtLow = 72, kPtHigh = 216;
+static_assert(128 * kPtLow + 256 * kPtHigh <= kPtThreads * kPtLaunch, "register split");
+constexpr uint32_t kPtTmem = 512;       // S (then P) of group 0, 1 in columns 0-127, 128-255;
+constexpr uint32_t kPtO = 256;          // O in 256 .. and 384 ..
+constexpr int kPtParts = 4;             // parts of items that are described at a time
+constexpr float kPtRise = 8.f;          // base-2 units by which a row may pass its reference
+
+template <int D>
+struct PtShape {
+    static constexpr uint32_t kTile = kPtKeys * D * 2;      // K, V or Q: halves of 64 columns, 16 KiB each
+    static constexpr int S = D == 64 ? 10 : 5;              // tiles of the ring
+    static constexpr size_t kSmem = 1024 + (2 + S) * (size_t)kTile;
+};
+
+struct PtPart {       // a block's part of an item
+    int h, row0;      // key head, first row of q
+    int tokens;
+    int pos0;         // position of the first token
+    int seen;         // keys that some row sees
+    int j0, n;        // first key block, blocks
+    int slot;         // the workspace's slot, or -1: the item is whole
+};
+
+__device__ __forceinline__ float pt_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t pt_pack(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void pt_unpack(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t pt_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t pt_add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float pt_max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ void pt_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void pt_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D (+)= A B with A (bf16, two to a 32-bit column) in TMEM.
+__device__ __forceinline__ void pt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// A V tile read MN-major: 64-column halves 16 KiB apart, groups of 8 keys 1 KiB.
+__device__ __forceinline__ uint64_t pt_v_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(16384u >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+// What group grp does of a part: tokens of its own, keys that they see, key blocks.
+struct PtShare {
+    int tokens, seen, n;
+};
+__device__ __forceinline__ PtShare pt_share(const PagedArgs& a, const PtPart& p, int grp) {
+    const int each = a.TQ / 2;
+    PtShare s;
+    s.tokens = min(max(p.tokens - grp * each, 0), each);
+    s.seen = a.causal ? max(min(p.seen, p.pos0 + grp * each + s.tokens), 0) : p.seen;
+    s.n = s.tokens == 0 ? 0 : min(max((s.seen + kPtKeys - 1) / kPtKeys - p.j0, 0), p.n);
+    return s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPtThreads, 1)
+paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const PagedArgs a) {
+    using P = PtShape<D>;
+    constexpr int S = P::S, HALVES = D / 64;
+    constexpr uint32_t kHalf = kPtKeys * 128;
+    constexpr uint32_t IDESC_S = make_idesc(1u, 128, kPtKeys);
+    constexpr uint32_t IDESC_O = make_idesc(1u, 128, D, false, true);
+
+    extern __shared__ uint8_t raw[];
+    __shared__ alignas(8) uint64_t bars[2 * S + 2 * kPtParts + 12];
+    __shared__ PtPart parts[kPtParts];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sQ = smem;
+    uint8_t* ring = smem + 2 * P::kTile;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S, pfull0 = empty0 + 8 * S,
+                   pempty0 = pfull0 + 8 * kPtParts, qfull0 = pempty0 + 8 * kPtParts, qempty0 = qfull0 + 16,
+                   sfull0 = qempty0 + 16, probs0 = sfull0 + 16, ofull0 = probs0 + 16, done0 = ofull0 + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 2);          // both groups
+        }
+        for (int s = 0; s < kPtParts; ++s) {
+            mbar_init(pfull0 + 8 * s, 1);
+            mbar_init(pempty0 + 8 * s, 2 + 8);     // both MMA threads, the softmax warps
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(qfull0 + 8 * g, 1);
+            mbar_init(qempty0 + 8 * g, 1);
+            mbar_init(sfull0 + 8 * g, 1);
+            mbar_init(probs0 + 8 * g, 4);
+            mbar_init(ofull0 + 8 * g, 1);
+            mbar_init(done0 + 8 * g, 1);
+        }
+        s_abort = 0;
+        mbar_fence_init();
+        tma_prefetch_map(&tmQ);
+        tma_prefetch_map(&tmK);
+        tma_prefetch_map(&tmV);
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&s_tmem), kPtTmem);
+    tc_fence_before();
+    pdl_wait();
+    pdl_launch_dependents();
+    const PagedStretch r = paged_stretch<kPtKeys, kPtThreads>(a);  // syncs the block
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int stretch = (int)(r.hi - r.lo);
+
+    auto give_up = [&]() {
+        atomicExch(&s_abort, 1);
+        atomicExch(a.status, (int)LIN_ERR_DEVICE_TIMEOUT);
+    };
+    auto aborted = [&]() { return *(volatile int*)&s_abort != 0; };
+
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtLow));
+    if (warp == 0) {
+        // ---- TMA: the whole warp walks the stretch ----
+        PagedCut cut = {0, 0, 0, 0};
+        uint32_t g = 0, np = 0, nq[2] = {0, 0};  // tiles, parts and Q tiles issued
+        bool ok = true;
+        if (stretch > 0) {
+            const int box = min(a.page_size, kPtKeys), each = a.TQ / 2;
+            PagedWalk<kPtKeys> w;
+            w.start(a, r);
+            while (ok) {
+                const int k = (int)min((long long)(w.n - w.j), r.hi - w.u);
+                PtPart p;
+                p.h = w.h;
+                p.row0 = w.q.row0 + w.t * a.TQ;
+                p.tokens = min(a.TQ, w.q.n - w.t * a.TQ);
+                p.pos0 = w.q.pos0 + w.t * a.TQ;
+                p.seen = tile_seen(a, w.q, w.t);
+                p.j0 = w.j;
+                p.n = k;
+                p.slot = k == w.n ? -1 : 2 * (int)blockIdx.x + (w.j == 0 ? 1 : 0);
+                if (w.j == 0 && k < w.n) cut = {p.row0, p.tokens, p.h, (int)((w.u + w.n - 1) / r.per)};
+                const uint32_t ps = np % kPtParts;
+                if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(pempty0 + 8 * ps, ((np / kPtParts) & 1) ^ 1))) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    parts[ps] = p;
+                    mbar_arrive(pfull0 + 8 * ps);
+                }
+                ++np;
+                const int* table = a.batch.block_table + w.b * a.batch.table_stride;
+                for (int i = 0; ok && i < k; ++i) {
+                    const int key0 = (w.j + i) * kPtKeys;
+                    const int nb = (min(max(p.seen - key0, 0), kPtKeys) + box - 1) / box, boxes = nb * HALVES;
+                    int page = a.pages, y = 0, at = 0, half = 0;
+                    if (lane < boxes) {
+                        at = lane % nb;
+                        half = lane / nb;
+                        const int key = key0 + at * box;
+                        page = table[key / a.page_size];
+                        if (page < 0 || page > a.pages) page = a.pages;  // no page: a box outside the map, zeros
+                        y = key & (a.page_size - 1);
+                    }
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t s = g % S, ph = (g / S) & 1;
+                        if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(empty0 + 8 * s, ph ^ 1))) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_expect_tx(full0 + 8 * s, (uint32_t)boxes * box * 128);
+                        __syncwarp();
+                        if (lane < boxes)
+                            tma_load_4d(smem_u32(ring + s * P::kTile + half * kHalf + at * box * 128), kv ? &tmV : &tmK,
+                                        full0 + 8 * s, 64 * half, y, p.h, page);
+                        ++g;
+                        if (i > 0 || kv > 0) continue;
+                        // the part's Q, once its predecessor's last S is done
+                        for (int grp = 0; ok && grp < 2; ++grp) {
+                            if (pt_share(a, p, grp).n == 0) continue;
+                            if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(qempty0 + 8 * grp, (nq[grp] & 1) ^ 1))) {
+                                ok = false;
+                                break;
+                            }
+                            if (lane == 0) mbar_expect_tx(qfull0 + 8 * grp, (uint32_t)(each * a.G) * D * 2);
+                            __syncwarp();
+                            if (lane < HALVES)
+                                tma_load_3d(smem_u32(sQ + grp * P::kTile + lane * kHalf), &tmQ, qfull0 + 8 * grp,
+                                            64 * lane, p.h * a.G, p.row0 + grp * each);
+                            ++nq[grp];
+                        }
+                        if (!ok) break;
+                    }
+                }
+                if (!ok || w.u + k >= r.hi) break;
+                w.next(a, k);
+            }
+        }
+        if (lane == 0) a.cuts[blockIdx.x] = cut;
+        if (!ok) {
+            if (lane == 0) give_up();
+            // the copies in flight land before the block ends
+            for (int grp = 0; grp < 2; ++grp)
+                if (nq[grp] > 0) mbar_wait(qfull0 + 8 * grp, (nq[grp] - 1) & 1);
+            for (uint32_t n = g > (uint32_t)S ? g - S : 0; n < g; ++n) mbar_wait(full0 + 8 * (n % S), (n / S) & 1);
+        }
+    } else if (warp == 1 || warp == 2) {
+        if (lane == 0) {
+            // ---- the products of group warp - 1 ----
+            const int grp = warp - 1;
+            const uint32_t tS = tmem + 128u * grp, tO = tmem + kPtO + 128u * grp;
+            const uint64_t qd = sw128_kmajor_desc(smem_u32(sQ + grp * P::kTile));
+            uint32_t g = 0, np = 0, nq = 0, c = 0;  // tiles, parts, Q tiles, blocks of the group
+            bool ok = true;
+            for (int u = 0; ok && u < stretch; ++np) {
+                const uint32_t ps = np % kPtParts;
+                if (aborted() || !mbar_wait(pfull0 + 8 * ps, (np / kPtParts) & 1)) {
+                    ok = false;
+                    break;
+                }
+                const PtPart p = parts[ps];
+                const int n = pt_share(a, p, grp).n;
+                if (n > 0 && !mbar_wait(qfull0 + 8 * grp, nq++ & 1)) {
+                    ok = false;
+                    break;
+                }
+                for (int i = 0; i < p.n; ++i, g += 2) {
+                    const uint32_t ks = g % S, kph = (g / S) & 1, vs = (g + 1) % S, vph = ((g + 1) / S) & 1;
+                    if (aborted() || !mbar_wait(full0 + 8 * ks, kph)) {
+                        ok = false;
+                        break;
+                    }
+                    if (i >= n) {  // the other group's block only
+                        mbar_arrive(empty0 + 8 * ks);
+                        if (!mbar_wait(full0 + 8 * vs, vph)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive(empty0 + 8 * vs);
+                        continue;
+                    }
+                    tc_fence_after();
+                    const uint64_t kd = sw128_kmajor_desc(smem_u32(ring + ks * P::kTile));
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc_mma<true>(tS, qd + 1024u * (kk >> 2) + 2u * (kk & 3), kd + 1024u * (kk >> 2) + 2u * (kk & 3),
+                                     IDESC_S, kk != 0 ? 1u : 0u);
+                    tc_commit(sfull0 + 8 * grp);  // S, and every product before it
+                    tc_commit(empty0 + 8 * ks);
+                    if (i == n - 1) tc_commit(qempty0 + 8 * grp);
+                    if (aborted() || !mbar_wait(full0 + 8 * vs, vph) || !mbar_wait(probs0 + 8 * grp, c++ & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t vd = pt_v_desc(smem_u32(ring + vs * P::kTile));
+#pragma unroll
+                    for (int kk = 0; kk < kPtKeys / 16; ++kk)
+                        pt_mma_ts(tO, tS + 8u * kk, vd + 128u * kk, IDESC_O, (kk != 0 || i != 0) ? 1u : 0u);
+                    tc_commit(empty0 + 8 * vs);
+                    if (i == n - 1) tc_commit(ofull0 + 8 * grp);
+                }
+                u += p.n;
+                mbar_arrive(pempty0 + 8 * ps);
+            }
+            if (!ok) give_up();
+            // all products are done before the block ends
+            tc_commit(done0 + 8 * grp);
+            mbar_wait(done0 + 8 * grp, 0);
+        }
+    } else if (warp >= 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPtHigh));
+        // ---- softmax and output of a group: thread = row ----
+        const int grp = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane;
+        const int each = a.TQ / 2, tok = row / a.G, sub = row - tok * a.G;
+        const uint32_t tS = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128u * grp;
+        const uint32_t tO = tmem + (static_cast<uint32_t>(32 * q) << 16) + kPtO + 128u * grp;
+        const float NEG = -INFINITY, sl2 = a.scale_log2;
+        const uint64_t sl2x2 = pt_pack(sl2, sl2);
+        uint32_t g = 0, np = 0, c = 0, no = 0;  // tiles, parts, blocks and outputs of the group
+        bool ok = true;
+        for (int u = 0; ok && u < stretch; ++np) {
+            const uint32_t ps = np % kPtParts;
+            if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(pfull0 + 8 * ps, (np / kPtParts) & 1))) {
+                ok = false;
+                break;
+            }
+            const PtPart p = parts[ps];
+            const PtShare sh = pt_share(a, p, grp);
+            // rows that are none see what the last one does (their results go nowhere)
+            const bool live = tok < sh.tokens;
+            const int lim = a.causal && live ? min(p.pos0 + grp * each + tok + 1, sh.seen) : sh.seen;
+            const int wmax = __reduce_max_sync(0xffffffffu, lim), wmin = __reduce_min_sync(0xffffffffu, lim);
+            float m = NEG, l = 0.f;
+            for (int i = 0; i < sh.n; ++i, ++c) {
+                const int k0 = (p.j0 + i) * kPtKeys;
+                if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(sfull0 + 8 * grp, c & 1))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t sv[4][32];
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+                    if (k0 + 32 * ch < wmax) tmem_ld32_async(tS + 32u * ch, sv[ch]);
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+                    if (k0 + 32 * ch < wmax) tmem_wait_ld(sv[ch]);
+                float mx[4] = {NEG, NEG, NEG, NEG};
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    const int c0 = k0 + 32 * ch;
+                    if (c0 >= wmax) continue;
+                    if (c0 + 32 > wmin) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (c0 + e >= lim) sv[ch][e] = __float_as_uint(NEG);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        mx[ch] = pt_max3(mx[ch], __uint_as_float(sv[ch][e]), __uint_as_float(sv[ch][e + 1]));
+                }
+                const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                if (i == 0) {
+                    m = top;
+                } else if (__any_sync(0xffffffffu, (top - m) * sl2 > kPtRise)) {
+                    const float alpha = pt_ex2((m - (top == NEG ? 0.f : top)) * sl2);
+                    m = top;
+                    l *= alpha;
+#pragma unroll
+                    for (int h = 0; h < D / 32; ++h) {
+                        uint32_t ov[32];
+                        tmem_ld32_async(tO + 32u * h, ov);
+                        tmem_wait_ld(ov);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t x[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                x[e] = __float_as_uint(__uint_as_float(ov[16 * half + e]) * alpha);
+                            pt_st16(tO + 32u * h + 16u * half, x);
+                        }
+                    }
+                }
+                const float ref = m == NEG ? 0.f : m;
+                const uint64_t nref = pt_pack(-ref * sl2, -ref * sl2);
+                uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t pk[16];
+                    if (k0 + 32 * ch < wmax) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float x0, x1;
+                            pt_unpack(pt_fma2(pt_pack(__uint_as_float(sv[ch][e]), __uint_as_float(sv[ch][e + 1])), sl2x2, nref),
+                                      x0, x1);
+                            const float p0 = pt_ex2(x0), p1 = pt_ex2(x1);
+                            sum[(e >> 1) & 1] = pt_add2(sum[(e >> 1) & 1], pt_pack(p0, p1));
+                            pk[e >> 1] = pack_bf16x2(p0, p1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                    }
+                    pt_st16(tS + 16u * ch, pk);
+                }
+                float la, lb, lc, ld;
+                pt_unpack(sum[0], la, lb);
+                pt_unpack(sum[1], lc, ld);
+                l += (la + lb) + (lc + ld);
+                if (k0 + kPtKeys > p.seen) {
+                    // values of keys that nobody sees
+                    const uint32_t v = g + 2 * (uint32_t)i + 1, vs = v % S;
+                    if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * vs, (v / S) & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    if (k0 + row >= p.seen) {
+                        uint8_t* dst = ring + vs * P::kTile + row * 128;
+#pragma unroll
+                        for (int x = 0; x < D / 8; ++x)
+                            *reinterpret_cast<uint4*>(dst + (x >> 3) * kHalf + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                pt_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(probs0 + 8 * grp);
+            }
+            if (!ok) break;
+            if (sh.tokens > 0) {
+                if (sh.n > 0) {
+                    if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(ofull0 + 8 * grp, no++ & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const int head = p.h * a.G + sub, at = grp * each * a.G + row;  // row of the tile
+                const size_t n = (size_t)p.row0 + grp * each + tok;
+#pragma unroll
+                for (int h = 0; h < D / 32; ++h) {
+                    uint32_t ov[32];
+                    if (sh.n > 0) {
+                        tmem_ld32_async(tO + 32u * h, ov);
+                        tmem_wait_ld(ov);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] = 0u;
+                    }
+                    if (!live) continue;
+                    if (p.slot < 0) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + n * a.ldo + (size_t)head * D + 32 * h);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)  // a row without keys is 0 whatever O holds
+                                x[e] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(ov[8 * v + 2 * e]) * inv,
+                                                                   __uint_as_float(ov[8 * v + 2 * e + 1]) * inv);
+                            dst[v] = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(a.sums + ((size_t)p.slot * 256 + at) * D + 32 * h);
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) dst[v] = make_uint4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
+                    }
+                }
+                if (live) {
+                    const float base2 = m == NEG ? NEG : m * sl2;
+                    if (p.slot >= 0)
+                        a.stats[(size_t)p.slot * 256 + at] = make_float2(base2, l);
+                    else if (a.lse)
+                        a.lse[n * (a.Hkv * a.G) + head] = row_lse(base2, l);
+                }
+                tc_fence_before();
+            }
+            u += p.n;
+            g += 2 * (uint32_t)p.n;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pempty0 + 8 * ps);
+        }
+        if (!ok) give_up();
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kPtTmem);
+    }
+}
+
+template <int D>
+int start(const PagedProblem& p) {
+    using P = PtShape<D>;
+    const int grid = p.sm_count;
+    PagedArgs a;
+    if (!paged_args(p, grid, 256, &a)) return LIN_ERR_WORKSPACE;
+    const int each = 128 / a.G;  // tokens of a group
+    a.TQ = 2 * each;
+    CUtensorMap tq, tk, tv;
+    if (!paged_q_map(&tq, p, each) || !paged_kv_map(&tk, p, p.cache.k, kPtKeys) || !paged_kv_map(&tv, p, p.cache.v, kPtKeys))
+        return LIN_ERR_CUDA;
+    static std::atomic<unsigned long long> attr_set{0};
+    if (ensure_smem_attr(attr_set, paged_tiles_kernel<D>, P::kSmem) != LIN_OK) return LIN_ERR_CUDA;
+    static const int regs = []() {
+        cudaFuncAttributes fa;
+        return cudaFuncGetAttributes(&fa, paged_tiles_kernel<D>) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs < kPtLaunch) return LIN_ERR_UNSUPPORTED;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kPtThreads);
+    cfg.dynamicSmemBytes = P::kSmem;
+    cfg.stream = p.stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = p.early_start ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, paged_tiles_kernel<D>, tq, tk, tv, a) != cudaSuccess) return LIN_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) return LIN_ERR_CUDA;
+    return launch_paged_join(p, a, grid, 256);
+}
+
+}  // namespace
+
+size_t paged_tiles_workspace(int sm_count, int D) { return paged_workspace(sm_count, 256, D); }
+
+int launch_paged_tiles(const PagedProblem& p) {
+    return p.cache.head_dim == 64 ? start<64>(p) : start<128>(p);
+}
+
+}  // namespace lin
