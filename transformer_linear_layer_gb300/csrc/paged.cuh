@@ -6,7 +6,8 @@
 // that share a key head: R or fewer rows (token, head) of one product with the key head's keys.
 // An item is a tile of one key head, a unit is KB keys of an item. The units of
 // the call, sequence by sequence, tile by tile, head by head, key block by key block, form
-// one line, and each block of the grid takes an equal stretch of it. Lengths lie
+// one line, and each block of the grid takes an equal stretch of it. What an item costs beside its
+// units (its queries, its output) stands on the line as `lead` units before the first, in which nothing happens. Lengths lie
 // on the device, so every block adds up the sequences' units itself. An item that a
 // stretch's end cuts is computed in parts: each block leaves its rows' sums (not
 // divided), maxima and totals in the workspace, and a second kernel joins them in the order of
@@ -52,6 +53,7 @@ struct PagedArgs {
     int pages, page_size;
     int Hkv, G, TQ;            // key heads, query heads of each, tokens of a tile
     int causal;
+    int lead;                  // units that an item's start and end cost
     float scale_log2;          // softmax scale times log2(e)
     uint16_t* out;             // row n, head h at n * ldo + h * D
     long long ldo;
@@ -107,14 +109,33 @@ __device__ __forceinline__ PagedStretch paged_stretch(const PagedArgs& a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int B = a.batch.sequences, each = (B + THREADS - 1) / THREADS;
     const int b0 = min((int)threadIdx.x * each, B), b1 = min(b0 + each, B);
-    auto units = [&](int b) {
-        const PagedSeq q = paged_seq(a, b);
-        long long n = 0;
-        for (int t = 0; t * a.TQ < q.n; ++t) n += tile_units<KB>(a, q, t);
-        return n * a.Hkv;
+    auto tiles = [&](const PagedSeq& q) { return (q.n + a.TQ - 1) / a.TQ; };
+    auto some = [&](const PagedSeq& q, int t, int n, int step) {
+        long long u = 0;
+        for (; t < n; t += step) u += tile_units<KB>(a, q, t) + a.lead;
+        return u;
     };
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += units(b);
+    for (int i = 0; i < each; ++i) {
+        PagedSeq q = {0, 0, 0, 0};
+        if (b0 + i < b1) q = paged_seq(a, b0 + i);
+        const int n = tiles(q);
+        if (n <= 4) mine += some(q, 0, n, 1);
+        // a long prompt's tiles by the whole warp
+        for (unsigned many = __ballot_sync(0xffffffffu, n > 4); many; many &= many - 1) {
+            const int from = __ffs(many) - 1;
+            PagedSeq o;
+            o.row0 = 0;
+            o.n = __shfl_sync(0xffffffffu, q.n, from);
+            o.held = __shfl_sync(0xffffffffu, q.held, from);
+            o.pos0 = __shfl_sync(0xffffffffu, q.pos0, from);
+            long long u = some(o, lane, __shfl_sync(0xffffffffu, n, from), 32);
+#pragma unroll
+            for (int d = 16; d > 0; d /= 2) u += __shfl_xor_sync(0xffffffffu, u, d);
+            if (lane == from) mine += u;
+        }
+    }
+    mine *= a.Hkv;
     long long upto = mine;  // inclusive over the threads
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -135,7 +156,12 @@ __device__ __forceinline__ PagedStretch paged_stretch(const PagedArgs& a) {
     long long at = upto - mine;
     if (r.lo < r.hi && at <= r.lo && r.lo < upto) {
         int b = b0;
-        for (long long u; b + 1 < b1 && at + (u = units(b)) <= r.lo; ++b) at += u;
+        for (; b + 1 < b1; ++b) {
+            const PagedSeq q = paged_seq(a, b);
+            const long long u = some(q, 0, tiles(q), 1) * a.Hkv;
+            if (at + u > r.lo) break;
+            at += u;
+        }
         s_b = b;
         s_off = r.lo - at;
     }
@@ -145,31 +171,67 @@ __device__ __forceinline__ PagedStretch paged_stretch(const PagedArgs& a) {
     return r;
 }
 
-// Walks a stretch item by item.
+// Walks a stretch item by item; by a whole warp. After start(), and after next(), part()
+// says whether there is another part of an item in the stretch, and which.
 template <int KB>
 struct PagedWalk {
     PagedSeq q;
     int b, t, h, n;   // sequence, tile, key head, units of the item
-    long long u;      // unit of the line
-    int j;            // unit of the item
+    long long u, hi;  // place on the line, end of the stretch
+    int j;            // place in the item: `lead` units, then n
+    int lead;
     __device__ __forceinline__ void start(const PagedArgs& a, const PagedStretch& r) {
-        b = r.b;
+        const int lane = threadIdx.x & 31;
         u = r.lo;
+        hi = r.hi;
+        lead = a.lead;
+        b = r.b;
+        t = h = j = n = 0;
+        if (u >= hi) return;
         q = paged_seq(a, b);
         long long off = r.off;
-        for (t = 0;; ++t) {
-            n = tile_units<KB>(a, q, t);
-            if (off < (long long)n * a.Hkv) break;
-            off -= (long long)n * a.Hkv;
+        for (int t0 = 0; t0 * a.TQ < q.n; t0 += 32) {
+            const bool some = (t0 + lane) * a.TQ < q.n;
+            const long long mine = some ? (long long)(tile_units<KB>(a, q, t0 + lane) + lead) * a.Hkv : 0;
+            long long upto = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const long long v = __shfl_up_sync(0xffffffffu, upto, d);
+                if (lane >= d) upto += v;
+            }
+            const unsigned in = __ballot_sync(0xffffffffu, off < upto);
+            if (in) {
+                const int at = __ffs(in) - 1;
+                t = t0 + at;
+                off -= __shfl_sync(0xffffffffu, upto - mine, at);
+                break;
+            }
+            off -= __shfl_sync(0xffffffffu, upto, 31);
         }
-        h = (int)(off / n);
-        j = (int)(off - (long long)h * n);
+        n = tile_units<KB>(a, q, t);
+        h = (int)(off / (n + lead));
+        j = (int)(off - (long long)h * (n + lead));
     }
-    // To the next item's first unit, `k` units on. Only when there is one.
+    // The next part: units j0 .. j0 + k - 1 of the item.
+    __device__ __forceinline__ bool part(const PagedArgs& a, int& j0, int& k) {
+        while (u < hi) {
+            if (j < lead) {
+                const int skip = (int)min((long long)(lead - j), hi - u);
+                u += skip;
+                j += skip;
+                continue;
+            }
+            j0 = j - lead;
+            k = (int)min((long long)(n - j0), hi - u);
+            return true;
+        }
+        return false;
+    }
+    // Past the part.
     __device__ __forceinline__ void next(const PagedArgs& a, int k) {
         u += k;
         j = 0;
-        if (++h < a.Hkv) return;
+        if (u >= hi || ++h < a.Hkv) return;
         h = 0;
         if ((++t) * a.TQ >= q.n) {
             t = 0;
@@ -179,6 +241,8 @@ struct PagedWalk {
         }
         n = tile_units<KB>(a, q, t);
     }
+    // What the block that starts the item and does not end it notes of it.
+    __device__ __forceinline__ int last_block(long long per) const { return (int)((u + n - 1) / per); }
 };
 
 // A row's result: sums over its maximum's scale divided by the total; a row that saw

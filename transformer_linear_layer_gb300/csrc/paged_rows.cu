@@ -114,20 +114,19 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         PagedCut cut = {0, 0, 0, 0};
         uint32_t g = 0;
         bool ok = true;
-        if (r.lo < r.hi) {
+        {
             const int box = min(a.page_size, kPrKeys);
             const uint32_t q_bytes = (uint32_t)(a.TQ * a.G) * D * 2;
             PagedWalk<kPrKeys> w;
             w.start(a, r);
-            while (ok) {
-                const int k = (int)min((long long)(w.n - w.j), r.hi - w.u);  // units of this item here
+            for (int j0, k; ok && w.part(a, j0, k); w.next(a, k)) {
                 const int seen = tile_seen(a, w.q, w.t);
                 const int row0 = w.q.row0 + w.t * a.TQ, tokens = min(a.TQ, w.q.n - w.t * a.TQ);
-                const int slot = k == w.n ? -1 : 2 * (int)blockIdx.x + (w.j == 0 ? 1 : 0);
-                if (w.j == 0 && k < w.n) cut = {row0, tokens, w.h, (int)((w.u + w.n - 1) / r.per)};
+                const int slot = k == w.n ? -1 : 2 * (int)blockIdx.x + (j0 == 0 ? 1 : 0);
+                if (j0 == 0 && k < w.n) cut = {row0, tokens, w.h, w.last_block(r.per)};
                 const int* table = a.batch.block_table + w.b * a.batch.table_stride;
                 for (int i = 0; i < k; ++i) {
-                    const int key0 = (w.j + i) * kPrKeys;
+                    const int key0 = (j0 + i) * kPrKeys;
                     const int nb = (min(max(seen - key0, 0), kPrKeys) + box - 1) / box;
                     const int boxes = nb * HALVES * 2;
                     // this lane's box: a page of K or of V, 64 columns of it
@@ -161,8 +160,6 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                                     w.h * a.G, row0);
                     ++g;
                 }
-                if (!ok || w.u + k >= r.hi) break;
-                w.next(a, k);
             }
         }
         if (lane == 0) a.cuts[blockIdx.x] = cut;
@@ -471,6 +468,7 @@ bool paged_args(const PagedProblem& p, int grid, int R, PagedArgs* a) {
     a->G = p.H / p.cache.heads;
     a->TQ = R / a->G;
     a->causal = p.causal ? 1 : 0;
+    a->lead = 0;
     a->scale_log2 = p.scale * 1.4426950408889634f;
     a->out = static_cast<uint16_t*>(p.out);
     a->ldo = p.ldo;

@@ -8,8 +8,9 @@
 // exponentials bound it, not memory. Both groups work on the same keys, so that
 // a block of 128 keys, brought in once, serves 256 rows (two tiles apart would ask the
 // L2 for 60 bytes a cycle and SM); and one group's softmax runs under the other's products.
-//   warp 0      TMA. K and V of 128 keys are tiles of one ring (K, V, K, V, ...),
-//               a box per page and 64 columns, each lane its own; Q per group.
+//   warps 0, 3  TMA. K and V of 128 keys are tiles of one ring (K, V, K, V, ...),
+//               a box per page and 64 columns, each lane its own (pages of 8 tokens take 32
+//               boxes a tile, so that K and V have a warp each); Q per group.
 //   warps 1, 2  tcgen05.mma, a thread per group: S = Q K^T (128 x 128) into the
 //               group's 128 TMEM columns, then O += P V with P (bf16) as the TMEM operand, in
 //               the columns that S had: nothing of the scores passes through shared memory.
@@ -41,6 +42,7 @@ static_assert(128 * kPtLow + 256 * kPtHigh <= kPtThreads * kPtLaunch, "register 
 constexpr uint32_t kPtTmem = 512;       // S (then P) of group 0, 1 in columns 0-127, 128-255;
 constexpr uint32_t kPtO = 256;          // O in 256 .. and 384 ..
 constexpr int kPtParts = 4;             // parts of items that are described at a time
+constexpr int kPtLead = 1;              // blocks that an item's start and end cost
 constexpr float kPtRise = 8.f;          // base-2 units by which a row may pass its reference
 
 template <int D>
@@ -104,6 +106,14 @@ __device__ __forceinline__ void pt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+// True in one lane of the warp.
+__device__ __forceinline__ bool pt_elect() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
 }
 // A V tile read MN-major: 64-column halves 16 KiB apart, groups of 8 keys 1 KiB.
 __device__ __forceinline__ uint64_t pt_v_desc(uint32_t saddr) {
@@ -182,38 +192,54 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const PagedStretch r = paged_stretch<kPtKeys, kPtThreads>(a);  // syncs the block
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const int stretch = (int)(r.hi - r.lo);
 
     auto give_up = [&]() {
         atomicExch(&s_abort, 1);
         atomicExch(a.status, (int)LIN_ERR_DEVICE_TIMEOUT);
     };
-    auto aborted = [&]() { return *(volatile int*)&s_abort != 0; };
+    // A warp's wait: all lanes agree on whether it ended.
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, *(volatile int*)&s_abort == 0 && mbar_wait(bar, parity)) != 0;
+    };
 
     if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtLow));
-    if (warp == 0) {
-        // ---- TMA: the whole warp walks the stretch ----
+    if (warp == 0 || warp == 3) {
+        // ---- TMA: warp 0 the parts, Q and K, warp 3 V; whole warps walk the stretch ----
+        const bool keys = warp == 0;
         PagedCut cut = {0, 0, 0, 0};
-        uint32_t g = 0, np = 0, nq[2] = {0, 0};  // tiles, parts and Q tiles issued
+        uint32_t g = keys ? 0 : 1, np = 0, nq[2] = {0, 0};  // the next tile; parts and Q tiles issued
         bool ok = true;
-        if (stretch > 0) {
-            const int box = min(a.page_size, kPtKeys), each = a.TQ / 2;
-            PagedWalk<kPtKeys> w;
-            w.start(a, r);
-            while (ok) {
-                const int k = (int)min((long long)(w.n - w.j), r.hi - w.u);
-                PtPart p;
-                p.h = w.h;
-                p.row0 = w.q.row0 + w.t * a.TQ;
-                p.tokens = min(a.TQ, w.q.n - w.t * a.TQ);
-                p.pos0 = w.q.pos0 + w.t * a.TQ;
-                p.seen = tile_seen(a, w.q, w.t);
-                p.j0 = w.j;
-                p.n = k;
-                p.slot = k == w.n ? -1 : 2 * (int)blockIdx.x + (w.j == 0 ? 1 : 0);
-                if (w.j == 0 && k < w.n) cut = {p.row0, p.tokens, p.h, (int)((w.u + w.n - 1) / r.per)};
+        const int box = min(a.page_size, kPtKeys), each = a.TQ / 2;
+        // this lane's box of key block `blk`: its page, and how many boxes there are
+        auto look_up = [&](const int* table, int blk, int seen, int& page, int& key) {
+            const int nb = (min(max(seen - blk * kPtKeys, 0), kPtKeys) + box - 1) / box;
+            page = a.pages;
+            key = 0;
+            if (lane < nb * HALVES) {
+                key = blk * kPtKeys + (lane % nb) * box;
+                page = table[key / a.page_size];
+                if (page < 0 || page > a.pages) page = a.pages;  // no page: a box outside the map, zeros
+            }
+            return nb;
+        };
+        PagedWalk<kPtKeys> w;
+        w.start(a, r);
+        for (int j0, k; ok && w.part(a, j0, k); w.next(a, k)) {
+            PtPart p;
+            p.h = w.h;
+            p.row0 = w.q.row0 + w.t * a.TQ;
+            p.tokens = min(a.TQ, w.q.n - w.t * a.TQ);
+            p.pos0 = w.q.pos0 + w.t * a.TQ;
+            p.seen = tile_seen(a, w.q, w.t);
+            p.j0 = j0;
+            p.n = k;
+            p.slot = k == w.n ? -1 : 2 * (int)blockIdx.x + (j0 == 0 ? 1 : 0);
+            const int* table = a.batch.block_table + w.b * a.batch.table_stride;
+            int page, key, nb = look_up(table, j0, p.seen, page, key);
+            if (keys) {
+                if (j0 == 0 && k < w.n) cut = {p.row0, p.tokens, p.h, w.last_block(r.per)};
                 const uint32_t ps = np % kPtParts;
-                if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(pempty0 + 8 * ps, ((np / kPtParts) & 1) ^ 1))) {
+                if (!wait(pempty0 + 8 * ps, ((np / kPtParts) & 1) ^ 1)) {
                     ok = false;
                     break;
                 }
@@ -222,98 +248,96 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     mbar_arrive(pfull0 + 8 * ps);
                 }
                 ++np;
-                const int* table = a.batch.block_table + w.b * a.batch.table_stride;
-                for (int i = 0; ok && i < k; ++i) {
-                    const int key0 = (w.j + i) * kPtKeys;
-                    const int nb = (min(max(p.seen - key0, 0), kPtKeys) + box - 1) / box, boxes = nb * HALVES;
-                    int page = a.pages, y = 0, at = 0, half = 0;
-                    if (lane < boxes) {
-                        at = lane % nb;
-                        half = lane / nb;
-                        const int key = key0 + at * box;
-                        page = table[key / a.page_size];
-                        if (page < 0 || page > a.pages) page = a.pages;  // no page: a box outside the map, zeros
-                        y = key & (a.page_size - 1);
-                    }
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const uint32_t s = g % S, ph = (g / S) & 1;
-                        if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(empty0 + 8 * s, ph ^ 1))) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0) mbar_expect_tx(full0 + 8 * s, (uint32_t)boxes * box * 128);
-                        __syncwarp();
-                        if (lane < boxes)
-                            tma_load_4d(smem_u32(ring + s * P::kTile + half * kHalf + at * box * 128), kv ? &tmV : &tmK,
-                                        full0 + 8 * s, 64 * half, y, p.h, page);
-                        ++g;
-                        if (i > 0 || kv > 0) continue;
-                        // the part's Q, once its predecessor's last S is done
-                        for (int grp = 0; ok && grp < 2; ++grp) {
-                            if (pt_share(a, p, grp).n == 0) continue;
-                            if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(qempty0 + 8 * grp, (nq[grp] & 1) ^ 1))) {
-                                ok = false;
-                                break;
-                            }
-                            if (lane == 0) mbar_expect_tx(qfull0 + 8 * grp, (uint32_t)(each * a.G) * D * 2);
-                            __syncwarp();
-                            if (lane < HALVES)
-                                tma_load_3d(smem_u32(sQ + grp * P::kTile + lane * kHalf), &tmQ, qfull0 + 8 * grp,
-                                            64 * lane, p.h * a.G, p.row0 + grp * each);
-                            ++nq[grp];
-                        }
-                        if (!ok) break;
-                    }
+            }
+            for (int i = 0; i < k; ++i, g += 2) {
+                const int nb0 = nb, page0 = page, y = key & (a.page_size - 1);
+                if (i + 1 < k) nb = look_up(table, j0 + i + 1, p.seen, page, key);  // ahead: its latency is the L2's
+                const uint32_t s = g % S, ph = (g / S) & 1;
+                if (!wait(empty0 + 8 * s, ph ^ 1)) {
+                    ok = false;
+                    break;
                 }
-                if (!ok || w.u + k >= r.hi) break;
-                w.next(a, k);
+                if (lane == 0) mbar_expect_tx(full0 + 8 * s, (uint32_t)(nb0 * HALVES * box) * 128);
+                __syncwarp();
+                if (lane < nb0 * HALVES)
+                    tma_load_4d(smem_u32(ring + s * P::kTile + (lane / nb0) * kHalf + (lane % nb0) * box * 128),
+                                keys ? &tmK : &tmV, full0 + 8 * s, 64 * (lane / nb0), y, p.h, page0);
+                if (i > 0 || !keys) continue;
+                // the part's Q, once its predecessor's last S is done
+                for (int grp = 0; ok && grp < 2; ++grp) {
+                    if (pt_share(a, p, grp).n == 0) continue;
+                    if (!wait(qempty0 + 8 * grp, (nq[grp] & 1) ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_expect_tx(qfull0 + 8 * grp, (uint32_t)(each * a.G) * D * 2);
+                    __syncwarp();
+                    if (lane < HALVES)
+                        tma_load_3d(smem_u32(sQ + grp * P::kTile + lane * kHalf), &tmQ, qfull0 + 8 * grp, 64 * lane,
+                                    p.h * a.G, p.row0 + grp * each);
+                    ++nq[grp];
+                }
+                if (!ok) break;
             }
         }
-        if (lane == 0) a.cuts[blockIdx.x] = cut;
+        if (keys && ok) {  // the end
+            const uint32_t ps = np % kPtParts;
+            ok = wait(pempty0 + 8 * ps, ((np / kPtParts) & 1) ^ 1);
+            if (ok && lane == 0) {
+                parts[ps].n = 0;
+                mbar_arrive(pfull0 + 8 * ps);
+            }
+        }
+        if (keys && lane == 0) a.cuts[blockIdx.x] = cut;
         if (!ok) {
             if (lane == 0) give_up();
             // the copies in flight land before the block ends
             for (int grp = 0; grp < 2; ++grp)
                 if (nq[grp] > 0) mbar_wait(qfull0 + 8 * grp, (nq[grp] - 1) & 1);
-            for (uint32_t n = g > (uint32_t)S ? g - S : 0; n < g; ++n) mbar_wait(full0 + 8 * (n % S), (n / S) & 1);
+            for (uint32_t back = 2; back <= g && back <= S + 1u; back += 2)
+                mbar_wait(full0 + 8 * ((g - back) % S), ((g - back) / S) & 1);
         }
-    } else if (warp == 1 || warp == 2) {
-        if (lane == 0) {
-            // ---- the products of group warp - 1 ----
-            const int grp = warp - 1;
-            const uint32_t tS = tmem + 128u * grp, tO = tmem + kPtO + 128u * grp;
-            const uint64_t qd = sw128_kmajor_desc(smem_u32(sQ + grp * P::kTile));
-            uint32_t g = 0, np = 0, nq = 0, c = 0;  // tiles, parts, Q tiles, blocks of the group
-            bool ok = true;
-            for (int u = 0; ok && u < stretch; ++np) {
-                const uint32_t ps = np % kPtParts;
-                if (aborted() || !mbar_wait(pfull0 + 8 * ps, (np / kPtParts) & 1)) {
+    } else if (warp < 3) {
+        // ---- the products of group warp - 1: the whole warp waits, one thread, which the
+        // compiler knows to be one, issues (descriptors stay in uniform registers) ----
+        const int grp = warp - 1;
+        const uint32_t tS = tmem + 128u * grp, tO = tmem + kPtO + 128u * grp;
+        const uint64_t qd = sw128_kmajor_desc(smem_u32(sQ + grp * P::kTile));
+        uint32_t g = 0, nq = 0, c = 0;  // tiles, Q tiles, blocks of the group
+        bool ok = true;
+        for (uint32_t np = 0; ok; ++np) {
+            const uint32_t ps = np % kPtParts;
+            if (!wait(pfull0 + 8 * ps, (np / kPtParts) & 1)) {
+                ok = false;
+                break;
+            }
+            const PtPart p = parts[ps];
+            if (p.n == 0) break;
+            const int n = pt_share(a, p, grp).n;
+            if (n > 0 && !wait(qfull0 + 8 * grp, nq++ & 1)) {
+                ok = false;
+                break;
+            }
+            for (int i = 0; i < p.n; ++i, g += 2) {
+                const uint32_t ks = g % S, kph = (g / S) & 1, vs = (g + 1) % S, vph = ((g + 1) / S) & 1;
+                if (!wait(full0 + 8 * ks, kph)) {
                     ok = false;
                     break;
                 }
-                const PtPart p = parts[ps];
-                const int n = pt_share(a, p, grp).n;
-                if (n > 0 && !mbar_wait(qfull0 + 8 * grp, nq++ & 1)) {
-                    ok = false;
-                    break;
-                }
-                for (int i = 0; i < p.n; ++i, g += 2) {
-                    const uint32_t ks = g % S, kph = (g / S) & 1, vs = (g + 1) % S, vph = ((g + 1) / S) & 1;
-                    if (aborted() || !mbar_wait(full0 + 8 * ks, kph)) {
+                if (i >= n) {  // the other group's block only
+                    if (!wait(full0 + 8 * vs, vph)) {
                         ok = false;
                         break;
                     }
-                    if (i >= n) {  // the other group's block only
+                    if (lane == 0) {
                         mbar_arrive(empty0 + 8 * ks);
-                        if (!mbar_wait(full0 + 8 * vs, vph)) {
-                            ok = false;
-                            break;
-                        }
                         mbar_arrive(empty0 + 8 * vs);
-                        continue;
                     }
-                    tc_fence_after();
-                    const uint64_t kd = sw128_kmajor_desc(smem_u32(ring + ks * P::kTile));
+                    continue;
+                }
+                tc_fence_after();
+                const uint64_t kd = sw128_kmajor_desc(smem_u32(ring + ks * P::kTile));
+                if (pt_elect()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         tc_mma<true>(tS, qd + 1024u * (kk >> 2) + 2u * (kk & 3), kd + 1024u * (kk >> 2) + 2u * (kk & 3),
@@ -321,26 +345,31 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     tc_commit(sfull0 + 8 * grp);  // S, and every product before it
                     tc_commit(empty0 + 8 * ks);
                     if (i == n - 1) tc_commit(qempty0 + 8 * grp);
-                    if (aborted() || !mbar_wait(full0 + 8 * vs, vph) || !mbar_wait(probs0 + 8 * grp, c++ & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t vd = pt_v_desc(smem_u32(ring + vs * P::kTile));
+                }
+                __syncwarp();
+                if (!wait(full0 + 8 * vs, vph) || !wait(probs0 + 8 * grp, c++ & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t vd = pt_v_desc(smem_u32(ring + vs * P::kTile));
+                if (pt_elect()) {
 #pragma unroll
                     for (int kk = 0; kk < kPtKeys / 16; ++kk)
                         pt_mma_ts(tO, tS + 8u * kk, vd + 128u * kk, IDESC_O, (kk != 0 || i != 0) ? 1u : 0u);
                     tc_commit(empty0 + 8 * vs);
                     if (i == n - 1) tc_commit(ofull0 + 8 * grp);
                 }
-                u += p.n;
-                mbar_arrive(pempty0 + 8 * ps);
+                __syncwarp();
             }
-            if (!ok) give_up();
-            // all products are done before the block ends
-            tc_commit(done0 + 8 * grp);
-            mbar_wait(done0 + 8 * grp, 0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pempty0 + 8 * ps);
         }
+        if (!ok && lane == 0) give_up();
+        // all products are done before the block ends
+        if (pt_elect()) tc_commit(done0 + 8 * grp);
+        __syncwarp();
+        mbar_wait(done0 + 8 * grp, 0);
     } else if (warp >= 4) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPtHigh));
         // ---- softmax and output of a group: thread = row ----
@@ -352,47 +381,45 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const uint64_t sl2x2 = pt_pack(sl2, sl2);
         uint32_t g = 0, np = 0, c = 0, no = 0;  // tiles, parts, blocks and outputs of the group
         bool ok = true;
-        for (int u = 0; ok && u < stretch; ++np) {
+        for (; ok; ++np) {
             const uint32_t ps = np % kPtParts;
-            if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(pfull0 + 8 * ps, (np / kPtParts) & 1))) {
+            if (!wait(pfull0 + 8 * ps, (np / kPtParts) & 1)) {
                 ok = false;
                 break;
             }
             const PtPart p = parts[ps];
+            if (p.n == 0) break;
             const PtShare sh = pt_share(a, p, grp);
             // rows that are none see what the last one does (their results go nowhere)
             const bool live = tok < sh.tokens;
             const int lim = a.causal && live ? min(p.pos0 + grp * each + tok + 1, sh.seen) : sh.seen;
-            const int wmax = __reduce_max_sync(0xffffffffu, lim), wmin = __reduce_min_sync(0xffffffffu, lim);
+            const int wmin = __reduce_min_sync(0xffffffffu, lim);
             float m = NEG, l = 0.f;
             for (int i = 0; i < sh.n; ++i, ++c) {
                 const int k0 = (p.j0 + i) * kPtKeys;
-                if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(sfull0 + 8 * grp, c & 1))) {
+                if (!wait(sfull0 + 8 * grp, c & 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 uint32_t sv[4][32];
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch)
-                    if (k0 + 32 * ch < wmax) tmem_ld32_async(tS + 32u * ch, sv[ch]);
+                for (int ch = 0; ch < 4; ++ch) tmem_ld32_async(tS + 32u * ch, sv[ch]);
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch)
-                    if (k0 + 32 * ch < wmax) tmem_wait_ld(sv[ch]);
-                float mx[4] = {NEG, NEG, NEG, NEG};
+                for (int ch = 0; ch < 4; ++ch) tmem_wait_ld(sv[ch]);
+                if (k0 + kPtKeys > wmin) {
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    const int c0 = k0 + 32 * ch;
-                    if (c0 >= wmax) continue;
-                    if (c0 + 32 > wmin) {
+                    for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (c0 + e >= lim) sv[ch][e] = __float_as_uint(NEG);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        mx[ch] = pt_max3(mx[ch], __uint_as_float(sv[ch][e]), __uint_as_float(sv[ch][e + 1]));
+                            if (k0 + 32 * ch + e >= lim) sv[ch][e] = __float_as_uint(NEG);
                 }
+                float mx[4] = {NEG, NEG, NEG, NEG};
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch)
+                        mx[ch] = pt_max3(mx[ch], __uint_as_float(sv[ch][e]), __uint_as_float(sv[ch][e + 1]));
                 const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
                 if (i == 0) {
                     m = top;
@@ -421,19 +448,14 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
                     uint32_t pk[16];
-                    if (k0 + 32 * ch < wmax) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float x0, x1;
-                            pt_unpack(pt_fma2(pt_pack(__uint_as_float(sv[ch][e]), __uint_as_float(sv[ch][e + 1])), sl2x2, nref),
-                                      x0, x1);
-                            const float p0 = pt_ex2(x0), p1 = pt_ex2(x1);
-                            sum[(e >> 1) & 1] = pt_add2(sum[(e >> 1) & 1], pt_pack(p0, p1));
-                            pk[e >> 1] = pack_bf16x2(p0, p1);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                    for (int e = 0; e < 32; e += 2) {
+                        float x0, x1;
+                        pt_unpack(pt_fma2(pt_pack(__uint_as_float(sv[ch][e]), __uint_as_float(sv[ch][e + 1])), sl2x2, nref),
+                                  x0, x1);
+                        const float p0 = pt_ex2(x0), p1 = pt_ex2(x1);
+                        sum[(e >> 1) & 1] = pt_add2(sum[(e >> 1) & 1], pt_pack(p0, p1));
+                        pk[e >> 1] = pack_bf16x2(p0, p1);
                     }
                     pt_st16(tS + 16u * ch, pk);
                 }
@@ -444,7 +466,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 if (k0 + kPtKeys > p.seen) {
                     // values of keys that nobody sees
                     const uint32_t v = g + 2 * (uint32_t)i + 1, vs = v % S;
-                    if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * vs, (v / S) & 1))) {
+                    if (!wait(full0 + 8 * vs, (v / S) & 1)) {
                         ok = false;
                         break;
                     }
@@ -464,7 +486,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             if (!ok) break;
             if (sh.tokens > 0) {
                 if (sh.n > 0) {
-                    if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(ofull0 + 8 * grp, no++ & 1))) {
+                    if (!wait(ofull0 + 8 * grp, no++ & 1)) {
                         ok = false;
                         break;
                     }
@@ -510,12 +532,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 }
                 tc_fence_before();
             }
-            u += p.n;
             g += 2 * (uint32_t)p.n;
             __syncwarp();
             if (lane == 0) mbar_arrive(pempty0 + 8 * ps);
         }
-        if (!ok) give_up();
+        if (!ok && lane == 0) give_up();
     }
 
     __syncwarp();
@@ -535,6 +556,7 @@ int start(const PagedProblem& p) {
     if (!paged_args(p, grid, 256, &a)) return LIN_ERR_WORKSPACE;
     const int each = 128 / a.G;  // tokens of a group
     a.TQ = 2 * each;
+    a.lead = kPtLead;
     CUtensorMap tq, tk, tv;
     if (!paged_q_map(&tq, p, each) || !paged_kv_map(&tk, p, p.cache.k, kPtKeys) || !paged_kv_map(&tv, p, p.cache.v, kPtKeys))
         return LIN_ERR_CUDA;
