@@ -50,7 +50,7 @@ struct PagedCut {
 
 struct PagedArgs {
     lin_kv_batch batch;
-    int pages, page_size;
+    int pages, page_size, page_shift;  // page_size = 1 << page_shift
     int Hkv, G, TQ;            // key heads, query heads of each, tokens of a tile
     int causal;
     int lead;                  // units that an item's start and end cost
@@ -255,6 +255,35 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 inline size_t paged_workspace(int C, int R, int D) {
     return align_up(sizeof(PagedCut) * (size_t)C, 256) + (size_t)C * 2 * R * (sizeof(float2) + (size_t)D * sizeof(float));
 }
+
+// A box of the key block at key0: KEYS keys in boxes of a page each (or all of them, when a page
+// holds more). Lane `at` of the first KEYS >> shift lanes, and those as far apart again, has box `at`.
+template <int KEYS>
+struct PagedBox {
+    int shift;       // keys of a box: 1 << shift
+    int at, group;   // this lane's box, and its group of lanes
+    __device__ __forceinline__ explicit PagedBox(const PagedArgs& a) {
+        constexpr int top = KEYS == 128 ? 7 : 6;
+        const int lane = threadIdx.x & 31;
+        shift = min(a.page_shift, top);
+        at = lane & ((KEYS >> shift) - 1);
+        group = lane >> (top - shift);
+    }
+    // The page of this lane's box, pages (outside the map: zeros) where the table names none; -1 when no key
+    // of the box is seen.
+    __device__ __forceinline__ int page(const PagedArgs& a, const int* table, int key0, int seen) const {
+        const int key = key0 + (at << shift);
+        if (key >= seen) return -1;
+        const int g = table[key >> a.page_shift];
+        return g < 0 || g > a.pages ? a.pages : g;
+    }
+    __device__ __forceinline__ int slot(const PagedArgs& a, int key0) const {
+        return (key0 + (at << shift)) & (a.page_size - 1);
+    }
+    __device__ __forceinline__ int count(int key0, int seen) const {
+        return (min(max(seen - key0, 0), KEYS) + (1 << shift) - 1) >> shift;
+    }
+};
 
 // Host side (paged_rows.cu). Maps of the pages of `base` (box: 64 elements x a page's tokens,
 // at most `keys`) and of q (box: 64 elements x the heads of a key head x `tokens`), 128-byte

@@ -115,8 +115,10 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         uint32_t g = 0;
         bool ok = true;
         {
-            const int box = min(a.page_size, kPrKeys);
+            const PagedBox<kPrKeys> box(a);
+            const int half = box.group % HALVES, isv = box.group / HALVES;
             const uint32_t q_bytes = (uint32_t)(a.TQ * a.G) * D * 2;
+            uint32_t s = 0, ph = 1;
             PagedWalk<kPrKeys> w;
             w.start(a, r);
             for (int j0, k; ok && w.part(a, j0, k); w.next(a, k)) {
@@ -125,40 +127,32 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 const int slot = k == w.n ? -1 : 2 * (int)blockIdx.x + (j0 == 0 ? 1 : 0);
                 if (j0 == 0 && k < w.n) cut = {row0, tokens, w.h, w.last_block(r.per)};
                 const int* table = a.batch.block_table + w.b * a.batch.table_stride;
-                for (int i = 0; i < k; ++i) {
-                    const int key0 = (j0 + i) * kPrKeys;
-                    const int nb = (min(max(seen - key0, 0), kPrKeys) + box - 1) / box;
-                    const int boxes = nb * HALVES * 2;
-                    // this lane's box: a page of K or of V, 64 columns of it
-                    int page = a.pages, y = 0, half = 0, isv = 0, at = 0;
-                    if (lane < boxes) {
-                        at = lane % nb;
-                        half = (lane / nb) % HALVES;
-                        isv = lane / (nb * HALVES);
-                        const int key = key0 + at * box;
-                        page = table[key / a.page_size];
-                        // an entry that is no page reads as zeros (a box outside the map)
-                        if (page < 0 || page > a.pages) page = a.pages;
-                        y = key & (a.page_size - 1);
-                    }
-                    const uint32_t s = g % S, ph = (g / S) & 1;
-                    if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(empty0 + 8 * s, ph ^ 1))) {
+                int key0 = j0 * kPrKeys, next = isv < 2 ? box.page(a, table, key0, seen) : -1;
+                for (int i = 0; i < k; ++i, key0 += kPrKeys) {
+                    const int page = next;
+                    if (i + 1 < k && isv < 2) next = box.page(a, table, key0 + kPrKeys, seen);  // ahead: it takes the L2's latency
+                    if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(empty0 + 8 * s, ph))) {
                         ok = false;
                         break;
                     }
                     uint8_t* stage = smem + s * P::kStage;
                     if (lane == 0) {
                         units[s] = PrUnit{key0, seen, i == 0, i == k - 1, row0, tokens, w.h, w.q.pos0 + w.t * a.TQ, slot};
-                        mbar_expect_tx(full0 + 8 * s, (uint32_t)boxes * box * 128 + (i == 0 ? q_bytes : 0));
+                        mbar_expect_tx(full0 + 8 * s,
+                                       (uint32_t)(box.count(key0, seen) * HALVES * 2) * (128u << box.shift) + (i == 0 ? q_bytes : 0));
                     }
                     __syncwarp();
-                    if (lane < boxes)
-                        tma_load_4d(smem_u32(stage + isv * P::kK + half * (kPrKeys * 128) + at * box * 128),
-                                    isv ? &tmV : &tmK, full0 + 8 * s, 64 * half, y, w.h, page);
+                    if (page >= 0 && isv < 2)
+                        tma_load_4d(smem_u32(stage + isv * P::kK + half * (kPrKeys * 128) + ((box.at << box.shift) * 128)),
+                                    isv ? &tmV : &tmK, full0 + 8 * s, 64 * half, box.slot(a, key0), w.h, page);
                     if (i == 0 && lane < HALVES)
                         tma_load_3d(smem_u32(stage + 2 * P::kK + lane * (R * 128)), &tmQ, full0 + 8 * s, 64 * lane,
                                     w.h * a.G, row0);
                     ++g;
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1;
+                    }
                 }
             }
         }
@@ -185,8 +179,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         return __all_sync(0xffffffffu, !aborted() && mbar_wait(join, joins++ & 1));
     };
     const int stretch = (int)(r.hi - r.lo);
-    for (uint32_t g = 0; g < (uint32_t)stretch; ++g) {
-        const uint32_t s = g % S, ph = (g / S) & 1;
+    uint32_t s = 0, ph = 0;
+    for (int g = 0; g < stretch; ++g) {
         if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(full0 + 8 * s, ph))) {
             ok = false;
             break;
@@ -377,6 +371,10 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (zeroed) fence_proxy_async_smem();  // written here, then by the next copy
         __syncwarp();
         if (lane == 0) mbar_arrive(empty0 + 8 * s);
+        if (++s == S) {
+            s = 0;
+            ph ^= 1;
+        }
     }
     if (!ok && lane == 0) give_up();
 }
@@ -464,6 +462,8 @@ bool paged_args(const PagedProblem& p, int grid, int R, PagedArgs* a) {
     a->batch = p.batch;
     a->pages = p.cache.pages;
     a->page_size = p.cache.page_size;
+    a->page_shift = 0;
+    while ((1 << a->page_shift) < p.cache.page_size) ++a->page_shift;
     a->Hkv = p.cache.heads;
     a->G = p.H / p.cache.heads;
     a->TQ = R / a->G;

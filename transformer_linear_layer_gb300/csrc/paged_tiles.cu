@@ -39,8 +39,7 @@ constexpr int kPtKeys = 128;            // keys of a block, and rows of a group
 // compiled to fewer than kPtLaunch: the increase could not be granted.
 constexpr int kPtLaunch = 168, kPtLow = 72, kPtHigh = 216;
 static_assert(128 * kPtLow + 256 * kPtHigh <= kPtThreads * kPtLaunch, "register split");
-constexpr uint32_t kPtTmem = 512;       // S (then P) of group 0, 1 in columns 0-127, 128-255;
-constexpr uint32_t kPtO = 256;          // O in 256 .. and 384 ..
+constexpr uint32_t kPtTmem = 512;
 constexpr int kPtParts = 4;             // parts of items that are described at a time
 constexpr int kPtLead = 1;              // blocks that an item's start and end cost
 constexpr float kPtRise = 8.f;          // base-2 units by which a row may pass its reference
@@ -50,6 +49,11 @@ struct PtShape {
     static constexpr uint32_t kTile = kPtKeys * D * 2;      // K, V or Q: halves of 64 columns, 16 KiB each
     static constexpr int S = D == 64 ? 10 : 5;              // tiles of the ring
     static constexpr size_t kSmem = 1024 + (2 + S) * (size_t)kTile;
+    // TMEM columns of a group: S (128), O (D) and P (64). Heads of 64 leave room for P beside
+    // S, so that the next block's S is computed while this one's exponentials are; with
+    // 128 columns of O a group P takes the place of the S that it came from.
+    static constexpr bool kApart = D == 64;
+    static constexpr uint32_t kS = 0, kP = kApart ? 256 : 0, kO = kApart ? 384 : 256, kPStep = kApart ? 64 : 128;
 };
 
 struct PtPart {       // a block's part of an item
@@ -150,7 +154,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     constexpr uint32_t IDESC_O = make_idesc(1u, 128, D, false, true);
 
     extern __shared__ uint8_t raw[];
-    __shared__ alignas(8) uint64_t bars[2 * S + 2 * kPtParts + 12];
+    __shared__ alignas(8) uint64_t bars[2 * S + 2 * kPtParts + 18];
     __shared__ PtPart parts[kPtParts];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
@@ -159,7 +163,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     uint8_t* ring = smem + 2 * P::kTile;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S, pfull0 = empty0 + 8 * S,
                    pempty0 = pfull0 + 8 * kPtParts, qfull0 = pempty0 + 8 * kPtParts, qempty0 = qfull0 + 16,
-                   sfull0 = qempty0 + 16, probs0 = sfull0 + 16, ofull0 = probs0 + 16, done0 = ofull0 + 16;
+                   sfull0 = qempty0 + 16, sread0 = sfull0 + 16, probs0 = sread0 + 16, pv0 = probs0 + 32, ofull0 = pv0 + 16,
+                   done0 = ofull0 + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -175,7 +180,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             mbar_init(qfull0 + 8 * g, 1);
             mbar_init(qempty0 + 8 * g, 1);
             mbar_init(sfull0 + 8 * g, 1);
-            mbar_init(probs0 + 8 * g, 4);
+            mbar_init(sread0 + 8 * g, 4);
+            mbar_init(probs0 + 16 * g, 4);         // keys 0-63 and 64-127 of the block
+            mbar_init(probs0 + 16 * g + 8, 4);
+            mbar_init(pv0 + 8 * g, 1);
             mbar_init(ofull0 + 8 * g, 1);
             mbar_init(done0 + 8 * g, 1);
         }
@@ -207,21 +215,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         // ---- TMA: warp 0 the parts, Q and K, warp 3 V; whole warps walk the stretch ----
         const bool keys = warp == 0;
         PagedCut cut = {0, 0, 0, 0};
-        uint32_t g = keys ? 0 : 1, np = 0, nq[2] = {0, 0};  // the next tile; parts and Q tiles issued
+        uint32_t st = keys ? 0 : 1, ph = 1, issued = 0, np = 0, nq[2] = {0, 0};  // the next tile; what has been issued
         bool ok = true;
-        const int box = min(a.page_size, kPtKeys), each = a.TQ / 2;
-        // this lane's box of key block `blk`: its page, and how many boxes there are
-        auto look_up = [&](const int* table, int blk, int seen, int& page, int& key) {
-            const int nb = (min(max(seen - blk * kPtKeys, 0), kPtKeys) + box - 1) / box;
-            page = a.pages;
-            key = 0;
-            if (lane < nb * HALVES) {
-                key = blk * kPtKeys + (lane % nb) * box;
-                page = table[key / a.page_size];
-                if (page < 0 || page > a.pages) page = a.pages;  // no page: a box outside the map, zeros
-            }
-            return nb;
-        };
+        const int each = a.TQ / 2;
+        const PagedBox<kPtKeys> box(a);
+        const bool mine = box.group < HALVES;
+        const uint32_t to = smem_u32(ring) + box.group * kHalf + ((box.at << box.shift) * 128);
         PagedWalk<kPtKeys> w;
         w.start(a, r);
         for (int j0, k; ok && w.part(a, j0, k); w.next(a, k)) {
@@ -235,7 +234,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             p.n = k;
             p.slot = k == w.n ? -1 : 2 * (int)blockIdx.x + (j0 == 0 ? 1 : 0);
             const int* table = a.batch.block_table + w.b * a.batch.table_stride;
-            int page, key, nb = look_up(table, j0, p.seen, page, key);
+            int key0 = j0 * kPtKeys, next = mine ? box.page(a, table, key0, p.seen) : -1;
             if (keys) {
                 if (j0 == 0 && k < w.n) cut = {p.row0, p.tokens, p.h, w.last_block(r.per)};
                 const uint32_t ps = np % kPtParts;
@@ -249,19 +248,24 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 }
                 ++np;
             }
-            for (int i = 0; i < k; ++i, g += 2) {
-                const int nb0 = nb, page0 = page, y = key & (a.page_size - 1);
-                if (i + 1 < k) nb = look_up(table, j0 + i + 1, p.seen, page, key);  // ahead: its latency is the L2's
-                const uint32_t s = g % S, ph = (g / S) & 1;
-                if (!wait(empty0 + 8 * s, ph ^ 1)) {
+            for (int i = 0; i < k; ++i, key0 += kPtKeys) {
+                const int page = next;
+                if (i + 1 < k && mine) next = box.page(a, table, key0 + kPtKeys, p.seen);  // ahead: it takes the L2's latency
+                if (!wait(empty0 + 8 * st, ph)) {
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_expect_tx(full0 + 8 * s, (uint32_t)(nb0 * HALVES * box) * 128);
+                if (lane == 0)
+                    mbar_expect_tx(full0 + 8 * st, (uint32_t)(box.count(key0, p.seen) * HALVES) * (128u << box.shift));
                 __syncwarp();
-                if (lane < nb0 * HALVES)
-                    tma_load_4d(smem_u32(ring + s * P::kTile + (lane / nb0) * kHalf + (lane % nb0) * box * 128),
-                                keys ? &tmK : &tmV, full0 + 8 * s, 64 * (lane / nb0), y, p.h, page0);
+                if (page >= 0)
+                    tma_load_4d(to + st * P::kTile, keys ? &tmK : &tmV, full0 + 8 * st, 64 * box.group, box.slot(a, key0),
+                                p.h, page);
+                ++issued;
+                if ((st += 2) >= S) {
+                    st -= S;
+                    ph ^= 1;
+                }
                 if (i > 0 || !keys) continue;
                 // the part's Q, once its predecessor's last S is done
                 for (int grp = 0; ok && grp < 2; ++grp) {
@@ -294,17 +298,47 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             // the copies in flight land before the block ends
             for (int grp = 0; grp < 2; ++grp)
                 if (nq[grp] > 0) mbar_wait(qfull0 + 8 * grp, (nq[grp] - 1) & 1);
-            for (uint32_t back = 2; back <= g && back <= S + 1u; back += 2)
-                mbar_wait(full0 + 8 * ((g - back) % S), ((g - back) / S) & 1);
+            for (uint32_t back = 1; back <= issued && back <= (S + 1u) / 2; ++back) {
+                const uint32_t g = 2 * (issued - back) + (keys ? 0 : 1);
+                mbar_wait(full0 + 8 * (g % S), (g / S) & 1);
+            }
         }
     } else if (warp < 3) {
         // ---- the products of group warp - 1: the whole warp waits, one thread, which the
         // compiler knows to be one, issues (descriptors stay in uniform registers) ----
         const int grp = warp - 1;
-        const uint32_t tS = tmem + 128u * grp, tO = tmem + kPtO + 128u * grp;
+        const uint32_t tS = tmem + P::kS + 128u * grp, tP = tmem + P::kP + P::kPStep * grp, tO = tmem + P::kO + P::kPStep * grp;
         const uint64_t qd = sw128_kmajor_desc(smem_u32(sQ + grp * P::kTile));
-        uint32_t g = 0, nq = 0, c = 0;  // tiles, Q tiles, blocks of the group
+        const uint64_t kd0 = sw128_kmajor_desc(smem_u32(ring)), vd0 = pt_v_desc(smem_u32(ring));
+        uint32_t ks = 0, kph = 0, vs = 1, vph = 0;  // the next K and V tile
+        uint32_t nq = 0, cs = 0, c = 0;             // Q tiles, blocks whose S is issued, blocks
         bool ok = true;
+        auto step = [&](uint32_t& s, uint32_t& ph) {
+            if ((s += 2) >= S) {
+                s -= S;
+                ph ^= 1;
+            }
+        };
+        // S of the group's next block; its columns have been read
+        auto scores = [&](bool last) {
+            if (!wait(full0 + 8 * ks, kph)) return false;
+            if (P::kApart && cs > 0 && !wait(sread0 + 8 * grp, (cs - 1) & 1)) return false;
+            tc_fence_after();
+            if (pt_elect()) {
+                const uint64_t kd = kd0 + ks * (P::kTile >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_mma<true>(tS, qd + 1024u * (kk >> 2) + 2u * (kk & 3), kd + 1024u * (kk >> 2) + 2u * (kk & 3),
+                                 IDESC_S, kk != 0 ? 1u : 0u);
+                tc_commit(sfull0 + 8 * grp);
+                tc_commit(empty0 + 8 * ks);
+                if (last) tc_commit(qempty0 + 8 * grp);
+            }
+            __syncwarp();
+            step(ks, kph);
+            ++cs;
+            return true;
+        };
         for (uint32_t np = 0; ok; ++np) {
             const uint32_t ps = np % kPtParts;
             if (!wait(pfull0 + 8 * ps, (np / kPtParts) & 1)) {
@@ -314,53 +348,49 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             const PtPart p = parts[ps];
             if (p.n == 0) break;
             const int n = pt_share(a, p, grp).n;
-            if (n > 0 && !wait(qfull0 + 8 * grp, nq++ & 1)) {
-                ok = false;
-                break;
-            }
-            for (int i = 0; i < p.n; ++i, g += 2) {
-                const uint32_t ks = g % S, kph = (g / S) & 1, vs = (g + 1) % S, vph = ((g + 1) / S) & 1;
-                if (!wait(full0 + 8 * ks, kph)) {
+            if (n > 0) ok = wait(qfull0 + 8 * grp, nq++ & 1) && scores(n == 1);
+            for (int i = 0; ok && i < n; ++i) {
+                if (P::kApart && i + 1 < n && !(ok = scores(i + 2 == n))) break;
+                if (!wait(full0 + 8 * vs, vph)) {
                     ok = false;
                     break;
                 }
-                if (i >= n) {  // the other group's block only
-                    if (!wait(full0 + 8 * vs, vph)) {
+                const uint64_t vd = vd0 + vs * (P::kTile >> 4);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {  // the first 64 keys while the others are exponentiated
+                    if (!wait(probs0 + 16 * grp + 8 * half, c & 1)) {
                         ok = false;
                         break;
                     }
-                    if (lane == 0) {
-                        mbar_arrive(empty0 + 8 * ks);
-                        mbar_arrive(empty0 + 8 * vs);
-                    }
-                    continue;
-                }
-                tc_fence_after();
-                const uint64_t kd = sw128_kmajor_desc(smem_u32(ring + ks * P::kTile));
-                if (pt_elect()) {
+                    tc_fence_after();
+                    if (pt_elect()) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        tc_mma<true>(tS, qd + 1024u * (kk >> 2) + 2u * (kk & 3), kd + 1024u * (kk >> 2) + 2u * (kk & 3),
-                                     IDESC_S, kk != 0 ? 1u : 0u);
-                    tc_commit(sfull0 + 8 * grp);  // S, and every product before it
-                    tc_commit(empty0 + 8 * ks);
-                    if (i == n - 1) tc_commit(qempty0 + 8 * grp);
+                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                            pt_mma_ts(tO, tP + 8u * kk, vd + 128u * kk, IDESC_O, (kk != 0 || i != 0) ? 1u : 0u);
+                        if (half == 1) {
+                            tc_commit(empty0 + 8 * vs);
+                            if (P::kApart) tc_commit(pv0 + 8 * grp);
+                            if (i == n - 1) tc_commit(ofull0 + 8 * grp);
+                        }
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (!wait(full0 + 8 * vs, vph) || !wait(probs0 + 8 * grp, c++ & 1)) {
+                if (!ok) break;
+                ++c;
+                step(vs, vph);
+                if (!P::kApart && i + 1 < n) ok = scores(i + 2 == n);
+            }
+            for (int i = n; ok && i < p.n; ++i) {  // the other group's blocks only
+                if (!wait(full0 + 8 * ks, kph) || !wait(full0 + 8 * vs, vph)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                const uint64_t vd = pt_v_desc(smem_u32(ring + vs * P::kTile));
-                if (pt_elect()) {
-#pragma unroll
-                    for (int kk = 0; kk < kPtKeys / 16; ++kk)
-                        pt_mma_ts(tO, tS + 8u * kk, vd + 128u * kk, IDESC_O, (kk != 0 || i != 0) ? 1u : 0u);
-                    tc_commit(empty0 + 8 * vs);
-                    if (i == n - 1) tc_commit(ofull0 + 8 * grp);
+                if (lane == 0) {
+                    mbar_arrive(empty0 + 8 * ks);
+                    mbar_arrive(empty0 + 8 * vs);
                 }
-                __syncwarp();
+                step(ks, kph);
+                step(vs, vph);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(pempty0 + 8 * ps);
@@ -375,8 +405,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         // ---- softmax and output of a group: thread = row ----
         const int grp = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane;
         const int each = a.TQ / 2, tok = row / a.G, sub = row - tok * a.G;
-        const uint32_t tS = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128u * grp;
-        const uint32_t tO = tmem + (static_cast<uint32_t>(32 * q) << 16) + kPtO + 128u * grp;
+        const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+        const uint32_t tS = tmem + lanes + P::kS + 128u * grp, tP = tmem + lanes + P::kP + P::kPStep * grp,
+                       tO = tmem + lanes + P::kO + P::kPStep * grp;
         const float NEG = -INFINITY, sl2 = a.scale_log2;
         const uint64_t sl2x2 = pt_pack(sl2, sl2);
         uint32_t g = 0, np = 0, c = 0, no = 0;  // tiles, parts, blocks and outputs of the group
@@ -407,6 +438,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 for (int ch = 0; ch < 4; ++ch) tmem_ld32_async(tS + 32u * ch, sv[ch]);
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) tmem_wait_ld(sv[ch]);
+                if (P::kApart) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sread0 + 8 * grp);
+                }
                 if (k0 + kPtKeys > wmin) {
 #pragma unroll
                     for (int ch = 0; ch < 4; ++ch)
@@ -421,6 +457,28 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     for (int ch = 0; ch < 4; ++ch)
                         mx[ch] = pt_max3(mx[ch], __uint_as_float(sv[ch][e]), __uint_as_float(sv[ch][e + 1]));
                 const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                if (k0 + kPtKeys > p.seen) {
+                    // values of keys that nobody sees
+                    const uint32_t v = g + 2 * (uint32_t)i + 1, vs = v % S;
+                    if (!wait(full0 + 8 * vs, (v / S) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (k0 + row >= p.seen) {
+                        uint8_t* dst = ring + vs * P::kTile + row * 128;
+#pragma unroll
+                        for (int x = 0; x < D / 8; ++x)
+                            *reinterpret_cast<uint4*>(dst + (x >> 3) * kHalf + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                // The product before this block's is done: its probabilities may be overwritten and O
+                // scaled (with P in S's place, S says so)
+                if (P::kApart && c > 0 && !wait(pv0 + 8 * grp, (c - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                if (P::kApart) tc_fence_after();
                 if (i == 0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, (top - m) * sl2 > kPtRise)) {
@@ -457,31 +515,18 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                         sum[(e >> 1) & 1] = pt_add2(sum[(e >> 1) & 1], pt_pack(p0, p1));
                         pk[e >> 1] = pack_bf16x2(p0, p1);
                     }
-                    pt_st16(tS + 16u * ch, pk);
+                    pt_st16(tP + 16u * ch, pk);
+                    if (ch & 1) {
+                        pt_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(probs0 + 16 * grp + 4 * (ch - 1));
+                    }
                 }
                 float la, lb, lc, ld;
                 pt_unpack(sum[0], la, lb);
                 pt_unpack(sum[1], lc, ld);
                 l += (la + lb) + (lc + ld);
-                if (k0 + kPtKeys > p.seen) {
-                    // values of keys that nobody sees
-                    const uint32_t v = g + 2 * (uint32_t)i + 1, vs = v % S;
-                    if (!wait(full0 + 8 * vs, (v / S) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    if (k0 + row >= p.seen) {
-                        uint8_t* dst = ring + vs * P::kTile + row * 128;
-#pragma unroll
-                        for (int x = 0; x < D / 8; ++x)
-                            *reinterpret_cast<uint4*>(dst + (x >> 3) * kHalf + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                }
-                pt_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(probs0 + 8 * grp);
             }
             if (!ok) break;
             if (sh.tokens > 0) {
