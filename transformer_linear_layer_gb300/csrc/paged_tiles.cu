@@ -16,11 +16,11 @@
 //               the columns that S had: nothing of the scores passes through shared memory.
 //   warps 4-7,  softmax of group 0 and 1, a thread per row: scores out of TMEM, scaled to
 //   warps 8-11  base-2 units by a packed FMA, exponentiated, rounded to bf16, back into TMEM.
-//               A commit of S also says that the product before it is done, so that O can
-//               be scaled when the reference for the exponents moves. That need not be the maximum: it stays
-//               where it is while no row of the warp has risen by more than 2^8, which keeps sums and
-//               probabilities in range (bf16 keeps its relative precision) and nearly always saves
-//               the trip of O through the registers.
+//               The reference for the exponents need not be the maximum: it is that of an
+//               item's first 64 keys, and stays while no row of the warp has risen above it by more than
+//               2^8, which keeps sums and probabilities in range (bf16 keeps its relative precision). So
+//               the exponentials do not wait for the maximum, which is only looked at after them; in the rare case
+//               that it has risen, O is scaled and the 64 keys are exponentiated again.
 // Keys past the last one that a row of the tile sees are not loaded where they fill a box, and their
 // values are set to zero in shared memory where they do not: a probability of 0 must not meet a
 // NaN in slots that were never written.
@@ -154,16 +154,16 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     constexpr uint32_t IDESC_O = make_idesc(1u, 128, D, false, true);
 
     extern __shared__ uint8_t raw[];
-    __shared__ alignas(8) uint64_t bars[2 * S + 2 * kPtParts + 18];
+    __shared__ alignas(8) uint64_t bars[2 * S + 2 * kPtParts + 20];
     __shared__ PtPart parts[kPtParts];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;
     uint8_t* ring = smem + 2 * P::kTile;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S, pfull0 = empty0 + 8 * S,
                    pempty0 = pfull0 + 8 * kPtParts, qfull0 = pempty0 + 8 * kPtParts, qempty0 = qfull0 + 16,
-                   sfull0 = qempty0 + 16, sread0 = sfull0 + 16, probs0 = sread0 + 16, pv0 = probs0 + 32, ofull0 = pv0 + 16,
+                   sfull0 = qempty0 + 16, sread0 = sfull0 + 16, probs0 = sread0 + 16, pv0 = probs0 + 32, pvhalf0 = pv0 + 16,
+                   ofull0 = pvhalf0 + 16,
                    done0 = ofull0 + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -184,10 +184,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             mbar_init(probs0 + 16 * g, 4);         // keys 0-63 and 64-127 of the block
             mbar_init(probs0 + 16 * g + 8, 4);
             mbar_init(pv0 + 8 * g, 1);
+            mbar_init(pvhalf0 + 8 * g, 1);
             mbar_init(ofull0 + 8 * g, 1);
             mbar_init(done0 + 8 * g, 1);
         }
-        s_abort = 0;
         mbar_fence_init();
         tma_prefetch_map(&tmQ);
         tma_prefetch_map(&tmK);
@@ -201,13 +201,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     tc_fence_after();
     const uint32_t tmem = s_tmem;
 
-    auto give_up = [&]() {
-        atomicExch(&s_abort, 1);
-        atomicExch(a.status, (int)LIN_ERR_DEVICE_TIMEOUT);
-    };
+    auto give_up = [&]() { atomicExch(a.status, (int)LIN_ERR_DEVICE_TIMEOUT); };
     // A warp's wait: all lanes agree on whether it ended.
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, *(volatile int*)&s_abort == 0 && mbar_wait(bar, parity)) != 0;
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
     };
 
     if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtLow));
@@ -319,25 +316,25 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 ph ^= 1;
             }
         };
-        // S of the group's next block; its columns have been read
-        auto scores = [&](bool last) {
-            if (!wait(full0 + 8 * ks, kph)) return false;
-            if (P::kApart && cs > 0 && !wait(sread0 + 8 * grp, (cs - 1) & 1)) return false;
-            tc_fence_after();
-            if (pt_elect()) {
-                const uint64_t kd = kd0 + ks * (P::kTile >> 4);
+        // S of the group's next block, issued by one thread once its keys are there and, with
+        // P beside it, its columns have been read
+        auto ready = [&]() {
+            return wait(full0 + 8 * ks, kph) && (!P::kApart || cs == 0 || wait(sread0 + 8 * grp, (cs - 1) & 1));
+        };
+        auto issue = [&](bool last) {
+            const uint64_t kd = kd0 + ks * (P::kTile >> 4);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma<true>(tS, qd + 1024u * (kk >> 2) + 2u * (kk & 3), kd + 1024u * (kk >> 2) + 2u * (kk & 3),
-                                 IDESC_S, kk != 0 ? 1u : 0u);
-                tc_commit(sfull0 + 8 * grp);
-                tc_commit(empty0 + 8 * ks);
-                if (last) tc_commit(qempty0 + 8 * grp);
-            }
+            for (int kk = 0; kk < D / 16; ++kk)
+                tc_mma<true>(tS, qd + 1024u * (kk >> 2) + 2u * (kk & 3), kd + 1024u * (kk >> 2) + 2u * (kk & 3), IDESC_S,
+                             kk != 0 ? 1u : 0u);
+            tc_commit(sfull0 + 8 * grp);  // S, and every product before it
+            tc_commit(empty0 + 8 * ks);
+            if (last) tc_commit(qempty0 + 8 * grp);
+        };
+        auto issued = [&]() {
             __syncwarp();
             step(ks, kph);
             ++cs;
-            return true;
         };
         for (uint32_t np = 0; ok; ++np) {
             const uint32_t ps = np % kPtParts;
@@ -348,37 +345,49 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             const PtPart p = parts[ps];
             if (p.n == 0) break;
             const int n = pt_share(a, p, grp).n;
-            if (n > 0) ok = wait(qfull0 + 8 * grp, nq++ & 1) && scores(n == 1);
-            for (int i = 0; ok && i < n; ++i) {
-                if (P::kApart && i + 1 < n && !(ok = scores(i + 2 == n))) break;
-                if (!wait(full0 + 8 * vs, vph)) {
-                    ok = false;
-                    break;
-                }
-                const uint64_t vd = vd0 + vs * (P::kTile >> 4);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {  // the first 64 keys while the others are exponentiated
-                    if (!wait(probs0 + 16 * grp + 8 * half, c & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (pt_elect()) {
-#pragma unroll
-                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                            pt_mma_ts(tO, tP + 8u * kk, vd + 128u * kk, IDESC_O, (kk != 0 || i != 0) ? 1u : 0u);
-                        if (half == 1) {
-                            tc_commit(empty0 + 8 * vs);
-                            if (P::kApart) tc_commit(pv0 + 8 * grp);
-                            if (i == n - 1) tc_commit(ofull0 + 8 * grp);
-                        }
-                    }
-                    __syncwarp();
-                }
+            if (n > 0) {
+                ok = wait(qfull0 + 8 * grp, nq++ & 1) && ready();
                 if (!ok) break;
+                tc_fence_after();
+                if (pt_elect()) issue(n == 1);
+                issued();
+            }
+            for (int i = 0; ok && i < n; ++i) {
+                const bool more = i + 1 < n;
+                if (P::kApart && more) {
+                    if (!(ok = ready())) break;
+                    tc_fence_after();
+                    if (pt_elect()) issue(i + 2 == n);
+                    issued();
+                }
+                // the first 64 keys while the others are exponentiated
+                if (!(ok = wait(full0 + 8 * vs, vph) && wait(probs0 + 16 * grp, c & 1))) break;
+                tc_fence_after();
+                const uint64_t vd = vd0 + vs * (P::kTile >> 4);
+                if (pt_elect()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        pt_mma_ts(tO, tP + 8u * kk, vd + 128u * kk, IDESC_O, (kk != 0 || i != 0) ? 1u : 0u);
+                    tc_commit(pvhalf0 + 8 * grp);
+                }
+                __syncwarp();
+                if (!P::kApart && more && !(ok = ready())) break;
+                if (!(ok = wait(probs0 + 16 * grp + 8, c & 1))) break;
+                tc_fence_after();
+                if (pt_elect()) {
+#pragma unroll
+                    for (int kk = 4; kk < 8; ++kk) pt_mma_ts(tO, tP + 8u * kk, vd + 128u * kk, IDESC_O, 1u);
+                    if (P::kApart) tc_commit(pv0 + 8 * grp);
+                    if (!more) tc_commit(ofull0 + 8 * grp);
+                    if (!P::kApart && more) issue(i + 2 == n);
+                    tc_commit(empty0 + 8 * vs);
+                }
+                if (!P::kApart && more)
+                    issued();
+                else
+                    __syncwarp();
                 ++c;
                 step(vs, vph);
-                if (!P::kApart && i + 1 < n) ok = scores(i + 2 == n);
             }
             for (int i = n; ok && i < p.n; ++i) {  // the other group's blocks only
                 if (!wait(full0 + 8 * ks, kph) || !wait(full0 + 8 * vs, vph)) {
@@ -425,7 +434,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             const bool live = tok < sh.tokens;
             const int lim = a.causal && live ? min(p.pos0 + grp * each + tok + 1, sh.seen) : sh.seen;
             const int wmin = __reduce_min_sync(0xffffffffu, lim);
-            float m = NEG, l = 0.f;
+            float m = NEG, l = 0.f;  // the reference of the exponents (raw score), the total
             for (int i = 0; i < sh.n; ++i, ++c) {
                 const int k0 = (p.j0 + i) * kPtKeys;
                 if (!wait(sfull0 + 8 * grp, c & 1)) {
@@ -433,30 +442,13 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     break;
                 }
                 tc_fence_after();
-                uint32_t sv[4][32];
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch) tmem_ld32_async(tS + 32u * ch, sv[ch]);
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch) tmem_wait_ld(sv[ch]);
-                if (P::kApart) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sread0 + 8 * grp);
-                }
-                if (k0 + kPtKeys > wmin) {
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (k0 + 32 * ch + e >= lim) sv[ch][e] = __float_as_uint(NEG);
-                }
-                float mx[4] = {NEG, NEG, NEG, NEG};
-#pragma unroll
-                for (int e = 0; e < 32; e += 2)
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch)
-                        mx[ch] = pt_max3(mx[ch], __uint_as_float(sv[ch][e]), __uint_as_float(sv[ch][e + 1]));
-                const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                uint32_t sv[2][2][32];
+                tmem_ld32_async(tS, sv[0][0]);
+                tmem_ld32_async(tS + 32u, sv[0][1]);
+                tmem_wait_ld(sv[0][0]);
+                tmem_wait_ld(sv[0][1]);
+                tmem_ld32_async(tS + 64u, sv[1][0]);
+                tmem_ld32_async(tS + 96u, sv[1][1]);
                 if (k0 + kPtKeys > p.seen) {
                     // values of keys that nobody sees
                     const uint32_t v = g + 2 * (uint32_t)i + 1, vs = v % S;
@@ -472,61 +464,103 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     }
                     fence_proxy_async_smem();
                 }
-                // The product before this block's is done: its probabilities may be overwritten and O
-                // scaled (with P in S's place, S says so)
-                if (P::kApart && c > 0 && !wait(pv0 + 8 * grp, (c - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                if (P::kApart) tc_fence_after();
-                if (i == 0) {
-                    m = top;
-                } else if (__any_sync(0xffffffffu, (top - m) * sl2 > kPtRise)) {
-                    const float alpha = pt_ex2((m - (top == NEG ? 0.f : top)) * sl2);
-                    m = top;
-                    l *= alpha;
 #pragma unroll
-                    for (int h = 0; h < D / 32; ++h) {
-                        uint32_t ov[32];
-                        tmem_ld32_async(tO + 32u * h, ov);
-                        tmem_wait_ld(ov);
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t x[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                x[e] = __float_as_uint(__uint_as_float(ov[16 * half + e]) * alpha);
-                            pt_st16(tO + 32u * h + 16u * half, x);
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t(&x)[2][32] = sv[half];
+                    if (half == 1) {
+                        tmem_wait_ld(x[0]);
+                        tmem_wait_ld(x[1]);
+                        if (P::kApart) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(sread0 + 8 * grp);
                         }
                     }
-                }
-                const float ref = m == NEG ? 0.f : m;
-                const uint64_t nref = pt_pack(-ref * sl2, -ref * sl2);
-                uint64_t sum[2] = {0ull, 0ull};
+                    const int c0 = k0 + 64 * half;
+                    if (c0 + 64 > wmin) {
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t pk[16];
+                        for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float x0, x1;
-                        pt_unpack(pt_fma2(pt_pack(__uint_as_float(sv[ch][e]), __uint_as_float(sv[ch][e + 1])), sl2x2, nref),
-                                  x0, x1);
-                        const float p0 = pt_ex2(x0), p1 = pt_ex2(x1);
-                        sum[(e >> 1) & 1] = pt_add2(sum[(e >> 1) & 1], pt_pack(p0, p1));
-                        pk[e >> 1] = pack_bf16x2(p0, p1);
+                            for (int e = 0; e < 32; ++e)
+                                if (c0 + 32 * ch + e >= lim) x[ch][e] = __float_as_uint(NEG);
                     }
-                    pt_st16(tP + 16u * ch, pk);
-                    if (ch & 1) {
-                        pt_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(probs0 + 16 * grp + 4 * (ch - 1));
+                    float mx[4] = {NEG, NEG, NEG, NEG};
+                    auto top = [&]() {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2)
+#pragma unroll
+                            for (int ch = 0; ch < 4; ++ch)
+                                mx[ch] = pt_max3(mx[ch], __uint_as_float(x[ch >> 1][16 * (ch & 1) + e]),
+                                                 __uint_as_float(x[ch >> 1][16 * (ch & 1) + e + 1]));
+                        return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    };
+                    uint32_t pk[2][16];
+                    float sum;
+                    auto exponentials = [&]() {
+                        const float ref = m == NEG ? 0.f : m;
+                        const uint64_t nref = pt_pack(-ref * sl2, -ref * sl2);
+                        uint64_t s2[2] = {0ull, 0ull};
+#pragma unroll
+                        for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                float x0, x1;
+                                pt_unpack(pt_fma2(pt_pack(__uint_as_float(x[ch][e]), __uint_as_float(x[ch][e + 1])), sl2x2,
+                                                  nref),
+                                          x0, x1);
+                                const float p0 = pt_ex2(x0), p1 = pt_ex2(x1);
+                                s2[(e >> 1) & 1] = pt_add2(s2[(e >> 1) & 1], pt_pack(p0, p1));
+                                pk[ch][e >> 1] = pack_bf16x2(p0, p1);
+                            }
+                        float la, lb, lc, ld;
+                        pt_unpack(s2[0], la, lb);
+                        pt_unpack(s2[1], lc, ld);
+                        sum = (la + lb) + (lc + ld);
+                    };
+                    if (half == 0 && i == 0) m = top();
+                    exponentials();
+                    if (half == 1 || i > 0) {
+                        const float now = fmaxf(m, top());
+                        if (__any_sync(0xffffffffu, (now - m) * sl2 > kPtRise)) {
+                            // The reference moves: the products so far are done, what they summed is
+                            // scaled, and this half is exponentiated again.
+                            if (half == 1 ? !wait(pvhalf0 + 8 * grp, c & 1)
+                                          : P::kApart && !wait(pv0 + 8 * grp, (c - 1) & 1)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const float alpha = pt_ex2((m - (now == NEG ? 0.f : now)) * sl2);
+                            m = now;
+                            l *= alpha;
+#pragma unroll 1
+                            for (int h = 0; h < D; h += 16) {
+                                uint32_t ov[16];
+                                tmem_ld16(tO + h, ov);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                                pt_st16(tO + h, ov);
+                            }
+                            exponentials();
+                        }
                     }
+                    l += sum;
+                    // with P beside S, the product that read the last block's probabilities is done
+                    if (P::kApart && half == 0 && c > 0) {
+                        if (!wait(pv0 + 8 * grp, (c - 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+                    pt_st16(tP + 32u * half, pk[0]);
+                    pt_st16(tP + 32u * half + 16u, pk[1]);
+                    pt_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(probs0 + 16 * grp + 8 * half);
                 }
-                float la, lb, lc, ld;
-                pt_unpack(sum[0], la, lb);
-                pt_unpack(sum[1], lc, ld);
-                l += (la + lb) + (lc + ld);
+                if (!ok) break;
             }
             if (!ok) break;
             if (sh.tokens > 0) {
