@@ -17,10 +17,10 @@
 //   warps 4-7,  softmax of group 0 and 1, a thread per row: scores out of TMEM, scaled to
 //   warps 8-11  base-2 units by a packed FMA, exponentiated, rounded to bf16, back into TMEM.
 //               The reference for the exponents need not be the maximum: it is that of an
-//               item's first 64 keys, and stays while no row of the warp has risen above it by more than
-//               2^8, which keeps sums and probabilities in range (bf16 keeps its relative precision). So
-//               the exponentials do not wait for the maximum, which is only looked at after them; in the rare case
-//               that it has risen, O is scaled and the 64 keys are exponentiated again.
+//               item's first 64 keys, and stays while 64 probabilities of a row add up to at most 2^16
+//               (bf16 keeps its relative precision; the argument of an exponential stays below 16, and its
+//               rounding below 2^-20). So nothing waits for a maximum and none is taken; in the
+//               rare case that the scores have risen, O is scaled and the 64 keys are exponentiated again.
 // Keys past the last one that a row of the tile sees are not loaded where they fill a box, and their
 // values are set to zero in shared memory where they do not: a probability of 0 must not meet a
 // NaN in slots that were never written.
@@ -42,7 +42,8 @@ static_assert(128 * kPtLow + 256 * kPtHigh <= kPtThreads * kPtLaunch, "register 
 constexpr uint32_t kPtTmem = 512;
 constexpr int kPtParts = 4;             // parts of items that are described at a time
 constexpr int kPtLead = 1;              // blocks that an item's start and end cost
-constexpr float kPtRise = 8.f;          // base-2 units by which a row may pass its reference
+constexpr int kPtBatch = 16;             // exponentials in flight
+constexpr float kPtRise = 65536.f;       // what 64 probabilities may add up to before their reference moves
 
 template <int D>
 struct PtShape {
@@ -65,9 +66,10 @@ struct PtPart {       // a block's part of an item
     int slot;         // the workspace's slot, or -1: the item is whole
 };
 
+// volatile: in the order that they are written in
 __device__ __forceinline__ float pt_ex2(float x) {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ uint64_t pt_pack(float lo, float hi) {
@@ -484,8 +486,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                             for (int e = 0; e < 32; ++e)
                                 if (c0 + 32 * ch + e >= lim) x[ch][e] = __float_as_uint(NEG);
                     }
-                    float mx[4] = {NEG, NEG, NEG, NEG};
                     auto top = [&]() {
+                        float mx[4] = {NEG, NEG, NEG, NEG};
 #pragma unroll
                         for (int e = 0; e < 16; e += 2)
 #pragma unroll
@@ -496,54 +498,54 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     };
                     uint32_t pk[2][16];
                     float sum;
-                    auto exponentials = [&]() {
+                    if (half == 0 && i == 0) m = top();
+                    for (int again = half == 0 && i == 0;; ++again) {
                         const float ref = m == NEG ? 0.f : m;
                         const uint64_t nref = pt_pack(-ref * sl2, -ref * sl2);
                         uint64_t s2[2] = {0ull, 0ull};
 #pragma unroll
-                        for (int ch = 0; ch < 2; ++ch)
+                        for (int b = 0; b < 64; b += kPtBatch) {  // stage by stage: one pair's chain of latencies is 30 cycles
+                            float y[kPtBatch];
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float x0, x1;
-                                pt_unpack(pt_fma2(pt_pack(__uint_as_float(x[ch][e]), __uint_as_float(x[ch][e + 1])), sl2x2,
-                                                  nref),
-                                          x0, x1);
-                                const float p0 = pt_ex2(x0), p1 = pt_ex2(x1);
-                                s2[(e >> 1) & 1] = pt_add2(s2[(e >> 1) & 1], pt_pack(p0, p1));
-                                pk[ch][e >> 1] = pack_bf16x2(p0, p1);
+                            for (int e = 0; e < kPtBatch; e += 2)
+                                pt_unpack(pt_fma2(pt_pack(__uint_as_float(x[b >> 5][(b & 31) + e]),
+                                                          __uint_as_float(x[b >> 5][(b & 31) + e + 1])), sl2x2, nref),
+                                          y[e], y[e + 1]);
+#pragma unroll
+                            for (int e = 0; e < kPtBatch; ++e) y[e] = pt_ex2(y[e]);
+#pragma unroll
+                            for (int e = 0; e < kPtBatch; e += 2) {
+                                s2[(e >> 1) & 1] = pt_add2(s2[(e >> 1) & 1], pt_pack(y[e], y[e + 1]));
+                                pk[b >> 5][((b & 31) + e) >> 1] = pack_bf16x2(y[e], y[e + 1]);
                             }
+                        }
                         float la, lb, lc, ld;
                         pt_unpack(s2[0], la, lb);
                         pt_unpack(s2[1], lc, ld);
                         sum = (la + lb) + (lc + ld);
-                    };
-                    if (half == 0 && i == 0) m = top();
-                    exponentials();
-                    if (half == 1 || i > 0) {
+                        if (again || !__any_sync(0xffffffffu, !(sum <= kPtRise))) break;
+                        // The reference moves: the products so far are done, what they summed is scaled, and
+                        // these keys are exponentiated again.
+                        if (half == 1 ? !wait(pvhalf0 + 8 * grp, c & 1)
+                                      : P::kApart && !wait(pv0 + 8 * grp, (c - 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
                         const float now = fmaxf(m, top());
-                        if (__any_sync(0xffffffffu, (now - m) * sl2 > kPtRise)) {
-                            // The reference moves: the products so far are done, what they summed is
-                            // scaled, and this half is exponentiated again.
-                            if (half == 1 ? !wait(pvhalf0 + 8 * grp, c & 1)
-                                          : P::kApart && !wait(pv0 + 8 * grp, (c - 1) & 1)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            const float alpha = pt_ex2((m - (now == NEG ? 0.f : now)) * sl2);
-                            m = now;
-                            l *= alpha;
+                        const float alpha = pt_ex2((m - (now == NEG ? 0.f : now)) * sl2);
+                        m = now;
+                        l *= alpha;
 #pragma unroll 1
-                            for (int h = 0; h < D; h += 16) {
-                                uint32_t ov[16];
-                                tmem_ld16(tO + h, ov);
+                        for (int h = 0; h < D; h += 16) {
+                            uint32_t ov[16];
+                            tmem_ld16(tO + h, ov);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                                pt_st16(tO + h, ov);
-                            }
-                            exponentials();
+                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                            pt_st16(tO + h, ov);
                         }
                     }
+                    if (!ok) break;
                     l += sum;
                     // with P beside S, the product that read the last block's probabilities is done
                     if (P::kApart && half == 0 && c > 0) {
