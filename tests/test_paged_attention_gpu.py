@@ -81,8 +81,9 @@ def test_parity(new, held, H, Hkv, D, page, causal):
         out, lse = tll.paged_attention(q, cache, batch, causal=causal, max_new=max_new, with_lse=True)
         tll.default_context(0).check()
         check(out, lse, q, cache, batch, starts, held, causal, D ** -0.5)
-    again = tll.paged_attention(q, cache, batch, causal=causal, max_new=max_new)
-    assert torch.equal(again, out)
+    for _ in range(5):
+        again = tll.paged_attention(q, cache, batch, causal=causal, max_new=max_new)
+        assert torch.equal(again, out)
 
 
 @pytest.mark.parametrize("D", [64, 128])

@@ -1,10 +1,12 @@
 // Joins the parts of the items that the ends of the blocks' stretches cut (paged.cuh):
 //   m = max_i m_i,  w_i = 2^(m_i - m),  out = sum_i w_i O_i / sum_i w_i l_i
-// for each row, parts in the order of the blocks. Blocks (c, y) take the item that block c of
-// the attention kernel started and did not end, if there is one. With few parts a warp takes a
-// row; with many (a long context on few heads is cut into as many parts as there are blocks) the
-// block's eight warps share a row's parts, whose loads would otherwise stand one behind the other.
-// Bound by latency: the parts lie in the L2.
+// for each row, in an order that the parts' number fixes. Blocks (c, y) take the item that block c of the
+// attention kernel started and did not end, if there is one. A thread has four columns of a row; with
+// few parts (nearly always two) the block's threads have different rows, with many (a long context
+// on few heads is cut into as many parts as there are blocks) they share a row's parts.
+// Bound by latency: the parts lie in the L2, and everything that a thread reads is asked
+// for at once. (A warp per row with a loop over the parts took 19 us behind the 69 of
+// 4 x 512 tokens over 8704 keys, 12 heads of 64.)
 #include <math.h>
 
 #include "paged.cuh"
@@ -12,75 +14,107 @@
 namespace lin {
 namespace {
 
-constexpr int kPjWarps = 8;
+constexpr int kPjThreads = 256;
+constexpr int kPjFew = 4, kPjMany = 6;  // parts that a thread asks for at once
 
 template <int D>
-__global__ void __launch_bounds__(32 * kPjWarps) paged_join_kernel(const PagedArgs a, int R) {
-    constexpr int V = D / 32;  // columns of a lane
-    __shared__ float s_acc[kPjWarps][D];
-    __shared__ float s_total[kPjWarps];
+__global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const PagedArgs a, int R) {
+    constexpr int LANES = D / 4, SLOTS = kPjThreads / LANES;
+    __shared__ float4 s_acc[SLOTS][LANES];
+    __shared__ float2 s_stat[SLOTS];
     pdl_wait();
     pdl_launch_dependents();
     const int c = blockIdx.x;
     const PagedCut cut = a.cuts[c];
     if (cut.last <= c) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int col = threadIdx.x % LANES, slot = threadIdx.x / LANES;
     const int parts = cut.last - c + 1, rows = cut.tokens * a.G;
-    const bool share = parts > kPjWarps;
-    const int first = share ? warp : 0, step = share ? kPjWarps : 1;      // this warp's parts
-    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * R; };
-    const int r0 = share ? blockIdx.y : blockIdx.y * kPjWarps + warp, rstep = gridDim.y * (share ? 1 : kPjWarps);
-    for (int row = r0; row < rows; row += rstep) {
-        float m = -INFINITY;
-        for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.stats[slot(i) + row].x);
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float base = m == -INFINITY ? 0.f : m;
-        float acc[V] = {}, total = 0.f;
-#pragma unroll 8
-        for (int i = first; i < parts; i += step) {
-            const float2 s = a.stats[slot(i) + row];
-            const float w = exp2f(s.x - base);
-            const float* src = a.sums + (slot(i) + row) * D + lane * V;
-            float x[V];
-            if constexpr (V == 2) {
-                *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
-            } else {
-                *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
-            }
-            total = fmaf(s.y, w, total);
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] = fmaf(x[e], w, acc[e]);
-        }
-        if (share) {
-            __syncthreads();  // the row before has been read
-#pragma unroll
-            for (int e = 0; e < V; ++e) s_acc[warp][lane * V + e] = acc[e];
-            if (lane == 0) s_total[warp] = total;
-            __syncthreads();
-            if (warp > 0) continue;
-            total = 0.f;
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kPjWarps; ++w) {
-                total += s_total[w];
-#pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] += s_acc[w][lane * V + e];
-            }
-        }
-        const int tok = row / a.G, head = cut.h * a.G + row % a.G;
+    // part i of the item: block c started it, the others continue it
+    auto at = [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * R; };
+    auto store = [&](int row, float m, float total, float4 v) {
+        const int tok = row / a.G, head = cut.h * a.G + row - tok * a.G;
         const float inv = 1.f / total;
-        uint32_t y[V / 2];
+        const bool none = total == 0.f;  // a row without keys is 0
+        *reinterpret_cast<uint2*>(a.out + (size_t)(cut.row0 + tok) * a.ldo + (size_t)head * D + 4 * col) =
+            make_uint2(none ? 0u : pack_bf16x2(v.x * inv, v.y * inv), none ? 0u : pack_bf16x2(v.z * inv, v.w * inv));
+        if (a.lse && col == 0) a.lse[(size_t)(cut.row0 + tok) * (a.Hkv * a.G) + head] = row_lse(m, total);
+    };
+    auto add = [](float4& v, const float4& x, float w) {
+        v.x = fmaf(x.x, w, v.x);
+        v.y = fmaf(x.y, w, v.y);
+        v.z = fmaf(x.z, w, v.z);
+        v.w = fmaf(x.w, w, v.w);
+    };
+    const float4* sums = reinterpret_cast<const float4*>(a.sums) + col;
+    if (parts <= kPjFew) {
+        for (int row = blockIdx.y * SLOTS + slot; row < rows; row += gridDim.y * SLOTS) {
+            float2 st[kPjFew];
+            float4 x[kPjFew];
 #pragma unroll
-        for (int e = 0; e < V; e += 2)  // a row without keys is 0
-            y[e / 2] = total == 0.f ? 0u : pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-        uint16_t* dst = a.out + (size_t)(cut.row0 + tok) * a.ldo + (size_t)head * D + lane * V;
-        if constexpr (V == 2)
-            *reinterpret_cast<uint32_t*>(dst) = y[0];
-        else
-            *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
-        if (a.lse && lane == 0) a.lse[(size_t)(cut.row0 + tok) * (a.Hkv * a.G) + head] = row_lse(m, total);
+            for (int i = 0; i < kPjFew; ++i) {
+                st[i] = i < parts ? __ldg(a.stats + at(i) + row) : make_float2(-INFINITY, 0.f);
+                x[i] = i < parts ? __ldg(sums + (at(i) + row) * LANES) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float m = st[0].x, total = 0.f;
+#pragma unroll
+            for (int i = 1; i < kPjFew; ++i) m = fmaxf(m, st[i].x);
+            const float base = m == -INFINITY ? 0.f : m;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kPjFew; ++i) {
+                const float w = exp2f(st[i].x - base);
+                total = fmaf(st[i].y, w, total);
+                add(v, x[i], w);
+            }
+            store(row, m, total, v);
+        }
+        return;
+    }
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        float m = -INFINITY, total = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = slot; i0 < parts; i0 += SLOTS * kPjMany) {
+            float2 st[kPjMany];
+            float4 x[kPjMany];
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < kPjMany; ++k) {
+                const int i = i0 + k * SLOTS;
+                st[k] = i < parts ? __ldg(a.stats + at(i) + row) : make_float2(-INFINITY, 0.f);
+                x[k] = i < parts ? __ldg(sums + (at(i) + row) * LANES) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < kPjMany; ++k) top = fmaxf(top, st[k].x);
+            const float base = top == -INFINITY ? 0.f : top, old = exp2f(m - base);
+            total *= old;
+            v = make_float4(v.x * old, v.y * old, v.z * old, v.w * old);
+            m = top;
+#pragma unroll
+            for (int k = 0; k < kPjMany; ++k) {
+                const float w = exp2f(st[k].x - base);
+                total = fmaf(st[k].y, w, total);
+                add(v, x[k], w);
+            }
+        }
+        s_acc[slot][col] = v;
+        if (col == 0) s_stat[slot] = make_float2(m, total);
+        __syncthreads();
+        if (slot == 0) {
+            m = -INFINITY;
+            total = 0.f;
+            v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) m = fmaxf(m, s_stat[i].x);
+            const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) {
+                const float w = exp2f(s_stat[i].x - base);
+                total = fmaf(s_stat[i].y, w, total);
+                add(v, s_acc[i][col], w);
+            }
+            store(row, m, total, v);
+        }
+        __syncthreads();
     }
 }
 
@@ -92,8 +126,8 @@ int launch_paged_join(const PagedProblem& p, const PagedArgs& a, int grid, int R
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1, R > 32 ? R / 8 : 4);
-    cfg.blockDim = dim3(32 * kPjWarps);
+    cfg.gridDim = dim3(grid - 1, R > 32 ? 16 : 8);
+    cfg.blockDim = dim3(kPjThreads);
     cfg.stream = p.stream;
     cfg.attrs = &attr;
     cfg.numAttrs = p.early_start ? 1 : 0;

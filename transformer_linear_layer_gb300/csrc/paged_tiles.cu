@@ -41,8 +41,8 @@ constexpr int kPtLaunch = 168, kPtLow = 72, kPtHigh = 216;
 static_assert(128 * kPtLow + 256 * kPtHigh <= kPtThreads * kPtLaunch, "register split");
 constexpr uint32_t kPtTmem = 512;
 constexpr int kPtParts = 4;             // parts of items that are described at a time
-constexpr int kPtLead = 1;              // blocks that an item's start and end cost
-constexpr int kPtBatch = 16;             // exponentials in flight
+constexpr int kPtLead = 2;               // blocks that an item's start and end cost (2 x 4096 tokens, 16 heads of 128
+                                        // on 2: 179 us with 1, 150 with 2 and 3, 156 with 6; 4 x 512 over 8704: 71, 72, 76)
 constexpr float kPtRise = 65536.f;       // what 64 probabilities may add up to before their reference moves
 
 template <int D>
@@ -66,10 +66,9 @@ struct PtPart {       // a block's part of an item
     int slot;         // the workspace's slot, or -1: the item is whole
 };
 
-// volatile: in the order that they are written in
 __device__ __forceinline__ float pt_ex2(float x) {
     float y;
-    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ uint64_t pt_pack(float lo, float hi) {
@@ -451,7 +450,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 tmem_wait_ld(sv[0][1]);
                 tmem_ld32_async(tS + 64u, sv[1][0]);
                 tmem_ld32_async(tS + 96u, sv[1][1]);
-                if (k0 + kPtKeys > p.seen) {
+                if (__builtin_expect(k0 + kPtKeys > p.seen, 0)) {
                     // values of keys that nobody sees
                     const uint32_t v = g + 2 * (uint32_t)i + 1, vs = v % S;
                     if (!wait(full0 + 8 * vs, (v / S) & 1)) {
@@ -479,7 +478,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                         }
                     }
                     const int c0 = k0 + 64 * half;
-                    if (c0 + 64 > wmin) {
+                    if (__builtin_expect(c0 + 64 > wmin, 0)) {
 #pragma unroll
                         for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
@@ -498,34 +497,32 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     };
                     uint32_t pk[2][16];
                     float sum;
-                    if (half == 0 && i == 0) m = top();
-                    for (int again = half == 0 && i == 0;; ++again) {
+                    auto exponentials = [&]() {
                         const float ref = m == NEG ? 0.f : m;
                         const uint64_t nref = pt_pack(-ref * sl2, -ref * sl2);
                         uint64_t s2[2] = {0ull, 0ull};
 #pragma unroll
-                        for (int b = 0; b < 64; b += kPtBatch) {  // stage by stage: one pair's chain of latencies is 30 cycles
-                            float y[kPtBatch];
+                        for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
-                            for (int e = 0; e < kPtBatch; e += 2)
-                                pt_unpack(pt_fma2(pt_pack(__uint_as_float(x[b >> 5][(b & 31) + e]),
-                                                          __uint_as_float(x[b >> 5][(b & 31) + e + 1])), sl2x2, nref),
-                                          y[e], y[e + 1]);
-#pragma unroll
-                            for (int e = 0; e < kPtBatch; ++e) y[e] = pt_ex2(y[e]);
-#pragma unroll
-                            for (int e = 0; e < kPtBatch; e += 2) {
-                                s2[(e >> 1) & 1] = pt_add2(s2[(e >> 1) & 1], pt_pack(y[e], y[e + 1]));
-                                pk[b >> 5][((b & 31) + e) >> 1] = pack_bf16x2(y[e], y[e + 1]);
+                            for (int e = 0; e < 32; e += 2) {
+                                float x0, x1;
+                                pt_unpack(pt_fma2(pt_pack(__uint_as_float(x[ch][e]), __uint_as_float(x[ch][e + 1])), sl2x2,
+                                                  nref),
+                                          x0, x1);
+                                const float p0 = pt_ex2(x0), p1 = pt_ex2(x1);
+                                s2[(e >> 1) & 1] = pt_add2(s2[(e >> 1) & 1], pt_pack(p0, p1));
+                                pk[ch][e >> 1] = pack_bf16x2(p0, p1);
                             }
-                        }
-                        float la, lb, lc, ld;
-                        pt_unpack(s2[0], la, lb);
-                        pt_unpack(s2[1], lc, ld);
-                        sum = (la + lb) + (lc + ld);
-                        if (again || !__any_sync(0xffffffffu, !(sum <= kPtRise))) break;
+                        float la, lb;
+                        pt_unpack(pt_add2(s2[0], s2[1]), la, lb);
+                        sum = la + lb;
+                    };
+                    if (half == 0 && i == 0) m = top();
+                    exponentials();
+                    if (__builtin_expect((half == 1 || i > 0) && __any_sync(0xffffffffu, live && !(sum <= kPtRise)), 0)) {
                         // The reference moves: the products so far are done, what they summed is scaled, and
-                        // these keys are exponentiated again.
+                        // these keys are exponentiated again. (Rows that are none have no say: their q
+                        // is whatever the shared memory held, and results would not repeat.)
                         if (half == 1 ? !wait(pvhalf0 + 8 * grp, c & 1)
                                       : P::kApart && !wait(pv0 + 8 * grp, (c - 1) & 1)) {
                             ok = false;
@@ -544,8 +541,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                             for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
                             pt_st16(tO + h, ov);
                         }
+                        exponentials();
                     }
-                    if (!ok) break;
                     l += sum;
                     // with P beside S, the product that read the last block's probabilities is done
                     if (P::kApart && half == 0 && c > 0) {
