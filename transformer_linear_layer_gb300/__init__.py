@@ -876,19 +876,22 @@ class Rotary:
             raise LinError(rc, "lin_rotary_turns")
         signed = [t - (1 << 64) if t >> 63 else t for t in turns]
         self.turns = torch.tensor(signed[:n] or [0], dtype=torch.int64, device=device)
+        self.index = self.turns.get_device()
         self._plan = RotaryPlan(dim, ROTARY_INTERLEAVED if self.interleaved else ROTARY_HALF, self.scale,
                                 self.turns.data_ptr())
         self._ref = ctypes.byref(self._plan)
 
 
-def _check_heads(t, dtype, what):
-    """(rows, heads, width, row stride) of an N x H x D tensor whose rows hold their
-    heads one after the other, any distance apart."""
-    if not t.is_cuda or t.dim() != 3 or (dtype is not None and t.dtype != dtype):
+def _check_heads(t, dtype, what, index=None):
+    """(rows, heads, width, row stride) of an N x H x D tensor (of ``dtype``, on CUDA
+    device ``index``) whose rows hold their heads one after the other, any distance apart."""
+    if t.dim() != 3 or (dtype is not None and t.dtype != dtype) or not t.is_cuda:
         raise ValueError(f"{what} must be an N x heads x width CUDA tensor" + (f" of {dtype}" if dtype else ""))
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{what} must be on cuda:{index}, got {t.device}")
     N, H, D = t.shape
     s0, s1, s2 = t.stride()
-    if (D > 1 and s2 != 1) or (H > 1 and s1 != D):
+    if (s2 != 1 and D > 1) or (s1 != D and H > 1):
         raise ValueError(f"{what}: a row must hold its heads one after the other")
     ld = s0 if N > 1 else H * D
     if ld < H * D:
@@ -896,23 +899,30 @@ def _check_heads(t, dtype, what):
     return N, H, D, ld
 
 
+def _check_positions(t, N, index):
+    if t.shape != (N,) or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"positions must be a contiguous tensor of {N} on cuda:{index}, got {tuple(t.shape)} on {t.device}")
+    return _index_type(t, "positions")
+
+
 def _rotary(call, x, positions, rotary, out, ctx, stream):
     import torch
 
     N, H, D, ldx = _check_heads(x, None, "x")
+    index = x.get_device()
     kind = _float_type(x, "x")
-    ptype = _index_type(positions, "positions")
-    _check(positions, positions.dtype, (N,), "positions")
+    ptype = _check_positions(positions, N, index)
+    if rotary.index != index:
+        raise ValueError(f"the rotary plan must be on cuda:{index}, got cuda:{rotary.index}")
     if out is None:
-        out = torch.empty((N, H, D), dtype=x.dtype, device=x.device)
-    No, Ho, Do, ldy = _check_heads(out, x.dtype, "out")
-    if (No, Ho, Do) != (N, H, D):
-        raise ValueError(f"out must have shape {(N, H, D)}, got {tuple(out.shape)}")
-    _same_device(x, positions, out, rotary.turns)
-    dev = x.device.index if x.device.index is not None else 0
-    ctx = ctx or default_context(dev)
+        out, ldy = torch.empty((N, H, D), dtype=x.dtype, device=x.device), H * D
+    else:
+        No, Ho, Do, ldy = _check_heads(out, x.dtype, "out", index)
+        if (No, Ho, Do) != (N, H, D):
+            raise ValueError(f"out must have shape {(N, H, D)}, got {tuple(out.shape)}")
+    ctx = ctx or default_context(index)
     rc = getattr(library(), call)(ctx._h, N, H, D, x.data_ptr(), ldx, out.data_ptr(), ldy, kind,
-                                  positions.data_ptr(), ptype, rotary._ref, _stream_ptr(stream, dev))
+                                  positions.data_ptr(), ptype, rotary._ref, _stream_ptr(stream, index))
     if rc != OK:
         raise LinError(rc, call)
     return out
@@ -953,7 +963,8 @@ class KVCache:
         _same_device(k, v)
         self.k, self.v = k, v
         self.pages, self.heads, self.page_size, self.head_dim = k.shape
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
+        self._sizes: dict = {}  # workspace bytes by query heads and tokens
         self._plan = KVCachePlan(k.data_ptr(), v.data_ptr(), *(k.shape[i] for i in (0, 2, 1, 3)), *k.stride()[:3])
         self._ref = ctypes.byref(self._plan)
 
@@ -979,7 +990,7 @@ class KVBatch:
         _same_device(kv_len, q_start, block_table)
         self.q_start, self.kv_len, self.block_table = q_start, kv_len, block_table
         self.sequences = B
-        self.device = kv_len.device
+        self.device, self.index = kv_len.device, kv_len.get_device()
         self._plans: dict = {}
 
     def _ref(self, tokens: int):
@@ -1005,33 +1016,29 @@ def cache_append(q, k, v, cache: KVCache, batch: KVBatch, rotary: Rotary | None 
     Rows that belong to no sequence are left out."""
     import torch
 
-    D, dev = cache.head_dim, cache.device
-    N, Hk, Dk, ldk = _check_heads(k, torch.bfloat16, "k")
-    Nv, Hv, Dv, ldv = _check_heads(v, torch.bfloat16, "v")
+    D, index, bf16 = cache.head_dim, cache.index, torch.bfloat16
+    N, Hk, Dk, ldk = _check_heads(k, bf16, "k", index)
+    Nv, Hv, Dv, ldv = _check_heads(v, bf16, "v", index)
     if (Hk, Dk) != (cache.heads, D) or (Nv, Hv, Dv) != (N, Hk, Dk):
         raise ValueError(f"k and v must be tokens x {cache.heads} x {D}, got {tuple(k.shape)} and {tuple(v.shape)}")
+    if batch.index != index or (rotary is not None and rotary.index != index):
+        raise ValueError(f"the batch and the rotary plan must be on cuda:{index}, like the cache")
     H = ldq = ldo = 0
     if q is not None:
-        Nq, H, Dq, ldq = _check_heads(q, torch.bfloat16, "q")
+        Nq, H, Dq, ldq = _check_heads(q, bf16, "q", index)
         if (Nq, Dq) != (N, D):
             raise ValueError(f"q must be {N} x heads x {D}, got {tuple(q.shape)}")
         if rotary is None:
             raise ValueError("q is only rotated: without a rotary plan it must be None")
         if q_out is None:
-            q_out = torch.empty((N, H, D), dtype=torch.bfloat16, device=dev)
-        No, Ho, Do, ldo = _check_heads(q_out, torch.bfloat16, "q_out")
-        if (No, Ho, Do) != (N, H, D):
-            raise ValueError(f"q_out must have shape {(N, H, D)}, got {tuple(q_out.shape)}")
+            q_out, ldo = torch.empty((N, H, D), dtype=bf16, device=cache.device), H * D
+        else:
+            No, Ho, Do, ldo = _check_heads(q_out, bf16, "q_out", index)
+            if (No, Ho, Do) != (N, H, D):
+                raise ValueError(f"q_out must have shape {(N, H, D)}, got {tuple(q_out.shape)}")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    ptype = TYPE_INT64
-    if positions is not None:
-        ptype = _index_type(positions, "positions")
-        _check(positions, positions.dtype, (N,), "positions")
-    for t in (q, q_out, k, v, batch, positions, None if rotary is None else rotary.turns):
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
-    index = dev.index if dev.index is not None else 0
+    ptype = TYPE_INT64 if positions is None else _check_positions(positions, N, index)
     ctx = ctx or default_context(index)
     rc = library().lin_cache_append(ctx._h, cache._ref, batch._ref(N), H, _ptr(q), ldq, _ptr(q_out), ldo,
                                     k.data_ptr(), ldk, v.data_ptr(), ldv, _ptr(positions), ptype,
@@ -1056,31 +1063,42 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     :func:`paged_attention_workspace` bytes (default: from torch's allocator, for this call)."""
     import torch
 
-    N, H, D, ldq = _check_heads(q, torch.bfloat16, "q")
-    dev = cache.device
+    index = cache.index
+    N, H, D, ldq = _check_heads(q, torch.bfloat16, "q", index)
     if D != cache.head_dim:
         raise ValueError(f"q must be tokens x heads x {cache.head_dim}, got {tuple(q.shape)}")
+    if batch.index != index:
+        raise ValueError(f"the batch must be on cuda:{index}, like the cache")
     if out is None:
-        out = torch.empty((N, H, D), dtype=torch.bfloat16, device=dev)
-    No, Ho, Do, ldo = _check_heads(out, torch.bfloat16, "out")
-    if (No, Ho, Do) != (N, H, D):
-        raise ValueError(f"out must have shape {(N, H, D)}, got {tuple(out.shape)}")
+        out, ldo = torch.empty((N, H, D), dtype=torch.bfloat16, device=cache.device), H * D
+    else:
+        No, Ho, Do, ldo = _check_heads(out, torch.bfloat16, "out", index)
+        if (No, Ho, Do) != (N, H, D):
+            raise ValueError(f"out must have shape {(N, H, D)}, got {tuple(out.shape)}")
     if lse is None and with_lse:
-        lse = torch.empty((N, H), dtype=torch.float32, device=dev)
-    if lse is not None:
+        lse = torch.empty((N, H), dtype=torch.float32, device=cache.device)
+    elif lse is not None:
         _check(lse, torch.float32, (N, H), "lse")
-    for t in (q, out, lse, batch, workspace):
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
-    index = dev.index if dev.index is not None else 0
+        _same_device(q, lse)
     ctx = ctx or default_context(index)
     hint = 0 if max_new is None else int(max_new)
     raw = _stream_ptr(stream, index)
     if workspace is None:
-        workspace = _scratch(paged_attention_workspace(cache, batch, N, H, hint, ctx), dev, stream)
+        # (the size goes by the device too, and all contexts of a cache are on its own)
+        key = (H, hint, N if hint == 0 else 0, batch.sequences if hint == 0 else 0)
+        size = cache._sizes.get(key)
+        if size is None:
+            size = paged_attention_workspace(cache, batch, N, H, hint, ctx)
+            if len(cache._sizes) > 64:
+                cache._sizes.clear()
+            cache._sizes[key] = size
+        workspace = _scratch(cache.device, size, stream)
+    else:
+        _same_device(q, workspace)
+        size = workspace.numel() * workspace.element_size()
     rc = library().lin_paged_attention(ctx._h, cache._ref, batch._ref(N), H, q.data_ptr(), ldq, out.data_ptr(), ldo,
                                        _ptr(lse), int(bool(causal)), 0.0 if scale is None else float(scale), hint,
-                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
+                                       workspace.data_ptr(), size, raw)
     if rc != OK:
         raise LinError(rc, "lin_paged_attention")
     return (out, lse) if lse is not None else out
@@ -1089,7 +1107,7 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
 def paged_attention_workspace(cache: KVCache, batch: KVBatch, tokens: int, heads: int, max_new: int = 0,
                               ctx: Context | None = None) -> int:
     """Bytes of workspace that :func:`paged_attention` needs for such a call."""
-    ctx = ctx or default_context(cache.device.index or 0)
+    ctx = ctx or default_context(cache.index)
     size = ctypes.c_size_t()
     rc = library().lin_paged_attention_workspace(ctx._h, cache._ref, batch._ref(tokens), heads, max_new,
                                                  ctypes.byref(size))
@@ -1098,7 +1116,7 @@ def paged_attention_workspace(cache: KVCache, batch: KVBatch, tokens: int, heads
     return size.value
 
 
-def _scratch(size, device, stream):
+def _scratch(device, size, stream):
     """Bytes from torch's allocator for one call's kernels, taken on the stream that they
     run on (the memory may still be in use by earlier work of any other)."""
     import torch
