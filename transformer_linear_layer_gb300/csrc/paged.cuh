@@ -24,9 +24,10 @@
 
 namespace lin {
 
-// The sequence that row n belongs to: the last b with q_start[b] <= n, or -1. By one
-// warp, 32 entries a step. q_start[0 .. B) is read and nothing else, whatever it holds.
-__device__ __forceinline__ int find_sequence(const int* q_start, int B, int n) {
+// The sequence that row n belongs to: the last b with q_start[b] <= n, or -1, with
+// end = q_start[b + 1] and kv = kv_len[b]. By one warp, 32 entries a step. Nothing but the entries is
+// read, whatever they hold.
+__device__ __forceinline__ int find_sequence(const int* q_start, const int* kv_len, int B, int n, int& end, int& kv) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = B;
     while (hi - lo > 32) {
@@ -36,7 +37,11 @@ __device__ __forceinline__ int find_sequence(const int* q_start, int B, int n) {
         lo += (c - 1) * step;
         hi = hi < lo + step ? hi : lo + step;
     }
-    const int c = __popc(__ballot_sync(0xffffffffu, lo + lane < hi && q_start[lo + lane] <= n));
+    const bool in = lo + lane < hi;
+    const int from = in ? q_start[lo + lane] : 0, to = in ? q_start[lo + lane + 1] : 0, held = in ? kv_len[lo + lane] : 0;
+    const int c = __popc(__ballot_sync(0xffffffffu, in && from <= n));
+    end = __shfl_sync(0xffffffffu, to, c > 0 ? c - 1 : 0);
+    kv = __shfl_sync(0xffffffffu, held, c > 0 ? c - 1 : 0);
     return c == 0 ? -1 : lo + c - 1;
 }
 

@@ -12,12 +12,16 @@
 // position 10^6). The nearest quarter turn is taken off in integers and
 // sincospif sees at most an eighth of a turn.
 //
-// Memory bounds both: each element is read and written once. A block of 256
-// threads takes a few rows (their cosines and sines are computed once for all
-// heads, into shared memory) and moves 16-byte units: with neighbours paired a unit
-// holds its pairs, with halves paired a thread moves two units, rot/2 apart. The
-// first units are asked for before the angles are computed. Element by element where
-// sizes, strides or addresses do not allow 16 bytes.
+// Memory bounds both: each element is read and written once. A thread has one place in a head (16
+// bytes of pairs; with halves paired two times 16, rot/2 apart) and up to K heads of a row, which
+// it asks for at once before the angles are computed; the cosines and sines of a block's rows are computed once,
+// into shared memory, and read once a thread. v's heads are places of the same kind that do not turn.
+// Element by element where sizes, strides or addresses do not allow 16 bytes. bf16 moves two to a word
+// (with single elements converted and stored the kernel was bound by its instructions, 13 us for the
+// first of the sizes below).
+// Measured (GB300): 8192 x 24 heads of 64, bf16, halves 7.9 us (6.4 TB/s); 2331 x 10 heads of 128, fp32,
+// half of each head, neighbours 3.9 us (6.2 TB/s); one row 1.4 us; append of 5757 rows of 32 + 16
+// heads of 128 25.7 us (5.5 TB/s), of 64 rows of 12 + 24 heads of 64 2.7 us.
 #include <limits.h>
 #include <math.h>
 
@@ -30,15 +34,18 @@ namespace lin {
 namespace {
 
 constexpr int kRtThreads = 256;
-constexpr int kRtMaxRows = 8;       // rows a block takes
+constexpr int kRtHeads = 4;         // heads a thread asks for at once
+constexpr int kRtMaxRows = 8;       // rows a block takes, a warp each for where they go
 
 struct RotaryArgs {
     RotaryProblem p;
+    int heads;                      // of a row: q, k and v
+    int turning;                    // q and k: those that turn
+    int rot_units, units;           // places of a head that rotate, all
+    int span;                       // places that a block takes (gridDim.z spans)
+    int each;                       // head groups of a row: a thread has heads g, g + each, ...
+    int chunk;                      // head groups that a block takes (gridDim.y chunks)
     int rows;                       // rows a block takes
-    int rot_units, units;           // of a rotated head: units that rotate, all
-    int copy_units;                 // of a head that is only copied (v)
-    int row_units;                  // of a row
-    int chunk;                      // units of a row that a block takes (gridDim.y chunks)
 };
 
 // cos and sin of p turns (turns in units of 2^-64 of a turn per position).
@@ -53,30 +60,55 @@ __device__ __forceinline__ void turn(long long p, unsigned long long turns, floa
     s = q >= 2 ? -sa : sa;
 }
 
-template <class T>
-__device__ __forceinline__ float to_f(T v);
-template <>
-__device__ __forceinline__ float to_f(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f(uint16_t v) { return bf16_bits_to_f32(v); }
-template <class T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ float from_f(float v) { return v; }
-template <>
-__device__ __forceinline__ uint16_t from_f(float v) { return f32_to_bf16_bits(v); }
+// The pairs of a place turned, 16 bytes of each of x0 and x1 (halves paired) or of x0 alone: bf16
+// two to a word, unpacked by shifts and rounded two at a time.
+template <class T, bool INTER>
+__device__ __forceinline__ void turn_words(uint32_t (&x0)[4], uint32_t (&x1)[4], const float* c, const float* s) {
+    auto pair = [&](float& a, float& b, int e) {
+        const float xa = a, xb = b;
+        a = fmaf(xa, c[e], -(xb * s[e]));
+        b = fmaf(xa, s[e], xb * c[e]);
+    };
+    if constexpr (sizeof(T) == 4 && !INTER) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            float a = __uint_as_float(x0[w]), b = __uint_as_float(x1[w]);
+            pair(a, b, w);
+            x0[w] = __float_as_uint(a);
+            x1[w] = __float_as_uint(b);
+        }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int w = 0; w < 4; w += 2) {
+            float a = __uint_as_float(x0[w]), b = __uint_as_float(x0[w + 1]);
+            pair(a, b, w / 2);
+            x0[w] = __float_as_uint(a);
+            x0[w + 1] = __float_as_uint(b);
+        }
+    } else if constexpr (!INTER) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            float a0 = __uint_as_float(x0[w] << 16), a1 = __uint_as_float(x0[w] & 0xffff0000u);
+            float b0 = __uint_as_float(x1[w] << 16), b1 = __uint_as_float(x1[w] & 0xffff0000u);
+            pair(a0, b0, 2 * w);
+            pair(a1, b1, 2 * w + 1);
+            x0[w] = pack_bf16x2(a0, a1);
+            x1[w] = pack_bf16x2(b0, b1);
+        }
+    } else {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            float a = __uint_as_float(x0[w] << 16), b = __uint_as_float(x0[w] & 0xffff0000u);
+            pair(a, b, w);
+            x0[w] = pack_bf16x2(a, b);
+        }
+    }
+}
 
-// A unit: V elements that move as one access.
-template <class T, int V>
-struct alignas(V * sizeof(T)) Unit {
-    T e[V];
-};
-
-// V elements a thread's access holds; INTER: neighbours are paired.
-template <class T, int V, bool INTER>
+// V elements a thread's access holds; INTER: neighbours are paired; K heads a thread.
+template <class T, int V, bool INTER, int K, bool APPEND>
 __global__ void __launch_bounds__(kRtThreads) rotary_kernel(const RotaryArgs a) {
-    using U = Unit<T, V>;
-    extern __shared__ float s_turn[];  // cos then sin: rows x rot/2 each
+    extern __shared__ __align__(16) float s_turn[];  // cos then sin: rows x rot/2 each
     __shared__ long long s_dst[kRtMaxRows];   // append: the row's place in its page, < 0 for none
     __shared__ long long s_pos[kRtMaxRows];
     __shared__ int s_live[kRtMaxRows];
@@ -84,83 +116,92 @@ __global__ void __launch_bounds__(kRtThreads) rotary_kernel(const RotaryArgs a) 
     const int half = p.rot >> 1;
     const long long row0 = (long long)blockIdx.x * a.rows;
     const int rows = (int)(p.N - row0 < a.rows ? p.N - row0 : a.rows);
-    const int u0 = blockIdx.y * a.chunk;
-    const int chunk = a.row_units - u0 < a.chunk ? a.row_units - u0 : a.chunk;
-    const int total = rows * chunk;
-    const int q_units = p.part[0].heads * a.units, k_units = p.part[1].heads * a.units;
+    const int g0 = blockIdx.y * a.chunk, chunk = min(a.chunk, a.each - g0);
+
+    // This thread's row, head group and place.
+    const int per_row = chunk * a.span;
+    const int row = (unsigned)threadIdx.x / (unsigned)per_row, rest = threadIdx.x - row * per_row;
+    const int in_row = (unsigned)rest / (unsigned)a.span;
+    const int group = g0 + in_row, place = blockIdx.z * a.span + rest - in_row * a.span;
+    const bool mine = row < rows && place < a.units, rot = place < a.rot_units;
+    // its first element: past the rotated ones for the rest of the head; a scalar pair of neighbours starts at 2 place
+    const int first = (V == 1 && INTER && rot) ? 2 * place : (rot ? place : place + p.rot / V - a.rot_units) * V;
+    // The second access of a rotating place: rot/2 further, or the neighbour.
+    constexpr bool TWO = !INTER || V == 1;
+    const int apart = INTER ? 1 : half;
 
     pdl_wait();
     pdl_launch_dependents();
 
-    // Where unit i of the block's lies: part, head, element, and whether it rotates.
-    struct Place {
-        const T* src;
-        int part, head, u, row;
-        bool rot;
+    uint32_t x0[K][4], x1[K][4];  // V == 1: the element's bits in the first
+    auto load = [&](const T* src, uint32_t (&x)[4]) {
+        if constexpr (V == 1) {
+            if constexpr (sizeof(T) == 2)
+                x[0] = (uint32_t)*reinterpret_cast<const uint16_t*>(src) << 16;
+            else
+                x[0] = *reinterpret_cast<const uint32_t*>(src);
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(src);
+            x[0] = v.x;
+            x[1] = v.y;
+            x[2] = v.z;
+            x[3] = v.w;
+        }
     };
-    auto place = [&](int i) {
-        Place w;
-        w.row = (unsigned)i / (unsigned)chunk;
-        int r = u0 + (i - w.row * chunk);
-        w.part = r < q_units ? 0 : r < q_units + k_units ? 1 : 2;
-        if (w.part > 0) r -= q_units;
-        if (w.part > 1) r -= k_units;
-        const int per = w.part == 2 ? a.copy_units : a.units;
-        w.head = (unsigned)r / (unsigned)per;
-        w.u = r - w.head * per;
-        w.rot = w.part != 2 && w.u < a.rot_units;
-        if (w.part != 2 && !w.rot) w.u += p.rot / V - a.rot_units;  // past the rotated elements
-        // unit u starts at element u V, but a scalar pair of neighbours at 2u
-        const int e = (V == 1 && INTER && w.rot) ? 2 * w.u : w.u * V;
-        w.src = static_cast<const T*>(p.part[w.part].src) + (row0 + w.row) * p.part[w.part].ld_src +
-                (long long)w.head * p.D + e;
-        return w;
+    // (a scalar that is only copied keeps its bits: a bf16 is its fp32's upper half)
+    auto store = [&](T* dst, const uint32_t (&x)[4], bool turned) {
+        if constexpr (V == 1) {
+            if constexpr (sizeof(T) == 2)
+                *reinterpret_cast<uint16_t*>(dst) =
+                    turned ? f32_to_bf16_bits(__uint_as_float(x[0])) : (uint16_t)(x[0] >> 16);
+            else
+                *reinterpret_cast<uint32_t*>(dst) = x[0];
+        } else {
+            *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+        }
     };
-    // The second access of a rotating unit: rot/2 further, or the neighbour.
-    constexpr bool TWO = !INTER || V == 1;
-    const int apart = INTER ? 1 : half;
-
-    U x0, x1;
-    Place w;
-    if (threadIdx.x < total) {
-        w = place(threadIdx.x);
-        x0 = *reinterpret_cast<const U*>(w.src);
-        if (TWO && w.rot) x1 = *reinterpret_cast<const U*>(w.src + apart);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int h = group + k * a.each;
+        if (mine && h < a.heads) {
+            const int part = !APPEND || h < p.part[0].heads ? 0 : h < a.turning ? 1 : 2;
+            const int in = h - (part == 0 ? 0 : part == 1 ? p.part[0].heads : a.turning);
+            const T* src = static_cast<const T*>(p.part[part].src) + (row0 + row) * p.part[part].ld_src + (in * p.D + first);
+            load(src, x0[k]);
+            if (TWO && rot) load(src + apart, x1[k]);
+        }
     }
 
     // Positions, and the places in the cache.
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (p.append) {
-        if (warp < rows) {
-            const int n = (int)(row0 + warp);
-            const int b = find_sequence(p.batch.q_start, p.batch.sequences, n);
+    if constexpr (APPEND) {
+        for (int r = warp; r < rows; r += blockDim.x >> 5) {
+            const int n = (int)(row0 + r);
+            int end, kv;
+            const int b = find_sequence(p.batch.q_start, p.batch.kv_len, p.batch.sequences, n, end, kv);
             if (lane == 0) {
                 long long pos = -1, dst = -1;
-                int live = 0;
-                if (b >= 0) {
-                    const int end = p.batch.q_start[b + 1];
-                    if (n < end) {
-                        live = 1;
-                        pos = (long long)p.batch.kv_len[b] - end + n;
-                        const long long slots = (long long)p.batch.table_pages * p.cache.page_size;
-                        if (pos >= 0 && pos < slots) {
-                            const int page = p.batch.block_table[b * p.batch.table_stride + pos / p.cache.page_size];
-                            if (page >= 0 && page < p.cache.pages)
-                                dst = page * p.cache.page_stride + pos % p.cache.page_size * p.cache.token_stride;
-                        }
+                const bool live = b >= 0 && n < end;
+                if (live) {
+                    pos = (long long)kv - end + n;
+                    const int shift = 31 - __clz(p.cache.page_size);  // a power of two
+                    if (pos >= 0 && pos < (long long)p.batch.table_pages << shift) {
+                        const int page = p.batch.block_table[b * p.batch.table_stride + (pos >> shift)];
+                        if (page >= 0 && page < p.cache.pages)
+                            dst = page * p.cache.page_stride + (pos & (p.cache.page_size - 1)) * p.cache.token_stride;
                     }
                 }
-                s_live[warp] = live;
-                s_dst[warp] = dst;
-                s_pos[warp] = pos;
+                s_live[r] = live;
+                s_dst[r] = dst;
+                s_pos[r] = pos;
             }
         }
         __syncthreads();
     }
-    for (int i = threadIdx.x; i < rows * half; i += kRtThreads) {
+    for (int i = threadIdx.x; i < rows * half; i += blockDim.x) {
         const int r = (unsigned)i / (unsigned)half, f = i - r * half;
         long long pos;
-        if (p.positions)
+        if (!APPEND || p.positions)
             pos = p.wide ? static_cast<const long long*>(p.positions)[row0 + r]
                          : (long long)static_cast<const int*>(p.positions)[row0 + r];
         else
@@ -171,85 +212,82 @@ __global__ void __launch_bounds__(kRtThreads) rotary_kernel(const RotaryArgs a) 
         s_turn[rows * half + i] = s * p.scale;
     }
     __syncthreads();
+    if (!mine) return;
 
-    for (int i = threadIdx.x; i < total;) {
-        T* dst = nullptr;
-        if (!p.append) {
-            dst = static_cast<T*>(p.part[0].dst) + (row0 + w.row) * p.part[0].ld_dst;
-        } else if (w.part == 0) {
-            if (s_live[w.row]) dst = static_cast<T*>(p.part[0].dst) + (row0 + w.row) * p.part[0].ld_dst;
-        } else if (s_dst[w.row] >= 0) {
-            dst = static_cast<T*>(w.part == 1 ? p.cache.k : p.cache.v) + s_dst[w.row];
-        }
-        if (dst) {
-            dst += w.part == 0 ? (long long)w.head * p.D : w.head * p.cache.head_stride;
-            dst += (V == 1 && INTER && w.rot) ? 2 * w.u : w.u * V;
-            if (w.rot) {
-                const float* cs = s_turn + w.row * half;
-                const float* sn = cs + rows * half;
-                if constexpr (TWO) {
+    constexpr int P = TWO ? V : V / 2;  // pairs of a place
+    alignas(16) float c[P], s[P];
+    if (rot) {
+        const float* cs = s_turn + row * half + place * P;
+        const float* sn = cs + rows * half;
+        if constexpr (P % 4 == 0) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const float c = cs[w.u * V + e], s = sn[w.u * V + e];
-                        const float xa = to_f(x0.e[e]), xb = to_f(x1.e[e]);
-                        x0.e[e] = from_f<T>(fmaf(xa, c, -(xb * s)));
-                        x1.e[e] = from_f<T>(fmaf(xa, s, xb * c));
-                    }
-                    *reinterpret_cast<U*>(dst + apart) = x1;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < V; e += 2) {
-                        const float c = cs[(w.u * V + e) >> 1], s = sn[(w.u * V + e) >> 1];
-                        const float xa = to_f(x0.e[e]), xb = to_f(x0.e[e + 1]);
-                        x0.e[e] = from_f<T>(fmaf(xa, c, -(xb * s)));
-                        x0.e[e + 1] = from_f<T>(fmaf(xa, s, xb * c));
-                    }
-                }
+            for (int e = 0; e < P; e += 4) {
+                *reinterpret_cast<float4*>(c + e) = *reinterpret_cast<const float4*>(cs + e);
+                *reinterpret_cast<float4*>(s + e) = *reinterpret_cast<const float4*>(sn + e);
             }
-            *reinterpret_cast<U*>(dst) = x0;
+        } else {
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                c[e] = cs[e];
+                s[e] = sn[e];
+            }
         }
-        i += kRtThreads;
-        if (i < total) {
-            w = place(i);
-            x0 = *reinterpret_cast<const U*>(w.src);
-            if (TWO && w.rot) x1 = *reinterpret_cast<const U*>(w.src + apart);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int h = group + k * a.each;
+        if (h >= a.heads) break;
+        T* dst;
+        if (!APPEND || h < p.part[0].heads) {
+            if (APPEND && !s_live[row]) continue;
+            dst = static_cast<T*>(p.part[0].dst) + (row0 + row) * p.part[0].ld_dst + h * p.D;
+        } else {
+            if (s_dst[row] < 0) continue;
+            dst = h < a.turning ? static_cast<T*>(p.cache.k) + (h - p.part[0].heads) * p.cache.head_stride
+                                : static_cast<T*>(p.cache.v) + (h - a.turning) * p.cache.head_stride;
+            dst += s_dst[row];
         }
+        dst += first;
+        const bool turned = rot && (!APPEND || h < a.turning);
+        if (turned) {
+            if constexpr (V == 1) {
+                const float xa = __uint_as_float(x0[k][0]), xb = __uint_as_float(x1[k][0]);
+                x0[k][0] = __float_as_uint(fmaf(xa, c[0], -(xb * s[0])));
+                x1[k][0] = __float_as_uint(fmaf(xa, s[0], xb * c[0]));
+            } else {
+                turn_words<T, INTER>(x0[k], x1[k], c, s);
+            }
+        }
+        store(dst, x0[k], turned);
+        if (TWO && rot) store(dst + apart, x1[k], turned);
     }
 }
 
-template <class T, int V, bool INTER>
+template <class T, int V, bool INTER, int K>
 int start(const RotaryProblem& p) {
     RotaryArgs a;
     a.p = p;
     const int pair = p.rot / 2;
+    a.turning = p.part[0].heads + p.part[1].heads;
+    a.heads = a.turning + p.part[2].heads;
     a.rot_units = INTER ? (V == 1 ? pair : p.rot / V) : pair / V;
     // in place the rest of the head stays where it is
     const bool rest = p.append || p.part[0].src != p.part[0].dst;
     a.units = a.rot_units + (rest ? (p.D - p.rot) / V : 0);
-    a.copy_units = p.D / V;
-    const long long row_units =
-        (long long)(p.part[0].heads + p.part[1].heads) * a.units + (long long)p.part[2].heads * a.copy_units;
-    if (row_units == 0) return LIN_OK;
-    if (row_units > INT_MAX / kRtMaxRows) return LIN_ERR_UNSUPPORTED;
-    a.row_units = (int)row_units;
-    // Rows enough for three accesses a thread, but blocks enough for two an SM;
-    // few rows: their units are spread over blocks of one access a thread.
-    long long rows = 3 * kRtThreads / row_units;
-    if (rows > p.N / (2 * p.sm_count)) rows = p.N / (2 * p.sm_count);
+    if (a.heads == 0 || a.units == 0) return LIN_OK;
+    a.each = (a.heads + K - 1) / K;
+    a.span = a.units < kRtThreads ? a.units : kRtThreads;
+    a.chunk = a.each < kRtThreads / a.span ? a.each : kRtThreads / a.span;
+    const int per_row = a.chunk * a.span;
+    long long rows = kRtThreads / per_row;
     if (rows > kRtMaxRows) rows = kRtMaxRows;
-    if (rows < 1) rows = 1;
+    if (rows > p.N) rows = p.N;
     a.rows = (int)rows;
-    long long chunks = 1;
-    if (p.N < 2 * p.sm_count) {
-        chunks = (row_units + kRtThreads - 1) / kRtThreads;
-        if (chunks > 64) chunks = 64;
-    }
-    a.chunk = (int)((row_units + chunks - 1) / chunks);
-    chunks = (row_units + a.chunk - 1) / a.chunk;
-    const long long grid = (p.N + rows - 1) / rows;
+    const int chunks = (a.each + a.chunk - 1) / a.chunk;
+    if (chunks > 65535) return LIN_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)chunks);
-    cfg.blockDim = dim3(kRtThreads);
+    cfg.gridDim = dim3((unsigned)((p.N + rows - 1) / rows), (unsigned)chunks, (unsigned)((a.units + a.span - 1) / a.span));
+    cfg.blockDim = dim3((unsigned)((rows * per_row + 31) / 32 * 32));
     cfg.dynamicSmemBytes = (size_t)rows * pair * 2 * sizeof(float);
     cfg.stream = p.stream;
     cudaLaunchAttribute attr;
@@ -257,7 +295,13 @@ int start(const RotaryProblem& p) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = p.early_start ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, rotary_kernel<T, V, INTER>, a) != cudaSuccess) return LIN_ERR_CUDA;
+    cudaError_t e;
+    if constexpr (sizeof(T) == 2)
+        e = p.append ? cudaLaunchKernelEx(&cfg, rotary_kernel<T, V, INTER, K, true>, a)
+                     : cudaLaunchKernelEx(&cfg, rotary_kernel<T, V, INTER, K, false>, a);
+    else
+        e = cudaLaunchKernelEx(&cfg, rotary_kernel<T, V, INTER, K, false>, a);
+    if (e != cudaSuccess) return LIN_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? LIN_OK : LIN_ERR_CUDA;
 }
 
@@ -269,7 +313,11 @@ int start_width(const RotaryProblem& p) {
     for (const RotaryPart& part : p.part)
         if (part.heads > 0) wide = wide && fits(part.src, part.ld_src) && fits(part.dst, part.ld_dst);
     // the cache's own addresses and strides are multiples of 16 bytes
-    return wide ? start<T, V, INTER>(p) : start<T, 1, INTER>(p);
+    if (!wide) return start<T, 1, INTER, 1>(p);
+    // Few rows: one head a thread, so that the row is done by as many threads as it has (64 rows of
+    // 12 + 24 heads of 64: 2.7 us; with four 3.0). Many: accesses in flight count (5757 rows of 48 heads of 128: 37.6 us
+    // with one head a thread, 35.5 with two, 25.7 with four).
+    return p.N < 4 * p.sm_count ? start<T, V, INTER, 1>(p) : start<T, V, INTER, kRtHeads>(p);
 }
 
 }  // namespace
