@@ -27,6 +27,8 @@
 // Every wait is bounded (about 1 s); a block that gives up sets the status word.
 #include <math.h>
 
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace lin {
@@ -436,12 +438,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             const int lim = a.causal && live ? min(p.pos0 + grp * each + tok + 1, sh.seen) : sh.seen;
             const int wmin = __reduce_min_sync(0xffffffffu, lim);
             float m = NEG, l = 0.f;  // the reference of the exponents (raw score), the total
-            for (int i = 0; i < sh.n; ++i, ++c) {
+            // One block; MASKED: some of the warp's rows do not see all of its keys. Two copies of the
+            // code, so that the one that nearly always runs is short and straight.
+            auto block = [&](int i, auto masked) {
                 const int k0 = (p.j0 + i) * kPtKeys;
-                if (!wait(sfull0 + 8 * grp, c & 1)) {
-                    ok = false;
-                    break;
-                }
+                if (!wait(sfull0 + 8 * grp, c & 1)) return false;
                 tc_fence_after();
                 uint32_t sv[2][2][32];
                 tmem_ld32_async(tS, sv[0][0]);
@@ -450,13 +451,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 tmem_wait_ld(sv[0][1]);
                 tmem_ld32_async(tS + 64u, sv[1][0]);
                 tmem_ld32_async(tS + 96u, sv[1][1]);
-                if (__builtin_expect(k0 + kPtKeys > p.seen, 0)) {
+                if (decltype(masked)::value && k0 + kPtKeys > p.seen) {
                     // values of keys that nobody sees
                     const uint32_t v = g + 2 * (uint32_t)i + 1, vs = v % S;
-                    if (!wait(full0 + 8 * vs, (v / S) & 1)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!wait(full0 + 8 * vs, (v / S) & 1)) return false;
                     if (k0 + row >= p.seen) {
                         uint8_t* dst = ring + vs * P::kTile + row * 128;
 #pragma unroll
@@ -478,7 +476,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                         }
                     }
                     const int c0 = k0 + 64 * half;
-                    if (__builtin_expect(c0 + 64 > wmin, 0)) {
+                    if constexpr (decltype(masked)::value) {
 #pragma unroll
                         for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
@@ -524,10 +522,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                         // these keys are exponentiated again. (Rows that are none have no say: their q
                         // is whatever the shared memory held, and results would not repeat.)
                         if (half == 1 ? !wait(pvhalf0 + 8 * grp, c & 1)
-                                      : P::kApart && !wait(pv0 + 8 * grp, (c - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
+                                      : P::kApart && !wait(pv0 + 8 * grp, (c - 1) & 1)) return false;
                         tc_fence_after();
                         const float now = fmaxf(m, top());
                         const float alpha = pt_ex2((m - (now == NEG ? 0.f : now)) * sl2);
@@ -546,10 +541,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     l += sum;
                     // with P beside S, the product that read the last block's probabilities is done
                     if (P::kApart && half == 0 && c > 0) {
-                        if (!wait(pv0 + 8 * grp, (c - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
+                        if (!wait(pv0 + 8 * grp, (c - 1) & 1)) return false;
                         tc_fence_after();
                     }
                     pt_st16(tP + 32u * half, pk[0]);
@@ -559,8 +551,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     __syncwarp();
                     if (lane == 0) mbar_arrive(probs0 + 16 * grp + 8 * half);
                 }
-                if (!ok) break;
-            }
+                return true;
+            };
+            for (int i = 0; ok && i < sh.n; ++i, ++c)
+                ok = (p.j0 + i + 1) * kPtKeys > wmin ? block(i, std::true_type()) : block(i, std::false_type());
             if (!ok) break;
             if (sh.tokens > 0) {
                 if (sh.n > 0) {
