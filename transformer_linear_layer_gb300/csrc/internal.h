@@ -287,12 +287,15 @@ struct PagedProblem {
     int sm_count = 0;
     bool early_start = false;      // programmatic launch (nothing is read before the dependency wait)
 };
-// kPagedRowsMax rows (tokens of a sequence with the query heads of a key head) and fewer go
-// to paged_rows.cu, more to paged_tiles.cu, whose tiles hold at least kPagedGroupMax query heads.
-constexpr int kPagedRowsMax = 32, kPagedGroupMax = 128;
-size_t paged_rows_workspace(int sm_count, int rows, int D);
+// Up to kPagedRowsMax rows (the longest sequence's new tokens with the query heads of a key head) go
+// to paged_rows.cu, more to paged_tiles.cu, whose tiles hold up to kPagedGroupMax query heads of a key
+// head. Measured on both (us): 64 sequences of up to 8000 keys, 32 heads of 128 on 8: 8 rows 164 and
+// 173, 16 rows 170 and 174, 20 rows (two tiles of the first) 304 and 175; 8 sequences of 2000 keys, 12
+// heads of 64: 1 row 16.6 and 23.8, 16 rows 16.8 and 23.2, 20 rows 25.0 and 23.2.
+constexpr int kPagedRowsMax = 16, kPagedGroupMax = 128;
+size_t paged_rows_workspace(int sm_count, int D);
 size_t paged_tiles_workspace(int sm_count, int D);
-int launch_paged_rows(const PagedProblem& p, int rows);
+int launch_paged_rows(const PagedProblem& p);
 int launch_paged_tiles(const PagedProblem& p);
 
 // Kernel timelines (timeline build only, see timeline.cuh): copy up to `bytes`

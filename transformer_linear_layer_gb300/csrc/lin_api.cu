@@ -1504,7 +1504,7 @@ int paged_rows(const lin_kv_cache& cache, const lin_kv_batch* batch, int H, int 
 }
 
 size_t paged_bytes(const lin_ctx& ctx, const lin_kv_cache& cache, int rows) {
-    return rows <= lin::kPagedRowsMax ? lin::paged_rows_workspace(ctx.sm_count, rows, cache.head_dim)
+    return rows <= lin::kPagedRowsMax ? lin::paged_rows_workspace(ctx.sm_count, cache.head_dim)
                                       : lin::paged_tiles_workspace(ctx.sm_count, cache.head_dim);
 }
 
@@ -1582,7 +1582,7 @@ int lin_paged_attention(lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_ba
         hull = Range{lo, (size_t)(hi - lo)};
     }
     note_output(p.stream, hull);
-    return launched(rows <= kPagedRowsMax ? launch_paged_rows(p, rows) : launch_paged_tiles(p), p.stream, hull);
+    return launched(rows <= kPagedRowsMax ? launch_paged_rows(p) : launch_paged_tiles(p), p.stream, hull);
 }
 
 int lin_check_device(lin_ctx* ctx, void* stream) {

@@ -126,7 +126,7 @@ int launch_paged_join(const PagedProblem& p, const PagedArgs& a, int grid, int R
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1, R > 32 ? 16 : 8);
+    cfg.gridDim = dim3(grid - 1, R > kPagedRowsMax ? 16 : 8);
     cfg.blockDim = dim3(kPjThreads);
     cfg.stream = p.stream;
     cfg.attrs = &attr;

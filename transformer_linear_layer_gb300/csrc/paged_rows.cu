@@ -1,5 +1,5 @@
 // Attention of few new tokens (single ones, short drafts) over a paged cache: tiles of
-// up to 16 or 32 rows (token, query head of one key head).
+// up to 16 rows (token, query head of one key head).
 //
 //   s_rj = (q_r . k_j) scale,  out_r = sum_j exp(s_rj - m) v_j / sum_j exp(s_rj - m)
 //
@@ -28,13 +28,13 @@ constexpr int kPrWarps = 4;                        // consumer warps
 constexpr int kPrThreads = 32 * (kPrWarps + 1);    // and the producer
 constexpr int kPrKeys = 16 * kPrWarps;             // keys of a unit
 
-template <int D, int MT>
+constexpr int kPrRows = kPagedRowsMax;             // rows of a tile
+static_assert(kPrRows == 16, "the products' M");
+
+template <int D>
 struct PrShape {
-    static constexpr int R = 16 * MT;
-    static constexpr uint32_t kK = kPrKeys * D * 2, kQ = R * D * 2, kStage = 2 * kK + kQ;
-    // the sums of 32 rows of 128 leave registers for one block an SM
-    static constexpr int kPerSm = R * D > 32 * 64 ? 1 : 2;
-    static constexpr int kRoom = (int)((222 / kPerSm * 1024) / kStage), S = kRoom < 6 ? kRoom : 6;
+    static constexpr uint32_t kK = kPrKeys * D * 2, kQ = kPrRows * D * 2, kStage = 2 * kK + kQ;
+    static constexpr int kRoom = 111 * 1024 / (int)kStage, S = kRoom < 6 ? kRoom : 6;  // two blocks an SM
     static constexpr size_t kSmem = 1024 + S * kStage;
 };
 
@@ -72,12 +72,12 @@ __device__ __forceinline__ float pr_ex2(float x) {
     return y;
 }
 
-template <int D, int MT>
-__global__ void __launch_bounds__(kPrThreads, PrShape<D, MT>::kPerSm)
+template <int D>
+__global__ void __launch_bounds__(kPrThreads, 2)
 paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const PagedArgs a) {
-    using P = PrShape<D, MT>;
-    constexpr int R = P::R, S = P::S, HALVES = D / 64;
+    using P = PrShape<D>;
+    constexpr int R = kPrRows, S = P::S, HALVES = D / 64;
     extern __shared__ uint8_t raw[];
     __shared__ alignas(8) uint64_t bars[2 * S + 1];
     __shared__ PrUnit units[S];
@@ -166,9 +166,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
 
     // ---- consumers: warp w has keys 16 w .. 16 w + 15 of each unit ----
-    float m[MT][2], l[MT][2], o[MT][D / 8][4];
-    uint32_t qf[MT][D / 16][4];
-    int lim[MT][2];        // keys that this lane's rows see
+    float m[2], l[2], o[D / 8][4];
+    uint32_t qf[D / 16][4];
+    int lim[2];            // keys that this lane's rows see
     uint32_t joins = 0, items = 0;
     bool ok = true;
     const int r8 = lane & 7;
@@ -189,26 +189,23 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         uint8_t* stage = smem + s * P::kStage;
         const uint32_t sk = smem_u32(stage), sv = sk + P::kK, sq = sk + 2 * P::kK;
         if (u.first) {
+            const int row = ((lane >> 3) & 1) * 8 + r8;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const int row = 16 * mt + ((lane >> 3) & 1) * 8 + r8;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const int chunk = (2 * kk + (lane >> 4)) & 7;
-                    ldsm4(sq + (kk >> 2) * (R * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), qf[mt][kk]);
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    m[mt][e] = -INFINITY;
-                    l[mt][e] = 0.f;
-                    const int tok = (16 * mt + (lane >> 2) + 8 * e) / a.G;
-                    lim[mt][e] = a.causal ? min(u.pos0 + tok + 1, u.seen) : u.seen;
-                }
-#pragma unroll
-                for (int d = 0; d < D / 8; ++d)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[mt][d][e] = 0.f;
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const int chunk = (2 * kk + (lane >> 4)) & 7;
+                ldsm4(sq + (kk >> 2) * (R * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), qf[kk]);
             }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[e] = -INFINITY;
+                l[e] = 0.f;
+                const int tok = ((lane >> 2) + 8 * e) / a.G;
+                lim[e] = a.causal ? min(u.pos0 + tok + 1, u.seen) : u.seen;
+            }
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
         }
         const int k0 = u.key0 + 16 * warp;
         bool zeroed = false;
@@ -225,72 +222,60 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 zeroed = true;
                 __syncwarp();
             }
-            float sc[MT][2][4] = {};
+            float sc[2][4] = {};
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 uint32_t kf[4];
                 const int key = 16 * warp + (lane >> 4) * 8 + r8, chunk = (2 * kk + ((lane >> 3) & 1)) & 7;
                 ldsm4(sk + (kk >> 2) * (kPrKeys * 128) + key * 128 + ((chunk ^ r8) << 4), kf);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    mma16816(sc[mt][0], qf[mt][kk], kf[0], kf[1]);
-                    mma16816(sc[mt][1], qf[mt][kk], kf[2], kf[3]);
-                }
+                mma16816(sc[0], qf[kk], kf[0], kf[1]);
+                mma16816(sc[1], qf[kk], kf[2], kf[3]);
             }
-            uint32_t pf[MT][4];
+            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                float mx[2] = {-INFINITY, -INFINITY};
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = k0 + nt * 8 + 2 * (lane & 3) + (e & 1);
+                    float& x = sc[nt][e];
+                    x = key < lim[e >> 1] ? x * a.scale_log2 : -INFINITY;
+                    mx[e >> 1] = fmaxf(mx[e >> 1], x);
+                }
+            float alpha[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                const float now = fmaxf(m[e], mx[e]);
+                const float base = now == -INFINITY ? 0.f : now;
+                alpha[e] = pr_ex2(m[e] - base);
+                m[e] = now;
+                float sum = 0.f;
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = k0 + nt * 8 + 2 * (lane & 3) + (e & 1);
-                        float& x = sc[mt][nt][e];
-                        x = key < lim[mt][e >> 1] ? x * a.scale_log2 : -INFINITY;
-                        mx[e >> 1] = fmaxf(mx[e >> 1], x);
+                    for (int f = 0; f < 2; ++f) {
+                        float& x = sc[nt][2 * e + f];
+                        x = pr_ex2(x - base);
+                        sum += x;
                     }
-                float alpha[2];
+                l[e] = fmaf(l[e], alpha[e], sum);
+            }
+            const uint32_t pf[4] = {pack_bf16x2(sc[0][0], sc[0][1]), pack_bf16x2(sc[0][2], sc[0][3]),
+                                    pack_bf16x2(sc[1][0], sc[1][1]), pack_bf16x2(sc[1][2], sc[1][3])};
+            if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-                    const float now = fmaxf(m[mt][e], mx[e]);
-                    const float base = now == -INFINITY ? 0.f : now;
-                    alpha[e] = pr_ex2(m[mt][e] - base);
-                    m[mt][e] = now;
-                    float sum = 0.f;
+                for (int d = 0; d < D / 8; ++d)
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            float& x = sc[mt][nt][2 * e + f];
-                            x = pr_ex2(x - base);
-                            sum += x;
-                        }
-                    l[mt][e] = fmaf(l[mt][e], alpha[e], sum);
-                }
-                pf[mt][0] = pack_bf16x2(sc[mt][0][0], sc[mt][0][1]);
-                pf[mt][1] = pack_bf16x2(sc[mt][0][2], sc[mt][0][3]);
-                pf[mt][2] = pack_bf16x2(sc[mt][1][0], sc[mt][1][1]);
-                pf[mt][3] = pack_bf16x2(sc[mt][1][2], sc[mt][1][3]);
-                if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-                    for (int d = 0; d < D / 8; ++d)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[mt][d][e] *= alpha[e >> 1];
-                }
+                    for (int e = 0; e < 4; ++e) o[d][e] *= alpha[e >> 1];
             }
 #pragma unroll
             for (int dd = 0; dd < D / 16; ++dd) {
                 uint32_t vf[4];
                 const int key = 16 * warp + ((lane >> 3) & 1) * 8 + r8, chunk = (2 * dd + (lane >> 4)) & 7;
                 ldsm4_t(sv + (dd >> 2) * (kPrKeys * 128) + key * 128 + ((chunk ^ r8) << 4), vf);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    mma16816(o[mt][2 * dd], pf[mt], vf[0], vf[1]);
-                    mma16816(o[mt][2 * dd + 1], pf[mt], vf[2], vf[3]);
-                }
+                mma16816(o[2 * dd], pf, vf[0], vf[1]);
+                mma16816(o[2 * dd + 1], pf, vf[2], vf[3]);
             }
         }
         if (u.last) {
@@ -298,74 +283,64 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             float2(&stat)[kPrWarps][R] = s_stat[items & 1];
             ++items;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float sum = l[mt][e];
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    if ((lane & 3) == 0) stat[warp][16 * mt + (lane >> 2) + 8 * e] = make_float2(m[mt][e], sum);
-                }
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[e];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if ((lane & 3) == 0) stat[warp][(lane >> 2) + 8 * e] = make_float2(m[e], sum);
+            }
             if (!all_warps()) {  // the stage's keys and values have been read, too
                 ok = false;
                 break;
             }
             float* part = reinterpret_cast<float*>(stage);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                if (mt > 0 && !all_warps()) {
-                    ok = false;
-                    break;
+            for (int e = 0; e < 2; ++e) {
+                const int row = (lane >> 2) + 8 * e;
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kPrWarps; ++w) top = fmaxf(top, stat[w][row].x);
+                const float f = pr_ex2(m[e] - (top == -INFINITY ? 0.f : top));
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d)  // groups of 8 columns swizzled by the row: no two lanes on a bank
+                    *reinterpret_cast<float2*>(part + (warp * 16 + row) * D + ((d ^ (row & 7)) << 3) + 2 * (lane & 3)) =
+                        make_float2(o[d][2 * e] * f, o[d][2 * e + 1] * f);
+            }
+            if (!all_warps()) {
+                ok = false;
+                break;
+            }
+            for (int i = threadIdx.x; i < 16 * D / 4; i += 32 * kPrWarps) {
+                const int row = i / (D / 4), col = 4 * (i % (D / 4));
+                if (row >= u.tokens * a.G) break;
+                float top = -INFINITY, total = 0.f;
+#pragma unroll
+                for (int w = 0; w < kPrWarps; ++w) top = fmaxf(top, stat[w][row].x);
+                const float base = top == -INFINITY ? 0.f : top;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kPrWarps; ++w) {
+                    const float2 st = stat[w][row];
+                    total = fmaf(st.y, pr_ex2(st.x - base), total);
+                    const float4 x = *reinterpret_cast<const float4*>(
+                        part + (w * 16 + row) * D + (((col >> 3) ^ (row & 7)) << 3) + (col & 7));
+                    v.x += x.x;
+                    v.y += x.y;
+                    v.z += x.z;
+                    v.w += x.w;
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int row = (lane >> 2) + 8 * e;
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < kPrWarps; ++w) top = fmaxf(top, stat[w][16 * mt + row].x);
-                    const float f = pr_ex2(m[mt][e] - (top == -INFINITY ? 0.f : top));
-#pragma unroll
-                    for (int d = 0; d < D / 8; ++d)  // groups of 8 columns swizzled by the row: no two lanes on a bank
-                        *reinterpret_cast<float2*>(part + (warp * 16 + row) * D + ((d ^ (row & 7)) << 3) + 2 * (lane & 3)) =
-                            make_float2(o[mt][d][2 * e] * f, o[mt][d][2 * e + 1] * f);
-                }
-                if (!all_warps()) {
-                    ok = false;
-                    break;
-                }
-                for (int i = threadIdx.x; i < 16 * D / 4; i += 32 * kPrWarps) {
-                    const int row = i / (D / 4), col = 4 * (i % (D / 4)), at = 16 * mt + row;
-                    if (at >= u.tokens * a.G) break;
-                    float top = -INFINITY, total = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kPrWarps; ++w) top = fmaxf(top, stat[w][at].x);
-                    const float base = top == -INFINITY ? 0.f : top;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int w = 0; w < kPrWarps; ++w) {
-                        const float2 st = stat[w][at];
-                        total = fmaf(st.y, pr_ex2(st.x - base), total);
-                        const float4 x = *reinterpret_cast<const float4*>(
-                            part + (w * 16 + row) * D + (((col >> 3) ^ (row & 7)) << 3) + (col & 7));
-                        v.x += x.x;
-                        v.y += x.y;
-                        v.z += x.z;
-                        v.w += x.w;
-                    }
-                    if (u.slot < 0) {
-                        const float inv = total == 0.f ? 0.f : 1.f / total;
-                        const int tok = at / a.G, head = u.h * a.G + at % a.G;
-                        *reinterpret_cast<uint2*>(a.out + (size_t)(u.row0 + tok) * a.ldo + (size_t)head * D + col) =
-                            make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
-                        if (a.lse && col == 0)
-                            a.lse[(size_t)(u.row0 + tok) * (a.Hkv * a.G) + head] = row_lse(top, total);
-                    } else {
-                        *reinterpret_cast<float4*>(a.sums + ((size_t)u.slot * R + at) * D + col) = v;
-                        if (col == 0) a.stats[(size_t)u.slot * R + at] = make_float2(top, total);
-                    }
+                if (u.slot < 0) {
+                    const bool none = total == 0.f;  // a row without keys is 0
+                    const float inv = 1.f / total;
+                    const int tok = row / a.G, head = u.h * a.G + row - tok * a.G;
+                    *reinterpret_cast<uint2*>(a.out + (size_t)(u.row0 + tok) * a.ldo + (size_t)head * D + col) =
+                        make_uint2(none ? 0u : pack_bf16x2(v.x * inv, v.y * inv), none ? 0u : pack_bf16x2(v.z * inv, v.w * inv));
+                    if (a.lse && col == 0) a.lse[(size_t)(u.row0 + tok) * (a.Hkv * a.G) + head] = row_lse(top, total);
+                } else {
+                    *reinterpret_cast<float4*>(a.sums + ((size_t)u.slot * R + row) * D + col) = v;
+                    if (col == 0) a.stats[(size_t)u.slot * R + row] = make_float2(top, total);
                 }
             }
-            if (!ok) break;
             zeroed = true;
         }
         if (zeroed) fence_proxy_async_smem();  // written here, then by the next copy
@@ -379,18 +354,18 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     if (!ok && lane == 0) give_up();
 }
 
-template <int D, int MT>
+template <int D>
 int start(const PagedProblem& p) {
-    using P = PrShape<D, MT>;
-    constexpr int R = P::R;
-    const int grid = P::kPerSm * p.sm_count;
+    using P = PrShape<D>;
+    constexpr int R = kPrRows;
+    const int grid = 2 * p.sm_count;
     PagedArgs a;
     if (!paged_args(p, grid, R, &a)) return LIN_ERR_WORKSPACE;
     CUtensorMap tq, tk, tv;
     if (!paged_q_map(&tq, p, a.TQ) || !paged_kv_map(&tk, p, p.cache.k, kPrKeys) || !paged_kv_map(&tv, p, p.cache.v, kPrKeys))
         return LIN_ERR_CUDA;
     static std::atomic<unsigned long long> attr_set{0};
-    if (ensure_smem_attr(attr_set, paged_rows_kernel<D, MT>, P::kSmem) != LIN_OK) return LIN_ERR_CUDA;
+    if (ensure_smem_attr(attr_set, paged_rows_kernel<D>, P::kSmem) != LIN_OK) return LIN_ERR_CUDA;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -401,14 +376,9 @@ int start(const PagedProblem& p) {
     cfg.stream = p.stream;
     cfg.attrs = &attr;
     cfg.numAttrs = p.early_start ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, paged_rows_kernel<D, MT>, tq, tk, tv, a) != cudaSuccess) return LIN_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, paged_rows_kernel<D>, tq, tk, tv, a) != cudaSuccess) return LIN_ERR_CUDA;
     if (cudaGetLastError() != cudaSuccess) return LIN_ERR_CUDA;
     return launch_paged_join(p, a, grid, R);
-}
-
-template <int D, int MT>
-size_t workspace(int sm_count) {
-    return paged_workspace(PrShape<D, MT>::kPerSm * sm_count, PrShape<D, MT>::R, D);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -482,14 +452,8 @@ bool paged_args(const PagedProblem& p, int grid, int R, PagedArgs* a) {
     return true;
 }
 
-size_t paged_rows_workspace(int sm_count, int rows, int D) {
-    if (D == 64) return rows <= 16 ? workspace<64, 1>(sm_count) : workspace<64, 2>(sm_count);
-    return rows <= 16 ? workspace<128, 1>(sm_count) : workspace<128, 2>(sm_count);
-}
+size_t paged_rows_workspace(int sm_count, int D) { return paged_workspace(2 * sm_count, kPrRows, D); }
 
-int launch_paged_rows(const PagedProblem& p, int rows) {
-    if (p.cache.head_dim == 64) return rows <= 16 ? start<64, 1>(p) : start<64, 2>(p);
-    return rows <= 16 ? start<128, 1>(p) : start<128, 2>(p);
-}
+int launch_paged_rows(const PagedProblem& p) { return p.cache.head_dim == 64 ? start<64>(p) : start<128>(p); }
 
 }  // namespace lin
