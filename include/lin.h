@@ -646,7 +646,7 @@ typedef struct {
     const int* q_start;       /* sequences + 1: sequence b's new tokens are rows q_start[b] to q_start[b + 1] - 1; ascending */
     const int* kv_len;        /* sequences: tokens that sequence b has in the cache, the new ones included */
     const int* block_table;   /* sequence b's tokens i * page_size .. lie in page block_table[b * table_stride + i] */
-    int table_pages;          /* entries of a sequence that may be read */
+    int table_pages;          /* entries of a sequence that may be read: at most 2^30 / page_size */
     long long table_stride;   /* >= table_pages */
 } lin_kv_batch;
 
@@ -662,8 +662,8 @@ typedef struct {
  *   positions: NULL, or one per row (LIN_TYPE_INT32 or LIN_TYPE_INT64), used for the rotation only.
  * Rows of no sequence are left out: nothing is written for them. A token whose
  * position lies outside the table, or whose table entry is not a page of the cache, is not
- * stored (its q_out is written). Two tokens with the same place: one of them
- * is stored. q_start has to ascend; whatever the arrays hold, nothing outside the
+ * stored (its q_out is written). Two tokens with the same place: what lies there
+ * afterwards is a mixture of both (16 bytes of the one or the other). q_start has to ascend; whatever the arrays hold, nothing outside the
  * operands is read or written. Columns of one matrix (a qkv
  * projection's output) are fine as q, k, v and q_out; nothing else may overlap an output. */
 LIN_API int lin_cache_append(lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_batch* batch, int H, const void* q,
@@ -685,7 +685,7 @@ LIN_API int lin_cache_append(lin_ctx* ctx, const lin_kv_cache* cache, const lin_
  * operands is read or written.
  *   q, out : tokens x H heads of head_dim, bf16, 16-byte aligned, rows ldq and ldo apart (multiples of 8).
  *   H      : a multiple of cache->heads, at most 128 times as many.
- *   scale  : > 0; 0 selects 1/sqrt(head_dim).
+ *   scale  : 2^-100 to 2^100; 0 selects 1/sqrt(head_dim).
  *   max_new: about how many new tokens the longest sequence has (0: as many as the average); it picks the
  *            kernel, and any value gives right results.
  *   workspace: DEVICE, 16-byte aligned, of lin_paged_attention_workspace's size for the same max_new: parts of

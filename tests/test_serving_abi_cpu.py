@@ -122,12 +122,12 @@ CACHES = [
     (tll.ERR_ALIGN, dict(hs=1028, ps=2060)), (tll.ERR_ALIGN, dict(ps=2052)), (tll.ERR_UNSUPPORTED, dict(page_size=12)),
     (tll.ERR_UNSUPPORTED, dict(page_size=4)), (tll.ERR_UNSUPPORTED, dict(page_size=8192)),
     (tll.ERR_UNSUPPORTED, dict(head_dim=96)), (tll.ERR_UNSUPPORTED, dict(heads=1 << 20)),
-    (tll.ERR_UNSUPPORTED, dict(ps=1 << 45))]
+    (tll.ERR_UNSUPPORTED, dict(ps=1 << 45)), (tll.ERR_UNSUPPORTED, dict(pages=2, ps=1 << 40))]
 BATCHES = [
     (tll.ERR_ARG, dict(sequences=-1)), (tll.ERR_ARG, dict(tokens=-1)), (tll.ERR_ARG, dict(q_start=None)),
     (tll.ERR_ARG, dict(kv_len=None)), (tll.ERR_ARG, dict(table=None)), (tll.ERR_ARG, dict(table_pages=-1)),
     (tll.ERR_ARG, dict(stride=8)), (tll.ERR_ALIGN, dict(q_start=at(12) + 2)), (tll.ERR_ALIGN, dict(kv_len=at(13) + 2)),
-    (tll.ERR_ALIGN, dict(table=at(14) + 2)), (tll.ERR_UNSUPPORTED, dict(table_pages=1 << 28, stride=1 << 28)),
+    (tll.ERR_ALIGN, dict(table=at(14) + 2)), (tll.ERR_UNSUPPORTED, dict(table_pages=(1 << 26) + 1, stride=1 << 27)),
     (tll.ERR_UNSUPPORTED, dict(stride=1 << 40))]
 
 
@@ -161,7 +161,8 @@ def test_append_arguments(ctx, status, bad):
 @pytest.mark.parametrize("status,bad", [
     (tll.ERR_ARG, {"H": -1}), (tll.ERR_ARG, {"H": 3}), (tll.ERR_ARG, {"q": None}), (tll.ERR_ARG, {"out": None}),
     (tll.ERR_ARG, {"ldq": 248}), (tll.ERR_ARG, {"ldo": 248}), (tll.ERR_ARG, {"causal": 2}), (tll.ERR_ARG, {"scale": -1.0}),
-    (tll.ERR_ARG, {"scale": float("nan")}), (tll.ERR_ARG, {"scale": float("inf")}), (tll.ERR_ARG, {"max_new": -1}),
+    (tll.ERR_ARG, {"scale": float("nan")}), (tll.ERR_ARG, {"scale": float("inf")}), (tll.ERR_ARG, {"scale": 1e-35}), (tll.ERR_ARG, {"scale": 1e35}),
+    (tll.ERR_ARG, {"max_new": -1}),
     (tll.ERR_ARG, {"out": at(0)}), (tll.ERR_ARG, {"out": at(10)}), (tll.ERR_ARG, {"out": at(11) + 64}),
     (tll.ERR_ARG, {"out": at(12)}), (tll.ERR_ARG, {"out": at(14)}), (tll.ERR_ARG, {"lse": at(1)}),
     (tll.ERR_ARG, {"lse": at(0) + 4}), (tll.ERR_ARG, {"lse": at(13)}), (tll.ERR_ARG, {"ws": at(0)}),

@@ -1311,8 +1311,10 @@ int rotary_ok(const lin_rotary* r, int D) {
     return (uintptr_t)r->turns % 8 != 0 ? LIN_ERR_ALIGN : LIN_OK;
 }
 
-// Largest row stride that is taken, and extent of a cache (elements).
+// Largest row stride that is taken, extent of a cache (elements).
 constexpr long long kMaxStride = 1ll << 30, kMaxCache = 1ll << 46;
+// A tensor map's strides are below 2^40 bytes.
+constexpr long long kMaxCacheStride = 1ll << 38;
 
 int rotary_run(lin_ctx* ctx, int N, int H, int D, const void* x, long long ldx, void* y, long long ldy, int type,
                const void* positions, int positions_type, const lin_rotary* rotary, bool inverse, void* stream) {
@@ -1391,7 +1393,7 @@ int cache_ok(const lin_kv_cache* c, const lin_kv_batch* b) {
         return LIN_ERR_ARG;
     if ((c->page_size & (c->page_size - 1)) != 0 || c->page_size < 8 || c->page_size > 4096 ||
         (c->head_dim != 64 && c->head_dim != 128) || c->heads > 65535 || b->table_stride > kMaxStride ||
-        (long long)b->table_pages * c->page_size > INT_MAX)
+        (long long)b->table_pages * c->page_size > (1 << 30))
         return LIN_ERR_UNSUPPORTED;
     if (b->tokens > 0 && b->sequences > 0 && (!b->q_start || !b->kv_len || (b->table_pages > 0 && !b->block_table)))
         return LIN_ERR_ARG;
@@ -1401,7 +1403,7 @@ int cache_ok(const lin_kv_cache* c, const lin_kv_batch* b) {
     const int counts[] = {c->pages, c->heads, c->page_size};
     for (int i = 0; i < 3; ++i) {
         if (strides[i] < 0) return LIN_ERR_ARG;
-        if (strides[i] > kMaxCache / counts[i]) return LIN_ERR_UNSUPPORTED;
+        if (strides[i] > kMaxCacheStride || strides[i] > kMaxCache / counts[i]) return LIN_ERR_UNSUPPORTED;
     }
     if (!cache_rows_apart(*c)) return LIN_ERR_ARG;
     if (((uintptr_t)c->k | (uintptr_t)c->v) % 16 != 0 || c->token_stride % 8 != 0 ||
@@ -1537,6 +1539,8 @@ int lin_paged_attention(lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_ba
     if ((ok = paged_heads_ok(cache, H, max_new)) != LIN_OK) return ok;
     const long long N = batch->tokens, width = (long long)H * cache->head_dim;
     if (!q || !out || ldq < width || ldo < width) return LIN_ERR_ARG;
+    // scaled scores and their differences are fp32
+    if (scale > 0.f && !(scale >= 0x1p-100f && scale <= 0x1p100f)) return LIN_ERR_ARG;
     if (ldq > kMaxStride || ldo > kMaxStride || batch->sequences > (1 << 24)) return LIN_ERR_UNSUPPORTED;
     if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) % 16 != 0 || ldq % 8 != 0 || ldo % 8 != 0 ||
         (uintptr_t)lse % 4 != 0)

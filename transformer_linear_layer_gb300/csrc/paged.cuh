@@ -80,7 +80,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
     PagedSeq q;
     q.row0 = min(max(s, 0), a.batch.tokens);
     q.n = max(min(e, a.batch.tokens) - q.row0, 0);
-    const int room = a.batch.table_pages * a.page_size;  // at most INT_MAX
+    const int room = a.batch.table_pages * a.page_size;  // at most 2^30
     q.held = min(max(kv, 0), room);
     const long long pos = (long long)kv - e + q.row0;
     q.pos0 = (int)max(min(pos, (1ll << 30) + (1ll << 29)), -(1ll << 30));
