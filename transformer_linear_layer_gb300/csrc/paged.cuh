@@ -274,14 +274,17 @@ struct PagedBox {
         at = lane & ((KEYS >> shift) - 1);
         group = lane >> (top - shift);
     }
-    // The page of this lane's box, pages (outside the map: zeros) where the table names none; -1 when no key
-    // of the box is seen.
-    __device__ __forceinline__ int page(const PagedArgs& a, const int* table, int key0, int seen) const {
+    // The table's entry for this lane's box, 0 when no key of the box is seen. Not looked at here: it
+    // is asked for a block ahead, and the first use of a load waits for it.
+    __device__ __forceinline__ int entry(const PagedArgs& a, const int* table, int key0, int seen) const {
         const int key = key0 + (at << shift);
-        if (key >= seen) return -1;
-        const int g = table[key >> a.page_shift];
-        return g < 0 || g > a.pages ? a.pages : g;
+        return key < seen ? table[key >> a.page_shift] : 0;
     }
+    // Its page: `pages` (outside the map: zeros) where the table names none.
+    __device__ __forceinline__ static int page(const PagedArgs& a, int entry) {
+        return entry < 0 || entry > a.pages ? a.pages : entry;
+    }
+    __device__ __forceinline__ bool holds(int key0, int seen) const { return key0 + (at << shift) < seen; }
     __device__ __forceinline__ int slot(const PagedArgs& a, int key0) const {
         return (key0 + (at << shift)) & (a.page_size - 1);
     }

@@ -127,10 +127,10 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 const int slot = k == w.n ? -1 : 2 * (int)blockIdx.x + (j0 == 0 ? 1 : 0);
                 if (j0 == 0 && k < w.n) cut = {row0, tokens, w.h, w.last_block(r.per)};
                 const int* table = a.batch.block_table + w.b * a.batch.table_stride;
-                int key0 = j0 * kPrKeys, next = isv < 2 ? box.page(a, table, key0, seen) : -1;
+                int key0 = j0 * kPrKeys, next = box.entry(a, table, key0, seen);
                 for (int i = 0; i < k; ++i, key0 += kPrKeys) {
-                    const int page = next;
-                    if (i + 1 < k && isv < 2) next = box.page(a, table, key0 + kPrKeys, seen);  // ahead: it takes the L2's latency
+                    const int entry = next;
+                    if (i + 1 < k) next = box.entry(a, table, key0 + kPrKeys, seen);
                     if (!__all_sync(0xffffffffu, !aborted() && mbar_wait(empty0 + 8 * s, ph))) {
                         ok = false;
                         break;
@@ -142,9 +142,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                                        (uint32_t)(box.count(key0, seen) * HALVES * 2) * (128u << box.shift) + (i == 0 ? q_bytes : 0));
                     }
                     __syncwarp();
-                    if (page >= 0 && isv < 2)
+                    if (isv < 2 && box.holds(key0, seen))
                         tma_load_4d(smem_u32(stage + isv * P::kK + half * (kPrKeys * 128) + ((box.at << box.shift) * 128)),
-                                    isv ? &tmV : &tmK, full0 + 8 * s, 64 * half, box.slot(a, key0), w.h, page);
+                                    isv ? &tmV : &tmK, full0 + 8 * s, 64 * half, box.slot(a, key0), w.h, box.page(a, entry));
                     if (i == 0 && lane < HALVES)
                         tma_load_3d(smem_u32(stage + 2 * P::kK + lane * (R * 128)), &tmQ, full0 + 8 * s, 64 * lane,
                                     w.h * a.G, row0);

@@ -234,7 +234,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             p.n = k;
             p.slot = k == w.n ? -1 : 2 * (int)blockIdx.x + (j0 == 0 ? 1 : 0);
             const int* table = a.batch.block_table + w.b * a.batch.table_stride;
-            int key0 = j0 * kPtKeys, next = mine ? box.page(a, table, key0, p.seen) : -1;
+            int key0 = j0 * kPtKeys, next = box.entry(a, table, key0, p.seen);
             if (keys) {
                 if (j0 == 0 && k < w.n) cut = {p.row0, p.tokens, p.h, w.last_block(r.per)};
                 const uint32_t ps = np % kPtParts;
@@ -249,8 +249,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 ++np;
             }
             for (int i = 0; i < k; ++i, key0 += kPtKeys) {
-                const int page = next;
-                if (i + 1 < k && mine) next = box.page(a, table, key0 + kPtKeys, p.seen);  // ahead: it takes the L2's latency
+                const int entry = next;
+                if (i + 1 < k) next = box.entry(a, table, key0 + kPtKeys, p.seen);
                 if (!wait(empty0 + 8 * st, ph)) {
                     ok = false;
                     break;
@@ -258,9 +258,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 if (lane == 0)
                     mbar_expect_tx(full0 + 8 * st, (uint32_t)(box.count(key0, p.seen) * HALVES) * (128u << box.shift));
                 __syncwarp();
-                if (page >= 0)
+                if (mine && box.holds(key0, p.seen))
                     tma_load_4d(to + st * P::kTile, keys ? &tmK : &tmV, full0 + 8 * st, 64 * box.group, box.slot(a, key0),
-                                p.h, page);
+                                p.h, box.page(a, entry));
                 ++issued;
                 if ((st += 2) >= S) {
                     st -= S;
