@@ -239,3 +239,29 @@ def test_workspaces_and_streams():
     small = tll.Context(0, 1 << 17)
     assert tll.library().lin_paged_attention(small.handle, cache._ref, batch._ref(N), 4, q.data_ptr(), 256,
                                              out.data_ptr(), 256, None, 1, 0.0, 0, None, 0, None) == tll.ERR_WORKSPACE
+
+
+def test_the_default_streams_workspace_is_its_own():
+    """Calls on the default stream share the cache's workspace, growing with what they need; calls on another
+    stream at the same time do not touch it."""
+    new, held = [1] * 6, [700 + 90 * i for i in range(6)]
+    cache, batch, starts, N = make(new, held, 2, 128, 16, "heads")
+    fill(cache, batch, held)
+    q = queries(N, 16, 128)
+    hints = (1, 100, 1, 100)
+    want = [tll.paged_attention(q, cache, batch, max_new=h).clone() for h in hints]
+    small = cache._workspace.numel()
+    assert small >= tll.paged_attention_workspace(cache, batch, N, 16, 100)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = {0: [], 1: []}
+    for _ in range(30):
+        for h in hints:
+            got[0].append(tll.paged_attention(q, cache, batch, max_new=h))
+            with torch.cuda.stream(side):
+                got[1].append(tll.paged_attention(q, cache, batch, max_new=h))
+    torch.cuda.synchronize()
+    assert cache._workspace.numel() == small
+    for outs in got.values():
+        for i, out in enumerate(outs):
+            assert torch.equal(out, want[i % 4])

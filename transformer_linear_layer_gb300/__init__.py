@@ -882,6 +882,26 @@ class Rotary:
         self._ref = ctypes.byref(self._plan)
 
 
+# A single token's call is bound by its time on the host: the entries below ask for the
+# library, the context and the stream without a lock or an object each.
+
+def _loaded():
+    return _lib if _lib is not None else library()
+
+
+def _context(index):
+    return _contexts.get(index) or default_context(index)
+
+
+def _raw_stream(stream, index):
+    import torch
+
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _check_heads(t, dtype, what, index=None):
     """(rows, heads, width, row stride) of an N x H x D tensor (of ``dtype``, on CUDA
     device ``index``) whose rows hold their heads one after the other, any distance apart."""
@@ -920,9 +940,9 @@ def _rotary(call, x, positions, rotary, out, ctx, stream):
         No, Ho, Do, ldy = _check_heads(out, x.dtype, "out", index)
         if (No, Ho, Do) != (N, H, D):
             raise ValueError(f"out must have shape {(N, H, D)}, got {tuple(out.shape)}")
-    ctx = ctx or default_context(index)
-    rc = getattr(library(), call)(ctx._h, N, H, D, x.data_ptr(), ldx, out.data_ptr(), ldy, kind,
-                                  positions.data_ptr(), ptype, rotary._ref, _stream_ptr(stream, index))
+    ctx = ctx or _context(index)
+    rc = getattr(_loaded(), call)(ctx._h, N, H, D, x.data_ptr(), ldx, out.data_ptr(), ldy, kind,
+                                  positions.data_ptr(), ptype, rotary._ref, _raw_stream(stream, index))
     if rc != OK:
         raise LinError(rc, call)
     return out
@@ -965,6 +985,7 @@ class KVCache:
         self.pages, self.heads, self.page_size, self.head_dim = k.shape
         self.device, self.index = k.device, k.get_device()
         self._sizes: dict = {}  # workspace bytes by query heads and tokens
+        self._workspace = None  # of paged attention's calls on the default stream, which are in order
         self._plan = KVCachePlan(k.data_ptr(), v.data_ptr(), *(k.shape[i] for i in (0, 2, 1, 3)), *k.stride()[:3])
         self._ref = ctypes.byref(self._plan)
 
@@ -1039,10 +1060,10 @@ def cache_append(q, k, v, cache: KVCache, batch: KVBatch, rotary: Rotary | None 
     elif q_out is not None:
         raise ValueError("q_out without q")
     ptype = TYPE_INT64 if positions is None else _check_positions(positions, N, index)
-    ctx = ctx or default_context(index)
-    rc = library().lin_cache_append(ctx._h, cache._ref, batch._ref(N), H, _ptr(q), ldq, _ptr(q_out), ldo,
+    ctx = ctx or _context(index)
+    rc = _loaded().lin_cache_append(ctx._h, cache._ref, batch._ref(N), H, _ptr(q), ldq, _ptr(q_out), ldo,
                                     k.data_ptr(), ldk, v.data_ptr(), ldv, _ptr(positions), ptype,
-                                    None if rotary is None else rotary._ref, _stream_ptr(stream, index))
+                                    None if rotary is None else rotary._ref, _raw_stream(stream, index))
     if rc != OK:
         raise LinError(rc, "lin_cache_append")
     return q_out
@@ -1060,7 +1081,8 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     tokens the longest sequence has (default: the average), which picks the kernel; any value is
     right. Returns out (like q, contiguous), or (out, lse) with lse tokens x heads fp32 when ``with_lse`` or an lse
     tensor is given. Rows that belong to no sequence are not written. workspace: a uint8 tensor of
-    :func:`paged_attention_workspace` bytes (default: from torch's allocator, for this call)."""
+    :func:`paged_attention_workspace` bytes. By default, calls on the default stream share one that the cache
+    keeps, and any other call has its own from torch's allocator."""
     import torch
 
     index = cache.index
@@ -1080,9 +1102,9 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     elif lse is not None:
         _check(lse, torch.float32, (N, H), "lse")
         _same_device(q, lse)
-    ctx = ctx or default_context(index)
+    ctx = ctx or _context(index)
     hint = 0 if max_new is None else int(max_new)
-    raw = _stream_ptr(stream, index)
+    raw = _raw_stream(stream, index)
     if workspace is None:
         # (the size goes by the device too, and all contexts of a cache are on its own)
         key = (H, hint, N if hint == 0 else 0, batch.sequences if hint == 0 else 0)
@@ -1092,11 +1114,18 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
             if len(cache._sizes) > 64:
                 cache._sizes.clear()
             cache._sizes[key] = size
-        workspace = _scratch(cache.device, size, stream)
+        if raw == 0 and stream is None:
+            # The default stream: its calls run one after the other, and none is captured. The rest
+            # of the time (an allocation takes 3 us of a call's 15) a call's workspace is its own.
+            workspace = cache._workspace
+            if workspace is None or workspace.numel() < size:
+                workspace = cache._workspace = _scratch(cache.device, size, None)
+        else:
+            workspace = _scratch(cache.device, size, stream)
     else:
         _same_device(q, workspace)
         size = workspace.numel() * workspace.element_size()
-    rc = library().lin_paged_attention(ctx._h, cache._ref, batch._ref(N), H, q.data_ptr(), ldq, out.data_ptr(), ldo,
+    rc = _loaded().lin_paged_attention(ctx._h, cache._ref, batch._ref(N), H, q.data_ptr(), ldq, out.data_ptr(), ldo,
                                        _ptr(lse), int(bool(causal)), 0.0 if scale is None else float(scale), hint,
                                        workspace.data_ptr(), size, raw)
     if rc != OK:
