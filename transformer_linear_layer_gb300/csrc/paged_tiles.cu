@@ -25,6 +25,13 @@
 // values are set to zero in shared memory where they do not: a probability of 0 must not meet a
 // NaN in slots that were never written.
 // Every wait is bounded (about 1 s); a block that gives up sets the status word.
+//
+// Measured (GB300, with the joining kernel): 2 prompts of 4096 tokens, 16 heads of 128 on 2: 137 us, 1004
+// TF/s of the visible pairs' products (3100 cycles a block of 256 x 128, 2070 of them products when
+// nothing else is done); 4 chunks of 512 over 8704 keys, 12 heads of 64: 67 us, 790 TF/s (2500 cycles a
+// block, 1160 of products and 1250 of exponentials with two warps a scheduler). Tensor pipe 45 and 36 %,
+// DRAM 4 and 23 %: bound by a group's chain of scores, exponentials and products, and by the waits
+// between them, which queue behind the exponentials.
 #include <math.h>
 
 #include <type_traits>
