@@ -265,3 +265,39 @@ def test_the_default_streams_workspace_is_its_own():
     for outs in got.values():
         for i, out in enumerate(outs):
             assert torch.equal(out, want[i % 4])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("far", [-600.0, 600.0])
+def test_scores_of_minus_infinity_before_far_ones(D, far):
+    """The first 130 keys of each sequence score -inf for every query; the others lie far below, or far above, zero,
+    where an exponential against anything but their own maximum is 0 or inf."""
+    new, held = [60, 1, 3], [400, 140, 131]
+    cache, batch, starts, N = make(new, held, 2, D, 16, "heads")
+    fill(cache, batch, held)
+    for b, n in enumerate(held):
+        for p in range(n):
+            page_id, slot = int(batch.block_table[b, p // 16]), p % 16
+            cache.k[page_id, :, slot, 0] = float("-inf") if p < 130 else far / 4
+    q = queries(N, 4, D)
+    q[:, :, 0] = 4.0 * D ** 0.5
+    for max_new in (1, 10 ** 6):
+        out, lse = tll.paged_attention(q, cache, batch, max_new=max_new, with_lse=True)
+        for b, n in enumerate(held):
+            for i in range(new[b]):
+                at = n - new[b] + i + 1
+                row = starts[b] + i
+                for h in range(4):
+                    if at <= 130:
+                        assert (out[row, h] == 0).all() and lse[row, h] == -float("inf")
+                        continue
+                    ids = batch.block_table[b, torch.arange(130, at, device="cuda") // 16].long()
+                    slots = torch.arange(130, at, device="cuda") % 16
+                    k, v = (c[ids, h // 2, slots].double() for c in (cache.k, cache.v))
+                    s = k @ q[row, h].double() * D ** -0.5
+                    want, size = torch.softmax(s, 0) @ v, torch.softmax(s, 0) @ v.abs()
+                    # scores near 600 in fp32, and their product with log2 e: 4 half steps of 2^-24 * 900, once for the
+                    # probability and once for the sum, on top of the usual bound
+                    tol = 1.05 * 2.0 ** -8 * (size + want.abs()) + 8 * 2.0 ** -24 * 900 * size + 1e-5
+                    assert ((out[row, h].double() - want).abs() <= tol).all()
+                    assert (lse[row, h].double() - torch.logsumexp(s, 0)).abs() <= 1e-4 * (1 + abs(far))

@@ -12,8 +12,8 @@
 //               a box per page and 64 columns, each lane its own (pages of 8 tokens take 32
 //               boxes a tile, so that K and V have a warp each); Q per group.
 //   warps 1, 2  tcgen05.mma, a thread per group: S = Q K^T (128 x 128) into the
-//               group's 128 TMEM columns, then O += P V with P (bf16) as the TMEM operand, in
-//               the columns that S had: nothing of the scores passes through shared memory.
+//               group's 128 TMEM columns, then O += P V with P (bf16) as the TMEM operand, beside S
+//               or in its columns: nothing of the scores passes through shared memory.
 //   warps 4-7,  softmax of group 0 and 1, a thread per row: scores out of TMEM, scaled to
 //   warps 8-11  base-2 units by a packed FMA, exponentiated, rounded to bf16, back into TMEM.
 //               The reference for the exponents need not be the maximum: it is that of an
@@ -50,9 +50,9 @@ constexpr int kPtLaunch = 168, kPtLow = 72, kPtHigh = 216;
 static_assert(128 * kPtLow + 256 * kPtHigh <= kPtThreads * kPtLaunch, "register split");
 constexpr uint32_t kPtTmem = 512;
 constexpr int kPtParts = 4;             // parts of items that are described at a time
-constexpr int kPtLead = 2;               // blocks that an item's start and end cost (2 x 4096 tokens, 16 heads of 128
+constexpr int kPtLead = 2;              // blocks that an item's start and end cost (2 x 4096 tokens, 16 heads of 128
                                         // on 2: 179 us with 1, 150 with 2 and 3, 156 with 6; 4 x 512 over 8704: 71, 72, 76)
-constexpr float kPtRise = 65536.f;       // what 64 probabilities may add up to before their reference moves
+constexpr float kPtRise = 65536.f;      // what 64 probabilities may add up to before their reference moves
 
 template <int D>
 struct PtShape {
@@ -514,8 +514,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     };
                     uint32_t pk[2][16];
                     float sum;
-                    auto exponentials = [&]() {
-                        const float ref = m == NEG ? 0.f : m;
+                    auto exponentials = [&](float ref) {
                         const uint64_t nref = pt_pack(-ref * sl2, -ref * sl2);
                         uint64_t s2[2] = {0ull, 0ull};
 #pragma unroll
@@ -534,9 +533,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                         pt_unpack(pt_add2(s2[0], s2[1]), la, lb);
                         sum = la + lb;
                     };
-                    if (half == 0 && i == 0) m = top();
-                    exponentials();
-                    if (__builtin_expect((half == 1 || i > 0) && __any_sync(0xffffffffu, live && !(sum <= kPtRise)), 0)) {
+                    // A row that has no reference yet (its scores so far were all -inf) sums up inf or NaN and so
+                    // looks for one, except among keys that it does not see.
+                    const bool first = half == 0 && i == 0, sees = !decltype(masked)::value || c0 < lim;
+                    if (first) m = top();
+                    exponentials((first || !sees) && m == NEG ? 0.f : m);
+                    if (__builtin_expect(!first && __any_sync(0xffffffffu, live && !(sum <= kPtRise)), 0)) {
                         // The reference moves: the products so far are done, what they summed is scaled, and
                         // these keys are exponentiated again. (Rows that are none have no say: their q
                         // is whatever the shared memory held, and results would not repeat.)
@@ -555,7 +557,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                             for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
                             pt_st16(tO + h, ov);
                         }
-                        exponentials();
+                        exponentials(m == NEG ? 0.f : m);
                     }
                     l += sum;
                     if (P::kTurns && half == 1 && i < shared) {
