@@ -48,9 +48,9 @@ struct RotaryArgs {
     int rows;                       // rows a block takes
 };
 
-// cos and sin of p turns (turns in units of 2^-64 of a turn per position).
-__device__ __forceinline__ void turn(long long p, unsigned long long turns, float& c, float& s) {
-    const unsigned long long t = static_cast<unsigned long long>(p) * turns;
+// cos and sin at position p, modulo 2^64 (turns in units of 2^-64 of a turn per position).
+__device__ __forceinline__ void turn(unsigned long long p, unsigned long long turns, float& c, float& s) {
+    const unsigned long long t = p * turns;
     const unsigned q = static_cast<unsigned>((t + (1ull << 61)) >> 62);                  // nearest quarter
     const long long rest = static_cast<long long>(t - (static_cast<unsigned long long>(q) << 62));  // +- 2^61
     float c0, s0;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kRtThreads) rotary_kernel(const RotaryArgs a) 
         else
             pos = s_pos[r];
         float c, s;
-        turn(p.inverse ? -pos : pos, p.turns[f], c, s);
+        turn(p.inverse ? 0ull - (unsigned long long)pos : (unsigned long long)pos, p.turns[f], c, s);
         s_turn[i] = c * p.scale;
         s_turn[rows * half + i] = s * p.scale;
     }
