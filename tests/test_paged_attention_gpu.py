@@ -301,3 +301,31 @@ def test_scores_of_minus_infinity_before_far_ones(D, far):
                     tol = 1.05 * 2.0 ** -8 * (size + want.abs()) + 8 * 2.0 ** -24 * 900 * size + 1e-5
                     assert ((out[row, h].double() - want).abs() <= tol).all()
                     assert (lse[row, h].double() - torch.logsumexp(s, 0)).abs() <= 1e-4 * (1 + abs(far))
+
+
+@pytest.mark.parametrize("max_new", [1, 10 ** 6])
+def test_sequences_that_share_pages(max_new):
+    """A common prefix of two pages, one page twice in a table, and columns of a wider table."""
+    new, held = [2, 1, 40], [50, 37, 64]
+    cache, batch, starts, N = make(new, held, 2, 64, 16, "heads")
+    fill(cache, batch, held)
+    table = batch.block_table
+    wide = torch.full((3, table.shape[1] + 3), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    wide[1, :2] = table[0, :2]
+    wide[2, 3] = table[2, 0]
+    shared = tll.KVBatch(batch.q_start, batch.kv_len, wide[:, :table.shape[1]])
+    q = queries(N, 6, 64)
+    for causal in (True, False):
+        out, lse = tll.paged_attention(q, cache, shared, causal=causal, max_new=max_new, with_lse=True)
+        check(out, lse, q, cache, shared, starts, held, causal, 0.125)
+
+
+def test_batches_keep_their_arrays():
+    cache, batch, _, _ = make([1, 1], [20, 30], 2, 64, 16, "heads")
+    with pytest.raises(AttributeError):
+        batch.kv_len = batch.kv_len + 1
+    with pytest.raises(AttributeError):
+        cache.k = cache.v
+    batch.kv_len += 1  # in place: what the kernels read
+    assert batch.kv_len.tolist() == [21, 31]

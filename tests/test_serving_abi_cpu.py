@@ -249,3 +249,13 @@ def test_the_binding_refuses_tensors_that_are_not_on_the_gpu():
         tll.KVCache(torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         tll.KVBatch(torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(2, 4, dtype=torch.int32))
+
+
+def test_plans_keep_what_the_library_was_given():
+    plan = tll.Rotary(64, device="cpu")
+    with pytest.raises(AttributeError):
+        plan.scale = 2.0
+    with pytest.raises(AttributeError):
+        plan.turns = plan.turns.clone()
+    plan.turns += 0  # in place: the same tensor
+    assert plan.scale == 1.0 and plan._plan.turns == plan.turns.data_ptr()

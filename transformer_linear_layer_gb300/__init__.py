@@ -810,7 +810,18 @@ def distill_forward_backward(logits, ids, teacher, weight=None, temperature: flo
 
 # ---------------------------------------------------------------- rotary positions
 
-class Rotary:
+class _Fixed:
+    """A plan whose public attributes cannot be set anew: the library was given their addresses
+    and sizes once. (What their tensors hold may change, ``batch.kv_len += 1`` for instance.)"""
+
+    def __setattr__(self, name, value):
+        held = self.__dict__
+        if not name.startswith("_") and name in held and held[name] is not value:
+            raise AttributeError(f"{type(self).__name__}.{name} cannot be set anew: write into it, or make another")
+        held[name] = value
+
+
+class Rotary(_Fixed):
     """The plan of rotary positions: which elements of a head turn, and how fast.
 
     dim: elements of each head that rotate (even; the rest of the head does not).
@@ -965,7 +976,7 @@ def rotary_backward(dy, positions, rotary: Rotary, out=None, ctx: Context | None
 
 # ---------------------------------------------------------------- paged cache
 
-class KVCache:
+class KVCache(_Fixed):
     """A paged cache of keys and values: ``k`` and ``v`` bf16 of pages x heads x
     page_size x head width (64 or 128; page_size a power of two from 8 to 4096), of the same
     strides. The last dimension is contiguous, the others may have any
@@ -990,7 +1001,7 @@ class KVCache:
         self._ref = ctypes.byref(self._plan)
 
 
-class KVBatch:
+class KVBatch(_Fixed):
     """Sequences whose new tokens are rows of packed tensors (int32, on the GPU; the
     kernels read them when they run).
 
@@ -1076,7 +1087,7 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     (:func:`cache_append`).
 
     q: tokens x query heads x width, bf16, rows any multiple of 8 elements apart; query heads a multiple
-    (at most 128) of the cache's. causal: each token sees the keys up to its own place; otherwise all of its
+    (at most 128) of the cache's. scale: of the scores, default (or 0) 1/sqrt(width). causal: each token sees the keys up to its own place; otherwise all of its
     sequence's (a cross attention over an encoder's states). max_new: about how many new
     tokens the longest sequence has (default: the average), which picks the kernel; any value is
     right. Returns out (like q, contiguous), or (out, lse) with lse tokens x heads fp32 when ``with_lse`` or an lse
