@@ -11,13 +11,14 @@
 //   warps 0, 3  TMA. K and V of 128 keys are tiles of one ring (K, V, K, V, ...),
 //               a box per page and 64 columns, each lane its own (pages of 8 tokens take 32
 //               boxes a tile, so that K and V have a warp each); Q per group.
-//   warps 1, 2  tcgen05.mma, a thread per group: S = Q K^T (128 x 128) into the
+//   warps 1, 2  tcgen05.mma, an elected thread per group: S = Q K^T (128 x 128) into the
 //               group's 128 TMEM columns, then O += P V with P (bf16) as the TMEM operand, beside S
-//               or in its columns: nothing of the scores passes through shared memory.
+//               (heads of 64) or in its columns: nothing of the scores passes through shared memory.
 //   warps 4-7,  softmax of group 0 and 1, a thread per row: scores out of TMEM, scaled to
 //   warps 8-11  base-2 units by a packed FMA, exponentiated, rounded to bf16, back into TMEM.
 //               The reference for the exponents need not be the maximum: it is that of an
-//               item's first 64 keys, and stays while 64 probabilities of a row add up to at most 2^16
+//               item's first 64 keys (when they all score -inf, of the first that do not), and stays
+//               while 64 probabilities of a row add up to at most 2^16
 //               (bf16 keeps its relative precision; the argument of an exponential stays below 16, and its
 //               rounding below 2^-20). So nothing waits for a maximum and none is taken; in the
 //               rare case that the scores have risen, O is scaled and the 64 keys are exponentiated again.
