@@ -8,7 +8,7 @@
 // exponentials bound it, not memory. Both groups work on the same keys, so that
 // a block of 128 keys, brought in once, serves 256 rows (two tiles apart would ask the
 // L2 for 60 bytes a cycle and SM); and one group's softmax runs under the other's products.
-//   warps 0, 3  TMA. K and V of 128 keys are tiles of one ring (K, V, K, V, ...),
+//   warps 0, 3  TMA. K and V of 128 keys are tiles of a ring each,
 //               a box per page and 64 columns, each lane its own (pages of 8 tokens take 32
 //               boxes a tile, so that K and V have a warp each); Q per group.
 //   warps 1, 2  tcgen05.mma, an elected thread per group: S = Q K^T (128 x 128) into the
@@ -58,7 +58,11 @@ constexpr float kPtRise = 65536.f;      // what 64 probabilities may add up to b
 template <int D>
 struct PtShape {
     static constexpr uint32_t kTile = kPtKeys * D * 2;      // K, V or Q: halves of 64 columns, 16 KiB each
-    static constexpr int S = D == 64 ? 10 : 5;              // tiles of the ring
+    // Tiles of K's ring and of V's. A barrier's wait tells odd phases from even ones only, so whoever waits for a slot
+    // may be at most one phase ahead of it: each ring has one producer, which fills every phase of its
+    // slots itself, and each group releases every tile of both. (Were a slot to alternate between the two producers, one of them
+    // would wait for it two phases after its last fill, and take the release before that for the one it waits for.)
+    static constexpr int KS = D == 64 ? 5 : 3, VS = D == 64 ? 5 : 2, S = KS + VS;
     static constexpr size_t kSmem = 1024 + (2 + S) * (size_t)kTile;
     // TMEM columns of a group: S (128), O (D) and P (64). Heads of 64 leave room for P beside
     // S, so that the next block's S is computed while this one's exponentials are; with
@@ -164,7 +168,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const PagedArgs a) {
     using P = PtShape<D>;
-    constexpr int S = P::S, HALVES = D / 64;
+    constexpr int KS = P::KS, VS = P::VS, S = P::S, HALVES = D / 64;  // slots: K's, then V's
     constexpr uint32_t kHalf = kPtKeys * 128;
     constexpr uint32_t IDESC_S = make_idesc(1u, 128, kPtKeys);
     constexpr uint32_t IDESC_O = make_idesc(1u, 128, D, false, true);
@@ -229,7 +233,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         // ---- TMA: warp 0 the parts, Q and K, warp 3 V; whole warps walk the stretch ----
         const bool keys = warp == 0;
         PagedCut cut = {0, 0, 0, 0};
-        uint32_t st = keys ? 0 : 1, ph = 1, issued = 0, np = 0, nq[2] = {0, 0};  // the next tile; what has been issued
+        const uint32_t first = keys ? 0 : KS, slots = keys ? KS : VS;             // this warp's ring
+        uint32_t st = first, ph = 1, issued = 0, np = 0, nq[2] = {0, 0};          // the next tile; what has been issued
         bool ok = true;
         const int each = a.TQ / 2;
         const PagedBox<kPtKeys> box(a);
@@ -276,8 +281,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     tma_load_4d(to + st * P::kTile, keys ? &tmK : &tmV, full0 + 8 * st, 64 * box.group, box.slot(a, key0),
                                 p.h, box.page(a, entry));
                 ++issued;
-                if ((st += 2) >= S) {
-                    st -= S;
+                if (++st == first + slots) {
+                    st = first;
                     ph ^= 1;
                 }
                 if (i > 0 || !keys) continue;
@@ -312,9 +317,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             // the copies in flight land before the block ends
             for (int grp = 0; grp < 2; ++grp)
                 if (nq[grp] > 0) mbar_wait(qfull0 + 8 * grp, (nq[grp] - 1) & 1);
-            for (uint32_t back = 1; back <= issued && back <= (S + 1u) / 2; ++back) {
-                const uint32_t g = 2 * (issued - back) + (keys ? 0 : 1);
-                mbar_wait(full0 + 8 * (g % S), (g / S) & 1);
+            for (uint32_t back = 1; back <= issued && back <= slots; ++back) {
+                const uint32_t g = issued - back;
+                mbar_wait(full0 + 8 * (first + g % slots), (g / slots) & 1);
             }
         }
     } else if (warp < 3) {
@@ -324,13 +329,19 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const uint32_t tS = tmem + P::kS + 128u * grp, tP = tmem + P::kP + P::kPStep * grp, tO = tmem + P::kO + P::kPStep * grp;
         const uint64_t qd = sw128_kmajor_desc(smem_u32(sQ + grp * P::kTile));
         const uint64_t kd0 = sw128_kmajor_desc(smem_u32(ring)), vd0 = pt_v_desc(smem_u32(ring));
-        uint32_t ks = 0, kph = 0, vs = 1, vph = 0;  // the next K and V tile
-        uint32_t nq = 0, cs = 0, c = 0;             // Q tiles, blocks whose S is issued, blocks
+        uint32_t ks = 0, kph = 0, vs = KS, vph = 0;  // the next K and V tile
+        uint32_t nq = 0, cs = 0, c = 0;              // Q tiles, blocks whose S is issued, blocks
         bool ok = true;
-        auto step = [&](uint32_t& s, uint32_t& ph) {
-            if ((s += 2) >= S) {
-                s -= S;
-                ph ^= 1;
+        auto step_k = [&]() {
+            if (++ks == KS) {
+                ks = 0;
+                kph ^= 1;
+            }
+        };
+        auto step_v = [&]() {
+            if (++vs == S) {
+                vs = KS;
+                vph ^= 1;
             }
         };
         // S of the group's next block, issued by one thread once its keys are there and, with
@@ -350,7 +361,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         };
         auto issued = [&]() {
             __syncwarp();
-            step(ks, kph);
+            step_k();
             ++cs;
         };
         for (uint32_t np = 0; ok; ++np) {
@@ -404,7 +415,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 else
                     __syncwarp();
                 ++c;
-                step(vs, vph);
+                step_v();
             }
             for (int i = n; ok && i < p.n; ++i) {  // the other group's blocks only
                 if (!wait(full0 + 8 * ks, kph) || !wait(full0 + 8 * vs, vph)) {
@@ -415,8 +426,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     mbar_arrive(empty0 + 8 * ks);
                     mbar_arrive(empty0 + 8 * vs);
                 }
-                step(ks, kph);
-                step(vs, vph);
+                step_k();
+                step_v();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(pempty0 + 8 * ps);
@@ -436,7 +447,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                        tO = tmem + lanes + P::kO + P::kPStep * grp;
         const float NEG = -INFINITY, sl2 = a.scale_log2;
         const uint64_t sl2x2 = pt_pack(sl2, sl2);
-        uint32_t g = 0, np = 0, c = 0, no = 0;  // tiles, parts, blocks and outputs of the group
+        uint32_t g = 0, np = 0, c = 0, no = 0;  // blocks of the parts so far, parts, blocks and outputs of the group
         uint32_t turns = 0;                     // blocks that both groups have taken turns with
         bool ok = true;
         for (; ok; ++np) {
@@ -469,8 +480,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 tmem_ld32_async(tS + 96u, sv[1][1]);
                 if (decltype(masked)::value && k0 + kPtKeys > p.seen) {
                     // values of keys that nobody sees
-                    const uint32_t v = g + 2 * (uint32_t)i + 1, vs = v % S;
-                    if (!wait(full0 + 8 * vs, (v / S) & 1)) return false;
+                    const uint32_t v = g + (uint32_t)i, vs = KS + v % VS;
+                    if (!wait(full0 + 8 * vs, (v / VS) & 1)) return false;
                     if (k0 + row >= p.seen) {
                         uint8_t* dst = ring + vs * P::kTile + row * 128;
 #pragma unroll
@@ -631,7 +642,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 }
                 tc_fence_before();
             }
-            g += 2 * (uint32_t)p.n;
+            g += (uint32_t)p.n;
             __syncwarp();
             if (lane == 0) mbar_arrive(pempty0 + 8 * ps);
         }
