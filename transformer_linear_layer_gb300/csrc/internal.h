@@ -134,6 +134,10 @@ int ensure_smem_attr(std::atomic<unsigned long long>& done, Kernel kern, size_t 
     return LIN_OK;
 }
 
+// Whether a CUDA context is current on this thread. There is none before the thread's first call of the runtime that needs
+// one; encoding a tensor map, a call of the driver, is not one of those, and fails.
+bool thread_has_context();
+
 // A call on `st` that was launched in plain stream order, or whose kernels wait for what
 // is before them before they let others start: [p, p + bytes) is all that may still be
 // written there.

@@ -319,12 +319,13 @@ bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
     return pa < pb + bn && pb < pa + an;
 }
 
+// Makes `dev` the thread's current device, and its context the current one.
 struct DeviceGuard {
     int prev = -1;
     bool ok = true;
     explicit DeviceGuard(int dev) {
         if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
-        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
+        if ((prev != dev || !thread_has_context()) && cudaSetDevice(dev) != cudaSuccess) ok = false;
     }
     ~DeviceGuard() {
         int cur = -1;

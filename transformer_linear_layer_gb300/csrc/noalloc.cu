@@ -86,6 +86,13 @@ bool ranges_overlap(const void* a, size_t an, const void* b, size_t bn) {
 }
 
 }  // namespace
+
+bool thread_has_context() {
+    CtxGetCurrentFn get_ctx = ctx_get_current_fn();
+    CUcontext ctx = nullptr;
+    return get_ctx && get_ctx(&ctx) == CUDA_SUCCESS && ctx != nullptr;
+}
+
 }  // namespace lin
 
 extern "C" int lin_forward_fp32_static(int M, int N, int K, const float* X, const float* W, const float* bias,
