@@ -1116,6 +1116,12 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     ctx = ctx or _context(index)
     hint = 0 if max_new is None else int(max_new)
     raw = _raw_stream(stream, index)
+
+    def enqueue(workspace, size):
+        return _loaded().lin_paged_attention(ctx._h, cache._ref, batch._ref(N), H, q.data_ptr(), ldq, out.data_ptr(), ldo,
+                                             _ptr(lse), int(bool(causal)), 0.0 if scale is None else float(scale), hint,
+                                             workspace.data_ptr(), size, raw)
+
     if workspace is None:
         # (the size goes by the device too, and all contexts of a cache are on its own)
         key = (H, hint, N if hint == 0 else 0, batch.sequences if hint == 0 else 0)
@@ -1126,22 +1132,30 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
                 cache._sizes.clear()
             cache._sizes[key] = size
         if raw == 0 and stream is None:
-            # The default stream: its calls run one after the other, and none is captured. The rest
+            # The default stream: its kernels run one after the other, and none is captured. The rest
             # of the time (an allocation takes 3 us of a call's 15) a call's workspace is its own.
-            workspace = cache._workspace
-            if workspace is None or workspace.numel() < size:
-                workspace = cache._workspace = _scratch(cache.device, size, None)
+            # One thread at a time, since a call's two kernels have to follow one another on the stream.
+            with _turn(index):
+                workspace = cache._workspace
+                if workspace is None or workspace.numel() < size:
+                    workspace = cache._workspace = _scratch(cache.device, size, None)
+                rc = enqueue(workspace, size)
         else:
-            workspace = _scratch(cache.device, size, stream)
+            rc = enqueue(_scratch(cache.device, size, stream), size)
     else:
         _same_device(q, workspace)
-        size = workspace.numel() * workspace.element_size()
-    rc = _loaded().lin_paged_attention(ctx._h, cache._ref, batch._ref(N), H, q.data_ptr(), ldq, out.data_ptr(), ldo,
-                                       _ptr(lse), int(bool(causal)), 0.0 if scale is None else float(scale), hint,
-                                       workspace.data_ptr(), size, raw)
+        rc = enqueue(workspace, workspace.numel() * workspace.element_size())
     if rc != OK:
         raise LinError(rc, "lin_paged_attention")
     return (out, lse) if lse is not None else out
+
+
+_turns: dict = {}  # by device: who enqueues on its default stream with the shared workspace
+
+
+def _turn(index):
+    turn = _turns.get(index)
+    return turn if turn is not None else _turns.setdefault(index, threading.RLock())
 
 
 def paged_attention_workspace(cache: KVCache, batch: KVBatch, tokens: int, heads: int, max_new: int = 0,
