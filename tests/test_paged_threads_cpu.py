@@ -59,3 +59,15 @@ def test_calls_of_two_threads_do_not_mix_their_launches(monkeypatch):
         t.join()
     assert len(lib.launches) == 60 and len({w for w, _ in lib.launches}) == 1
     assert all(a == b for a, b in zip(lib.launches[::2], lib.launches[1::2]))
+
+
+def test_caches_of_a_device_share_one_workspace(monkeypatch):
+    """A model has a cache a layer: what calls on the default stream keep does not grow with their number."""
+    lib = stand_ins(monkeypatch)
+    batch = types.SimpleNamespace(index=0, sequences=1, _ref=lambda n: None)
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    layers = caches(5)
+    for c in layers:
+        tll.paged_attention(q, c, batch, max_new=1, out=torch.empty_like(q))
+    assert len({w for w, _ in lib.launches}) == 1
+    assert len({c._workspace.data_ptr() for c in layers}) == 1

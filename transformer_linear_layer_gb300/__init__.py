@@ -996,9 +996,12 @@ class KVCache(_Fixed):
         self.pages, self.heads, self.page_size, self.head_dim = k.shape
         self.device, self.index = k.device, k.get_device()
         self._sizes: dict = {}  # workspace bytes by query heads and tokens
-        self._workspace = None  # of paged attention's calls on the default stream, which are in order
         self._plan = KVCachePlan(k.data_ptr(), v.data_ptr(), *(k.shape[i] for i in (0, 2, 1, 3)), *k.stride()[:3])
         self._ref = ctypes.byref(self._plan)
+
+    @property
+    def _workspace(self):
+        return _default_stream(self.index).workspace
 
 
 class KVBatch(_Fixed):
@@ -1092,8 +1095,8 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     tokens the longest sequence has (default: the average), which picks the kernel; any value is
     right. Returns out (like q, contiguous), or (out, lse) with lse tokens x heads fp32 when ``with_lse`` or an lse
     tensor is given. Rows that belong to no sequence are not written. workspace: a uint8 tensor of
-    :func:`paged_attention_workspace` bytes. By default, calls on the default stream share one that the cache
-    keeps, and any other call has its own from torch's allocator."""
+    :func:`paged_attention_workspace` bytes, for one call at a time. By default, calls on the default stream share one
+    that is kept for the device (up to 40 MB on a GB300), and any other call has its own from torch's allocator."""
     import torch
 
     index = cache.index
@@ -1135,11 +1138,11 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
             # The default stream: its kernels run one after the other, and none is captured. The rest
             # of the time (an allocation takes 3 us of a call's 15) a call's workspace is its own.
             # One thread at a time, since a call's two kernels have to follow one another on the stream.
-            with _turn(index):
-                workspace = cache._workspace
-                if workspace is None or workspace.numel() < size:
-                    workspace = cache._workspace = _scratch(cache.device, size, None)
-                rc = enqueue(workspace, size)
+            shared = _default_stream(index)
+            with shared.turn:
+                if shared.workspace is None or shared.workspace.numel() < size:
+                    shared.workspace = _scratch(cache.device, size, None)
+                rc = enqueue(shared.workspace, size)
         else:
             rc = enqueue(_scratch(cache.device, size, stream), size)
     else:
@@ -1150,12 +1153,19 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     return (out, lse) if lse is not None else out
 
 
-_turns: dict = {}  # by device: who enqueues on its default stream with the shared workspace
+class _DefaultStream:
+    """The workspace of paged attention's calls on a device's default stream, and whose turn it is to enqueue with it."""
+
+    def __init__(self):
+        self.turn, self.workspace = threading.RLock(), None
 
 
-def _turn(index):
-    turn = _turns.get(index)
-    return turn if turn is not None else _turns.setdefault(index, threading.RLock())
+_default_streams: dict = {}
+
+
+def _default_stream(index) -> _DefaultStream:
+    shared = _default_streams.get(index)
+    return shared if shared is not None else _default_streams.setdefault(index, _DefaultStream())
 
 
 def paged_attention_workspace(cache: KVCache, batch: KVBatch, tokens: int, heads: int, max_new: int = 0,
