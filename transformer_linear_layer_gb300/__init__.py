@@ -333,6 +333,16 @@ def _stream_ptr(stream, device):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _torch_stream(stream, device):
+    """torch's stream of a stream object or a raw handle (to torch, an external stream of handle 0 is any of its own)."""
+    import torch
+
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+
+
 _contexts: dict = {}
 
 
@@ -1187,8 +1197,5 @@ def _scratch(device, size, stream):
 
     if stream is None:
         return torch.empty(size, dtype=torch.uint8, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
-                                           device=device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_torch_stream(stream, device)):
         return torch.empty(size, dtype=torch.uint8, device=device)
