@@ -6,6 +6,10 @@ arguments: torch supplies device memory and the current CUDA stream, and every
 step of the multiply runs in this package's CUDA kernels. There is no CPU path:
 if the library is missing or the GPU call fails, an exception is raised.
 
+Calls run on the current stream, or on ``stream`` (a stream object or a raw handle): their
+results are then that stream's memory, as if made with it as the current one, and may be
+used on the current stream too once it waits for them.
+
     import torch, transformer_linear_layer_gb300 as tll
     y = tll.forward(x_bf16, w_bf16, bias_fp32, epilogue="gelu")   # -> bf16
 """
@@ -343,6 +347,20 @@ def _torch_stream(stream, device):
     return torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
 
 
+def _empty(shape, dtype, device, stream):
+    """A call's result: memory taken on the stream that its kernels run on (a block freed on another may still be in use
+    there), and not given back before what the current stream does with it is done."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(current)
+    return out
+
+
 _contexts: dict = {}
 
 
@@ -357,7 +375,7 @@ def default_context(device: int) -> Context:
     return ctx
 
 
-def _marshal(x, w, bias, out, precision):
+def _marshal(x, w, bias, out, precision, stream):
     import torch
 
     prec = precision
@@ -379,7 +397,7 @@ def _marshal(x, w, bias, out, precision):
         if bias.dtype != torch.float32 or not bias.is_cuda or bias.shape != (N,) or not bias.is_contiguous():
             raise ValueError("bias must be a contiguous fp32 CUDA vector of length N")
     if out is None:
-        out = torch.empty((M, N), dtype=want, device=x.device)
+        out = _empty((M, N), want, x.device, stream)
     elif out.dtype != want or out.shape != (M, N) or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("out must be a contiguous M x N CUDA tensor of the output dtype")
     return prec, M, N, K, out
@@ -391,7 +409,7 @@ def forward(x, w, bias=None, epilogue="none", precision=None, out=None, ctx: Con
     x: M x K, w: N x K (bf16 for precision "bf16", fp32 for "fp32"/"tf32"),
     bias: fp32 length N or None, epilogue: "none" | "gelu". Returns Y (M x N).
     """
-    prec, M, N, K, out = _marshal(x, w, bias, out, precision)
+    prec, M, N, K, out = _marshal(x, w, bias, out, precision, stream)
     dev = x.device.index if x.device.index is not None else 0
     ctx = ctx or default_context(dev)
     rc = ctx.forward_ptr(M, N, K, x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
@@ -406,7 +424,7 @@ def forward_residual(x, w, residual, bias=None, epilogue="none", precision=None,
     """Y = act(x . w^T + bias) + residual, the add in the GEMM's store.
     ``out`` may be ``residual`` itself (x = x + layer(h) in place); by
     default Y is a new tensor."""
-    prec, M, N, K, out = _marshal(x, w, bias, out, precision)
+    prec, M, N, K, out = _marshal(x, w, bias, out, precision, stream)
     _check(residual, out.dtype, (M, N), "residual")
     dev = x.device.index if x.device.index is not None else 0
     ctx = ctx or default_context(dev)
@@ -436,10 +454,10 @@ def fold_layernorm(w, gamma, beta=None, bias=None, precision="fp32", w_out=None,
     prec = _prec(precision)
     wdt = torch.bfloat16 if prec == PREC_BF16 else torch.float32
     if w_out is None:
-        w_out = torch.empty((N, K), dtype=wdt, device=w.device)
+        w_out = _empty((N, K), wdt, w.device, stream)
     _check(w_out, wdt, (N, K), "w_out")
     if bias_out is None:
-        bias_out = torch.empty((N,), dtype=torch.float32, device=w.device)
+        bias_out = _empty((N,), torch.float32, w.device, stream)
     _check(bias_out, torch.float32, (N,), "bias_out")
     dev = w.device.index if w.device.index is not None else 0
     ctx = ctx or default_context(dev)
@@ -454,7 +472,7 @@ def fold_layernorm(w, gamma, beta=None, bias=None, precision="fp32", w_out=None,
 def forward_plan(plan: Plan, x, w, bias=None, epilogue="none", precision=None, out=None,
                  ctx: Context | None = None, stream=None):
     """As :func:`forward` with an explicit launch configuration."""
-    prec, M, N, K, out = _marshal(x, w, bias, out, precision)
+    prec, M, N, K, out = _marshal(x, w, bias, out, precision, stream)
     dev = x.device.index if x.device.index is not None else 0
     ctx = ctx or default_context(dev)
     rc = ctx.forward_plan_ptr(plan, M, N, K, x.data_ptr(), w.data_ptr(),
@@ -493,7 +511,7 @@ def backward_data(dz, w, out=None, precision=None, ctx: Context | None = None, s
     _check(dz, want, (M, N), "dz")
     _check(w, want, (N, K), "w")
     if out is None:
-        out = torch.empty((M, K), dtype=want, device=dz.device)
+        out = _empty((M, K), want, dz.device, stream)
     _check(out, want, (M, K), "out")
     dev = dz.device.index if dz.device.index is not None else 0
     ctx = ctx or default_context(dev)
@@ -517,7 +535,7 @@ def backward_data_gelu(dz, w, zp, out=None, precision=None, ctx: Context | None 
     _check(w, want, (N, K), "w")
     _check(zp, want, (M, K), "zp")
     if out is None:
-        out = torch.empty((M, K), dtype=want, device=dz.device)
+        out = _empty((M, K), want, dz.device, stream)
     _check(out, want, (M, K), "out")
     dev = dz.device.index if dz.device.index is not None else 0
     ctx = ctx or default_context(dev)
@@ -539,10 +557,10 @@ def backward_weight(dz, x, out=None, db=None, precision=None, ctx: Context | Non
     _check(dz, want, (M, N), "dz")
     _check(x, want, (M, K), "x")
     if out is None:
-        out = torch.empty((N, K), dtype=want, device=dz.device)
+        out = _empty((N, K), want, dz.device, stream)
     _check(out, want, (N, K), "out")
     if db is True:
-        db = torch.empty((N,), dtype=torch.float32, device=dz.device)
+        db = _empty((N,), torch.float32, dz.device, stream)
     if db is not None and db is not False:
         _check(db, torch.float32, (N,), "db")
     else:
@@ -564,7 +582,7 @@ def gelu_backward(dy, z, out=None, precision=None, ctx: Context | None = None, s
     _check(dy, want, tuple(dy.shape), "dy")
     _check(z, want, tuple(dy.shape), "z")
     if out is None:
-        out = torch.empty_like(dy)
+        out = _empty(dy.shape, dy.dtype, dy.device, stream)
     _check(out, want, tuple(dy.shape), "out")
     dev = dy.device.index if dy.device.index is not None else 0
     ctx = ctx or default_context(dev)
@@ -591,10 +609,10 @@ def attention_forward(qkv, B: int, T: int, H: int, causal: bool = True, scale: f
     C = H * D
     _check(qkv, torch.bfloat16, (B * T, 3 * C), "qkv")
     if out is None:
-        out = torch.empty((B * T, C), dtype=torch.bfloat16, device=qkv.device)
+        out = _empty((B * T, C), torch.bfloat16, qkv.device, stream)
     _check(out, torch.bfloat16, (B * T, C), "out")
     if lse is None and with_lse:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=qkv.device)
+        lse = _empty((B, H, T), torch.float32, qkv.device, stream)
     if lse is not None:
         _check(lse, torch.float32, (B, H, T), "lse")
     dev = qkv.device.index if qkv.device.index is not None else 0
@@ -623,7 +641,7 @@ def attention_backward(qkv, out, lse, dout, B: int, T: int, H: int, causal: bool
     _check(lse, torch.float32, (B, H, T), "lse")
     _check(dout, torch.bfloat16, (B * T, C), "dout")
     if dqkv is None:
-        dqkv = torch.empty_like(qkv)
+        dqkv = _empty(qkv.shape, qkv.dtype, qkv.device, stream)
     _check(dqkv, torch.bfloat16, (B * T, 3 * C), "dqkv")
     _same_device(qkv, out, lse, dout, dqkv)
     dev = qkv.device.index if qkv.device.index is not None else 0
@@ -709,11 +727,11 @@ def token_logprobs(logits, tokens=None, top: int = 0, temperature: float = 1.0, 
     if tokens is not None:
         ttype = _index_type(tokens, "tokens")
         _check(tokens, tokens.dtype, (R,), "tokens")
-    logprob = None if tokens is None else torch.empty(R, dtype=torch.float32, device=logits.device)
-    entropy = torch.empty(R, dtype=torch.float32, device=logits.device)
-    lse = torch.empty(R, dtype=torch.float32, device=logits.device)
-    top_logprob = torch.empty((R, top), dtype=torch.float32, device=logits.device)
-    top_ids = torch.empty((R, top), dtype=torch.int32, device=logits.device)
+    logprob = None if tokens is None else _empty(R, torch.float32, logits.device, stream)
+    entropy = _empty(R, torch.float32, logits.device, stream)
+    lse = _empty(R, torch.float32, logits.device, stream)
+    top_logprob = _empty((R, top), torch.float32, logits.device, stream)
+    top_ids = _empty((R, top), torch.int32, logits.device, stream)
     dev = logits.device.index if logits.device.index is not None else 0
     ctx = ctx or default_context(dev)
     rc = library().lin_token_logprobs(ctx._h, R, V, logits.data_ptr(), ld, ztype, _ptr(tokens), ttype,
@@ -743,7 +761,7 @@ def _distill_args(logits, ids, teacher, lse=None, weight=None):
             teacher.data_ptr(), ttype)
 
 
-def _dlogits(logits, out, args):
+def _dlogits(logits, out, args, stream):
     """The gradient's tensor and row stride: ``out``, or a new one whose rows
     lie like the logits' (padding included, so that both move in whole units)."""
     import torch
@@ -751,7 +769,7 @@ def _dlogits(logits, out, args):
     R, V, ld = args[0], args[1], args[4]
     if out is None:
         pitch = ld if ld <= V + 1024 else V
-        out = torch.empty((R, pitch), dtype=logits.dtype, device=logits.device)
+        out = _empty((R, pitch), logits.dtype, logits.device, stream)
         return (out if pitch == V else out[:, :V]), pitch
     if out.dtype != logits.dtype or out.shape != logits.shape:
         raise ValueError("out must have the logits' shape and type")
@@ -770,8 +788,8 @@ def distill_forward(logits, ids, teacher, temperature: float = 1.0, ctx: Context
     import torch
 
     args = _distill_args(logits, ids, teacher)
-    loss = torch.empty(args[0], dtype=torch.float32, device=logits.device)
-    lse = torch.empty(args[0], dtype=torch.float32, device=logits.device)
+    loss = _empty(args[0], torch.float32, logits.device, stream)
+    lse = _empty(args[0], torch.float32, logits.device, stream)
     dev = logits.device.index if logits.device.index is not None else 0
     ctx = ctx or default_context(dev)
     rc = library().lin_distill_forward(ctx._h, *args, float(temperature), loss.data_ptr(), lse.data_ptr(),
@@ -789,7 +807,7 @@ def distill_backward(logits, ids, teacher, lse, grad_loss, temperature: float = 
     probabilities' digits (above 512 for bf16 logits, 64 for fp32) are summed
     again."""
     args = _distill_args(logits, ids, teacher, lse, grad_loss)
-    out, ldd = _dlogits(logits, out, args)
+    out, ldd = _dlogits(logits, out, args, stream)
     dev = logits.device.index if logits.device.index is not None else 0
     ctx = ctx or default_context(dev)
     rc = library().lin_distill_backward(ctx._h, *args, float(temperature), lse.data_ptr(), grad_loss.data_ptr(),
@@ -807,8 +825,8 @@ def distill_forward_backward(logits, ids, teacher, weight=None, temperature: flo
     import torch
 
     args = _distill_args(logits, ids, teacher, None, weight)
-    out, ldd = _dlogits(logits, out, args)
-    loss = torch.empty(args[0], dtype=torch.float32, device=logits.device)
+    out, ldd = _dlogits(logits, out, args, stream)
+    loss = _empty(args[0], torch.float32, logits.device, stream)
     dev = logits.device.index if logits.device.index is not None else 0
     ctx = ctx or default_context(dev)
     rc = library().lin_distill_forward_backward(ctx._h, *args, float(temperature), _ptr(weight), loss.data_ptr(),
@@ -956,7 +974,7 @@ def _rotary(call, x, positions, rotary, out, ctx, stream):
     if rotary.index != index:
         raise ValueError(f"the rotary plan must be on cuda:{index}, got cuda:{rotary.index}")
     if out is None:
-        out, ldy = torch.empty((N, H, D), dtype=x.dtype, device=x.device), H * D
+        out, ldy = _empty((N, H, D), x.dtype, x.device, stream), H * D
     else:
         No, Ho, Do, ldy = _check_heads(out, x.dtype, "out", index)
         if (No, Ho, Do) != (N, H, D):
@@ -1076,7 +1094,7 @@ def cache_append(q, k, v, cache: KVCache, batch: KVBatch, rotary: Rotary | None 
         if rotary is None:
             raise ValueError("q is only rotated: without a rotary plan it must be None")
         if q_out is None:
-            q_out, ldo = torch.empty((N, H, D), dtype=bf16, device=cache.device), H * D
+            q_out, ldo = _empty((N, H, D), bf16, cache.device, stream), H * D
         else:
             No, Ho, Do, ldo = _check_heads(q_out, bf16, "q_out", index)
             if (No, Ho, Do) != (N, H, D):
@@ -1116,13 +1134,13 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     if batch.index != index:
         raise ValueError(f"the batch must be on cuda:{index}, like the cache")
     if out is None:
-        out, ldo = torch.empty((N, H, D), dtype=torch.bfloat16, device=cache.device), H * D
+        out, ldo = _empty((N, H, D), torch.bfloat16, cache.device, stream), H * D
     else:
         No, Ho, Do, ldo = _check_heads(out, torch.bfloat16, "out", index)
         if (No, Ho, Do) != (N, H, D):
             raise ValueError(f"out must have shape {(N, H, D)}, got {tuple(out.shape)}")
     if lse is None and with_lse:
-        lse = torch.empty((N, H), dtype=torch.float32, device=cache.device)
+        lse = _empty((N, H), torch.float32, cache.device, stream)
     elif lse is not None:
         _check(lse, torch.float32, (N, H), "lse")
         _same_device(q, lse)
@@ -1191,8 +1209,7 @@ def paged_attention_workspace(cache: KVCache, batch: KVBatch, tokens: int, heads
 
 
 def _scratch(device, size, stream):
-    """Bytes from torch's allocator for one call's kernels, taken on the stream that they
-    run on (the memory may still be in use by earlier work of any other)."""
+    """Bytes from torch's allocator for one call's kernels, taken on the stream that they run on."""
     import torch
 
     if stream is None:
