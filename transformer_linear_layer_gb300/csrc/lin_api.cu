@@ -1337,6 +1337,9 @@ int rotary_run(lin_ctx* ctx, int N, int H, int D, const void* x, long long ldx, 
         rows_overlap(out, Rows{rotary->turns, 1, (long long)turn_bytes, (long long)turn_bytes, 1}))
         return LIN_ERR_ARG;
     if (((uintptr_t)x | (uintptr_t)y) % esz != 0 || (uintptr_t)positions % psz != 0) return LIN_ERR_ALIGN;
+    // Nothing turns and everything is in its place. No kernel runs, so what the stream's earlier calls may still
+    // be writing stays on its list.
+    if (in_place && rotary->dim == 0) return LIN_OK;
     DeviceGuard guard(ctx->device);
     if (!guard.ok) return LIN_ERR_CUDA;
     RotaryProblem p;
