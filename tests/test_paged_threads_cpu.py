@@ -4,6 +4,7 @@ import threading
 import time
 import types
 
+import pytest
 import torch
 
 import transformer_linear_layer_gb300 as tll
@@ -71,3 +72,18 @@ def test_caches_of_a_device_share_one_workspace(monkeypatch):
         tll.paged_attention(q, c, batch, max_new=1, out=torch.empty_like(q))
     assert len({w for w, _ in lib.launches}) == 1
     assert len({c._workspace.data_ptr() for c in layers}) == 1
+
+
+def test_a_workspace_must_hold_what_its_shape_says(monkeypatch):
+    """One byte expanded, or every other byte: the kernels would write past the tensor's memory."""
+    lib = stand_ins(monkeypatch)
+    cache, = caches(1)
+    batch = types.SimpleNamespace(index=0, sequences=1, _ref=lambda n: None)
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    for bad in (torch.empty(1, dtype=torch.uint8).expand(1 << 20), torch.empty(8192, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            tll.paged_attention(q, cache, batch, max_new=1, out=torch.empty_like(q), workspace=bad)
+    assert not lib.launches
+    good = torch.empty(1024, dtype=torch.float32)
+    tll.paged_attention(q, cache, batch, max_new=1, out=torch.empty_like(q), workspace=good)
+    assert lib.launches == [(good.data_ptr(), threading.get_ident())] * 2

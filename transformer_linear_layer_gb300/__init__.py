@@ -1175,6 +1175,8 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
             rc = enqueue(_scratch(cache.device, size, stream), size)
     else:
         _same_device(q, workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
         rc = enqueue(workspace, workspace.numel() * workspace.element_size())
     if rc != OK:
         raise LinError(rc, "lin_paged_attention")
