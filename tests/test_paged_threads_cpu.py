@@ -17,7 +17,7 @@ class Library:
         self.launches = []  # (workspace, call)
 
     def lin_paged_attention(self, *args):
-        workspace, call = args[13], threading.get_ident()
+        workspace, call = args[12], threading.get_ident()
         self.launches.append((workspace, call))
         time.sleep(0.001)
         self.launches.append((workspace, call))
