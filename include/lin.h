@@ -641,8 +641,8 @@ typedef struct {
  * after the other. The arrays are on the DEVICE and are read when the kernels run, so a captured graph
  * follows them. */
 typedef struct {
-    int sequences;
-    int tokens;               /* rows of the packed matrices */
+    int sequences;            /* at most 2^30, for attention 2^24 */
+    int tokens;               /* rows of the packed matrices; for attention at most 2^28 */
     const int* q_start;       /* sequences + 1: sequence b's new tokens are rows q_start[b] to q_start[b + 1] - 1; ascending */
     const int* kv_len;        /* sequences: tokens that sequence b has in the cache, the new ones included */
     const int* block_table;   /* sequence b's tokens i * page_size .. lie in page block_table[b * table_stride + i] */

@@ -941,6 +941,11 @@ def _raw_stream(stream, index):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _check_sizes(t, what):
+    if max(t.shape) > 2 ** 31 - 1:
+        raise ValueError(f"{what}: sizes are 32 bits, got {tuple(t.shape)}")
+
+
 def _check_heads(t, dtype, what, index=None):
     """(rows, heads, width, row stride) of an N x H x D tensor (of ``dtype``, on CUDA
     device ``index``) whose rows hold their heads one after the other, any distance apart."""
@@ -949,6 +954,7 @@ def _check_heads(t, dtype, what, index=None):
     if index is not None and t.get_device() != index:
         raise ValueError(f"{what} must be on cuda:{index}, got {t.device}")
     N, H, D = t.shape
+    _check_sizes(t, what)
     s0, s1, s2 = t.stride()
     if (s2 != 1 and D > 1) or (s1 != D and H > 1):
         raise ValueError(f"{what}: a row must hold its heads one after the other")
@@ -1019,6 +1025,7 @@ class KVCache(_Fixed):
                 raise ValueError(f"{what} must be a bf16 CUDA tensor of pages x heads x page_size x width")
         if k.shape != v.shape or k.stride() != v.stride():
             raise ValueError("k and v must have the same shape and strides")
+        _check_sizes(k, "k")
         _same_device(k, v)
         self.k, self.v = k, v
         self.pages, self.heads, self.page_size, self.head_dim = k.shape
@@ -1050,6 +1057,7 @@ class KVBatch(_Fixed):
         if (not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or
                 block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
             raise ValueError(f"block_table must be an int32 CUDA tensor of {B} rows, each contiguous")
+        _check_sizes(block_table, "block_table")
         _same_device(kv_len, q_start, block_table)
         self.q_start, self.kv_len, self.block_table = q_start, kv_len, block_table
         self.sequences = B

@@ -1397,7 +1397,7 @@ int cache_ok(const lin_kv_cache* c, const lin_kv_batch* b) {
         return LIN_ERR_ARG;
     if ((c->page_size & (c->page_size - 1)) != 0 || c->page_size < 8 || c->page_size > 4096 ||
         (c->head_dim != 64 && c->head_dim != 128) || c->heads > 65535 || b->table_stride > kMaxStride ||
-        (long long)b->table_pages * c->page_size > (1 << 30))
+        (long long)b->table_pages * c->page_size > (1 << 30) || b->sequences > (1 << 30))
         return LIN_ERR_UNSUPPORTED;
     if (b->tokens > 0 && b->sequences > 0 && (!b->q_start || !b->kv_len || (b->table_pages > 0 && !b->block_table)))
         return LIN_ERR_ARG;
@@ -1545,7 +1545,8 @@ int lin_paged_attention(lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_ba
     if (!q || !out || ldq < width || ldo < width) return LIN_ERR_ARG;
     // scaled scores and their differences are fp32
     if (scale > 0.f && !(scale >= 0x1p-100f && scale <= 0x1p100f)) return LIN_ERR_ARG;
-    if (ldq > kMaxStride || ldo > kMaxStride || batch->sequences > (1 << 24)) return LIN_ERR_UNSUPPORTED;
+    // positions, clipped to +-1.5 * 2^30, plus a row's number are 32 bits in the kernels
+    if (ldq > kMaxStride || ldo > kMaxStride || batch->sequences > (1 << 24) || N > (1 << 28)) return LIN_ERR_UNSUPPORTED;
     if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) % 16 != 0 || ldq % 8 != 0 || ldo % 8 != 0 ||
         (uintptr_t)lse % 4 != 0)
         return LIN_ERR_ALIGN;
