@@ -597,9 +597,10 @@ typedef struct {
 } lin_rotary;
 
 /* turns[i] (host) from frequencies[i] (host, radians per position, finite): the
- * fixed-point form that lin_rotary holds on the device. The kernels multiply it by
- * the position modulo 2^64, which is the angle modulo one turn, without
- * rounding, for any 64-bit position. */
+ * fixed-point form that lin_rotary holds on the device, off by at most 0.6 of its unit
+ * for frequencies up to 2^40 in size. The kernels multiply it by the position modulo 2^64, which
+ * is p times the entry modulo one turn, without rounding, for any 64-bit position p: the angle
+ * is off by at most |p| 2^-62 radians. */
 LIN_API int lin_rotary_turns(const double* frequencies, int n, unsigned long long* turns);
 
 /* y = x with every head rotated by its row's position. Row n, head h at
@@ -609,7 +610,7 @@ LIN_API int lin_rotary_turns(const double* frequencies, int n, unsigned long lon
  *               interleave (column ranges of one matrix).
  *   positions : N of LIN_TYPE_INT32 or LIN_TYPE_INT64 (positions_type), any value.
  *   D         : 1 to 1024.
- * Angles, cosines and products in fp32 (the angle itself is exact), one rounding to
+ * Angles, cosines and products in fp32 (from the exact product of position and table entry), one rounding to
  * the type. A NaN or infinity reaches its own pair only. Fast when addresses and
  * strides are multiples of 16 bytes and the pairs fill them; right for any. No workspace. Reads and writes only
  * after the previous kernel on the stream has finished. */

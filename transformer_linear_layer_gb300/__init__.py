@@ -869,7 +869,8 @@ class Rotary(_Fixed):
 
     or by ``frequencies`` (dim/2 radians per position) in place of all of these.
     ``scale`` replaces the factor on the rotated elements. The plan holds its
-    table on ``device``; positions may be any 64-bit integers."""
+    table on ``device``; positions p may be any 64-bit integers (the angle is that of the
+    frequencies to |p| 2^-62 radians)."""
 
     def __init__(self, dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str | None = None,
                  factor: float = 1.0, original_length: int | None = None, fast: float = 32.0, slow: float = 1.0,

@@ -1269,10 +1269,16 @@ int lin_rotary_turns(const double* frequencies, int n, unsigned long long* turns
     for (int i = 0; i < n; ++i)
         if (!std::isfinite(frequencies[i])) return LIN_ERR_ARG;
     for (int i = 0; i < n; ++i) {
-        const double t = frequencies[i] / 6.283185307179586476925;
-        double part = t - std::floor(t);  // [0, 1], 1 when a tiny negative rounds up
-        if (part >= 1.0) part = 0.0;
-        turns[i] = static_cast<unsigned long long>(std::ldexp(part, 64));
+        // f / 2 pi as the sum of a double and what it lacks, 1 / 2 pi being the sum of two: 106 bits, so that the
+        // 64 of the fraction are right (to 0.6 of the last, with its rounding) up to f = 2^40.
+        constexpr double kInv = 0x1.45f306dc9c883p-3, kInvRest = -0x1.6b01ec5417056p-57;
+        const double f = std::fabs(frequencies[i]);
+        const double t = f * kInv, rest = std::fmod(std::fma(f, kInv, -t) + f * kInvRest, 1.0);
+        const double part = std::ldexp(std::fmod(t, 1.0), 64), whole = std::floor(part);
+        const double low = (part - whole) + std::ldexp(rest, 64);  // below 2^64 in size
+        const unsigned long long add = static_cast<unsigned long long>(std::floor(std::fabs(low) + 0.5));
+        const unsigned long long turn = static_cast<unsigned long long>(whole) + (low < 0.0 ? 0ull - add : add);
+        turns[i] = std::signbit(frequencies[i]) ? 0ull - turn : turn;
     }
     return LIN_OK;
 }
