@@ -100,3 +100,10 @@ def test_the_model_sees_a_slot_that_two_producers_share():
     assert overwrites(shared(5), PROGRAMS["one ends first"])
     assert not overwrites(shared(5), PROGRAMS["both"])
     assert not overwrites(shared(4), PROGRAMS["one ends first"])
+
+
+def test_the_joining_kernel_reads_no_constants():
+    """It may start before the attention kernel has written what it reads (it waits inside), so loads of data that is
+    constant while a kernel runs are not for it."""
+    join = open(os.path.join(os.path.dirname(SOURCE), "paged_join.cu")).read()
+    assert not re.search(r"__ldg\s*\(|ld\.global\.nc|__restrict__", join)

@@ -5,7 +5,8 @@
 // few parts (nearly always two) the block's threads have different rows, with many (a long context
 // on few heads is cut into as many parts as there are blocks) they share a row's parts.
 // Bound by latency: the parts lie in the L2, and everything that a thread reads is asked
-// for at once. (A warp per row with a loop over the parts took 19 us behind the 69 of
+// for at once, past the L1 (not by loads of constant data: this kernel may have started before the
+// attention kernel wrote the parts). (A warp per row with a loop over the parts took 19 us behind the 69 of
 // 4 x 512 tokens over 8704 keys, 12 heads of 64.)
 #include <math.h>
 
@@ -52,8 +53,8 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const PagedAr
             float4 x[kPjFew];
 #pragma unroll
             for (int i = 0; i < kPjFew; ++i) {
-                st[i] = i < parts ? __ldg(a.stats + at(i) + row) : make_float2(-INFINITY, 0.f);
-                x[i] = i < parts ? __ldg(sums + (at(i) + row) * LANES) : make_float4(0.f, 0.f, 0.f, 0.f);
+                st[i] = i < parts ? __ldcg(a.stats + at(i) + row) : make_float2(-INFINITY, 0.f);
+                x[i] = i < parts ? __ldcg(sums + (at(i) + row) * LANES) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float m = st[0].x, total = 0.f;
 #pragma unroll
@@ -80,8 +81,8 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const PagedAr
 #pragma unroll
             for (int k = 0; k < kPjMany; ++k) {
                 const int i = i0 + k * SLOTS;
-                st[k] = i < parts ? __ldg(a.stats + at(i) + row) : make_float2(-INFINITY, 0.f);
-                x[k] = i < parts ? __ldg(sums + (at(i) + row) * LANES) : make_float4(0.f, 0.f, 0.f, 0.f);
+                st[k] = i < parts ? __ldcg(a.stats + at(i) + row) : make_float2(-INFINITY, 0.f);
+                x[k] = i < parts ? __ldcg(sums + (at(i) + row) * LANES) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
             for (int k = 0; k < kPjMany; ++k) top = fmaxf(top, st[k].x);
