@@ -303,29 +303,6 @@ bool paged_args(const PagedProblem& p, int grid, int R, PagedArgs* a);
 // The joining kernel, behind an attention kernel of `grid` blocks (paged_join.cu).
 int launch_paged_join(const PagedProblem& p, const PagedArgs& a, int grid, int R);
 
-// A wait that sleeps: the barrier wakes the thread, or the hint's time has passed. (Polling
-// takes issue slots from the warps of the same scheduler that compute.) Bounded like mbar_wait.
-__device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity), "r"(1000000u)
-        : "memory");
-    return done != 0;
-}
-__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity) {
-    if (mbar_try_wait_long(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
-    for (uint32_t i = 1; i < kWaitIters; ++i) {
-        if (mbar_try_wait_long(bar, parity)) return true;
-        if (global_ns() - t0 > kWaitNs) return false;
-    }
-    return false;
-}
-
 // 4-D TMA load of a box at (element, slot, head, page), 3-D at (element, head, row).
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
     asm volatile(
