@@ -863,11 +863,25 @@ class Rotary(_Fixed):
                 divided by the factor, the fastest kept
       "yarn"    by parts: pairs that turn at most ``slow`` times in
                 ``original_length`` positions are divided by the factor, those that
-                turn ``fast`` times or more are kept, with a ramp between; the rotated
-                elements are multiplied by 0.1 ln(factor) + 1 (Peng et al., "YaRN:
-                Efficient Context Window Extension of Large Language Models")
+                turn ``fast`` times or more are kept, with a ramp between that is linear
+                in the number of turns; the rotated elements are multiplied by
+                0.1 ln(factor) + 1 (Peng et al., "YaRN: Efficient Context Window Extension
+                of Large Language Models", whose text defines it so)
 
-    or by ``frequencies`` (dim/2 radians per position) in place of all of these.
+    or by ``frequencies`` (dim/2 radians per position) in place of all of these. Many
+    checkpoints that name YaRN were made with another ramp, linear in the pair's
+    index i from the pair that turns ``fast`` times to the one that turns ``slow`` times, and
+    a model has to be served with the one that it was trained with: the two differ by up to a
+    factor of 2.3 (dim 128, base 10000, original_length 4096, factor 8). For that one, pass::
+
+        place = lambda turns: dim * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
+        low, high = math.floor(place(fast)), math.ceil(place(slow))
+        keep = [1 - min(1, max(0, (i - low) / (high - low))) for i in range(dim // 2)]
+        plain = [base ** (-2 * i / dim) for i in range(dim // 2)]
+        Rotary(dim, frequencies=[f * (k + (1 - k) / factor) for f, k in zip(plain, keep)],
+               scale=0.1 * math.log(factor) + 1)
+
+    (without floor and ceil where the model's configuration says so).
     ``scale`` replaces the factor on the rotated elements. The plan holds its
     table on ``device``; positions p may be any 64-bit integers (the angle is that of the
     frequencies to |p| 2^-62 radians)."""
