@@ -609,7 +609,8 @@ LIN_API int lin_rotary_turns(const double* frequencies, int n, unsigned long lon
  *               otherwise no row's heads of y may lie over x's. Rows of equal stride may
  *               interleave (column ranges of one matrix).
  *   positions : N of LIN_TYPE_INT32 or LIN_TYPE_INT64 (positions_type), any value.
- *   D         : 1 to 1024.
+ *   D         : 1 to 1024. H up to 65535 (more where heads are narrow), H * D up to 2^27, ldx and
+ *               ldy up to 2^30; LIN_ERR_UNSUPPORTED beyond.
  * Angles, cosines and products in fp32 (from the exact product of position and table entry), one rounding to
  * the type. A NaN or infinity reaches its own pair only. Fast when addresses and
  * strides are multiples of 16 bytes and the pairs fill them; right for any. No workspace. Reads and writes only
@@ -660,6 +661,7 @@ typedef struct {
  *              may be q (ldqo == ldq). Both NULL (H 0): keys and values only. Without a
  *              rotary plan they must be.
  *   k, v     : tokens x cache->heads heads of head_dim, bf16, rows ldk and ldv apart.
+ *              H * head_dim up to 2^27, all row strides up to 2^30 (LIN_ERR_UNSUPPORTED beyond).
  *   positions: NULL, or one per row (LIN_TYPE_INT32 or LIN_TYPE_INT64), used for the rotation only.
  * Rows of no sequence are left out: nothing is written for them. A token whose
  * position lies outside the table, or whose table entry is not a page of the cache, is not
@@ -684,8 +686,8 @@ LIN_API int lin_cache_append(lin_ctx* ctx, const lin_kv_cache* cache, const lin_
  * left as they were. kv_len is taken as 0 below 0, and up to table_pages * page_size; what lies on a page that is
  * none of the cache's reads as zeros. Whatever the arrays hold, nothing outside the
  * operands is read or written.
- *   q, out : tokens x H heads of head_dim, bf16, 16-byte aligned, rows ldq and ldo apart (multiples of 8).
- *   H      : a multiple of cache->heads, at most 128 times as many.
+ *   q, out : tokens x H heads of head_dim, bf16, 16-byte aligned, rows ldq and ldo apart (multiples of 8, up to 2^30).
+ *   H      : a multiple of cache->heads, at most 128 times as many, and at most 65535.
  *   scale  : 2^-100 to 2^100; 0 selects 1/sqrt(head_dim).
  *   max_new: about how many new tokens the longest sequence has (0: as many as the average); it picks the
  *            kernel, and any value gives right results.

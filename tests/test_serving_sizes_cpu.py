@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import transformer_linear_layer_gb300 as tll
-from test_serving_abi_cpu import append, attention, at, batch, ctx, needs_no_gpu  # noqa: F401
+from test_serving_abi_cpu import append, attention, at, batch, cache, ctx, needs_no_gpu, rotary  # noqa: F401
 
 
 def wide(n):
@@ -68,3 +68,16 @@ def test_the_binding_counts_in_32_bits():
     with pytest.raises(ValueError):
         tll.KVBatch(Huge((big + 1,), i32), Huge((big,), i32), Huge((big, 1), i32))
     assert tll.KVBatch(Huge((2,), i32), Huge((1,), i32), Huge((1, 9), i32)).sequences == 1
+
+
+@needs_no_gpu
+def test_the_widest_rows(ctx):  # noqa: F811
+    far = dict(y=at(0) + (1 << 45), N=2, D=1024)
+    most, less = 1 << 17, (1 << 17) + 1
+    for form in ("forward", "backward"):
+        assert rotary(ctx, form, H=most, ldx=1 << 30, ldy=1 << 30, **far) == tll.ERR_CUDA  # past the checks
+        assert rotary(ctx, form, H=less, ldx=1 << 30, ldy=1 << 30, **far) == tll.ERR_UNSUPPORTED
+        assert rotary(ctx, form, H=3, ldx=(1 << 30) + 1, ldy=1 << 30, **far) == tll.ERR_UNSUPPORTED
+    many = cache(heads=512, ps=512 * 16 * 64)
+    assert attention(ctx, c=many, H=65536, ldq=1 << 22, ldo=1 << 22) == tll.ERR_UNSUPPORTED
+    assert append(ctx, H=(1 << 21) + 1, ldq=1 << 28, ldqo=1 << 28, c=many, ldk=1 << 15, ldv=1 << 15) == tll.ERR_UNSUPPORTED
