@@ -947,6 +947,12 @@ def _context(index):
     return _contexts.get(index) or default_context(index)
 
 
+def _on_device(ctx, index):
+    if ctx.device != index:
+        raise ValueError(f"the tensors are on cuda:{index}, the context is of cuda:{ctx.device}")
+    return ctx
+
+
 def _raw_stream(stream, index):
     import torch
 
@@ -1000,7 +1006,7 @@ def _rotary(call, x, positions, rotary, out, ctx, stream):
         No, Ho, Do, ldy = _check_heads(out, x.dtype, "out", index)
         if (No, Ho, Do) != (N, H, D):
             raise ValueError(f"out must have shape {(N, H, D)}, got {tuple(out.shape)}")
-    ctx = ctx or _context(index)
+    ctx = _context(index) if ctx is None else _on_device(ctx, index)
     rc = getattr(_loaded(), call)(ctx._h, N, H, D, x.data_ptr(), ldx, out.data_ptr(), ldy, kind,
                                   positions.data_ptr(), ptype, rotary._ref, _raw_stream(stream, index))
     if rc != OK:
@@ -1125,7 +1131,7 @@ def cache_append(q, k, v, cache: KVCache, batch: KVBatch, rotary: Rotary | None 
     elif q_out is not None:
         raise ValueError("q_out without q")
     ptype = TYPE_INT64 if positions is None else _check_positions(positions, N, index)
-    ctx = ctx or _context(index)
+    ctx = _context(index) if ctx is None else _on_device(ctx, index)
     rc = _loaded().lin_cache_append(ctx._h, cache._ref, batch._ref(N), H, _ptr(q), ldq, _ptr(q_out), ldo,
                                     k.data_ptr(), ldk, v.data_ptr(), ldv, _ptr(positions), ptype,
                                     None if rotary is None else rotary._ref, _raw_stream(stream, index))
@@ -1167,7 +1173,7 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     elif lse is not None:
         _check(lse, torch.float32, (N, H), "lse")
         _same_device(q, lse)
-    ctx = ctx or _context(index)
+    ctx = _context(index) if ctx is None else _on_device(ctx, index)
     hint = 0 if max_new is None else int(max_new)
     raw = _raw_stream(stream, index)
 
@@ -1224,7 +1230,7 @@ def _default_stream(index) -> _DefaultStream:
 def paged_attention_workspace(cache: KVCache, batch: KVBatch, tokens: int, heads: int, max_new: int = 0,
                               ctx: Context | None = None) -> int:
     """Bytes of workspace that :func:`paged_attention` needs for such a call."""
-    ctx = ctx or default_context(cache.index)
+    ctx = default_context(cache.index) if ctx is None else _on_device(ctx, cache.index)
     size = ctypes.c_size_t()
     rc = library().lin_paged_attention_workspace(ctx._h, cache._ref, batch._ref(tokens), heads, max_new,
                                                  ctypes.byref(size))
