@@ -690,7 +690,9 @@ LIN_API int lin_cache_append(lin_ctx* ctx, const lin_kv_cache* cache, const lin_
  *   H      : a multiple of cache->heads, at most 128 times as many, and at most 65535.
  *   scale  : 2^-100 to 2^100; 0 selects 1/sqrt(head_dim).
  *   max_new: about how many new tokens the longest sequence has (0: as many as the average); it picks the
- *            kernel, and any value gives right results.
+ *            kernel, and any value gives right results. The average of a long prompt among single tokens can pick the one
+ *            for few tokens, which reads the prompt's keys once per 16 rows (63 single tokens and a prompt of 900, 12 heads
+ *            of 64: 161 us instead of 138).
  *   workspace: DEVICE, 16-byte aligned, of lin_paged_attention_workspace's size for the same max_new: parts of
  *            items that several blocks share. NULL: the context's own (LIN_ERR_WORKSPACE when it is too
  *            small); calls that may run at the same time, captured ones included, need one each.

@@ -1150,7 +1150,8 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     (at most 128) of the cache's. scale: of the scores, default (or 0) 1/sqrt(width). causal: each token sees the keys up to its own place; otherwise all of its
     sequence's (a cross attention over an encoder's states). max_new: about how many new
     tokens the longest sequence has (default: the average), which picks the kernel; any value is
-    right. Returns out (like q, contiguous), or (out, lse) with lse tokens x heads fp32 when ``with_lse`` or an lse
+    right, but the average misjudges a long prompt among single tokens (63 of them and a prompt of 900, 12 heads of 64:
+    161 us instead of 138). Returns out (like q, contiguous), or (out, lse) with lse tokens x heads fp32 when ``with_lse`` or an lse
     tensor is given. Rows that belong to no sequence are not written. workspace: a uint8 tensor of
     :func:`paged_attention_workspace` bytes, for one call at a time. By default, calls on the default stream share one
     that is kept for the device (up to 40 MB on a GB300), and any other call has its own from torch's allocator."""

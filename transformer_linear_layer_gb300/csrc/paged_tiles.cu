@@ -51,8 +51,16 @@ constexpr int kPtLaunch = 168, kPtLow = 72, kPtHigh = 216;
 static_assert(128 * kPtLow + 256 * kPtHigh <= kPtThreads * kPtLaunch, "register split");
 constexpr uint32_t kPtTmem = 512;
 constexpr int kPtParts = 4;             // parts of items that are described at a time
-constexpr int kPtLead = 2;              // blocks that an item's start and end cost (2 x 4096 tokens, 16 heads of 128
-                                        // on 2: 179 us with 1, 150 with 2 and 3, 156 with 6; 4 x 512 over 8704: 71, 72, 76)
+// Blocks that an item's start and end cost. Measured (us) with              0    1    2    3    4    6
+//     2 prompts of 4096, 16 heads of 128 on 2                             209  164  136  131  132  133
+//     4 prompts of 2048, 12 heads of 64                                    74   63   59   59   58   58
+//     4 chunks of 512 over 8704, 12 heads of 64                            68   67   67   68   68   70
+//     the same, 16 heads of 128 on 2                                      114  115  114  114  114  116
+//     8 x 77 to 101 queries over 1500, 12 heads of 64, full              21.6 22.2 21.3 22.8 22.3 23.4
+//     the same, 16 heads of 128 on 4                                     26.9 31.2 29.6 29.3 28.6 29.8
+//     33 sequences, a quarter with 200 to 301 tokens, 20 heads of 64 on 4   59   55   53   53   53   55
+//     the same, 32 heads of 128 on 8                                      123  114  110  104  104  106
+constexpr int kPtLead = 2;
 constexpr float kPtRise = 65536.f;      // what 64 probabilities may add up to before their reference moves
 
 template <int D>
@@ -62,6 +70,7 @@ struct PtShape {
     // may be at most one phase ahead of it: each ring has one producer, which fills every phase of its
     // slots itself, and each group releases every tile of both. (Were a slot to alternate between the two producers, one of them
     // would wait for it two phases after its last fill, and take the release before that for the one it waits for.)
+    // Heads of 128 with 2 slots for K and 3 for V: the same times (2 x 4096 tokens 135.8 us and 136.4).
     static constexpr int KS = D == 64 ? 5 : 3, VS = D == 64 ? 5 : 2, S = KS + VS;
     static constexpr size_t kSmem = 1024 + (2 + S) * (size_t)kTile;
     // TMEM columns of a group: S (128), O (D) and P (64). Heads of 64 leave room for P beside

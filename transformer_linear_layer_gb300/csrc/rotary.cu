@@ -315,9 +315,14 @@ int start_width(const RotaryProblem& p) {
         if (part.heads > 0) wide = wide && fits(part.src, part.ld_src) && fits(part.dst, part.ld_dst);
     // the cache's own addresses and strides are multiples of 16 bytes
     if (!wide) return start<T, 1, INTER, 1>(p);
-    // Few rows: one head a thread, so that the row is done by as many threads as it has (64 rows of
-    // 12 + 24 heads of 64: 2.7 us; with four 3.0). Many: accesses in flight count (5757 rows of 48 heads of 128: 37.6 us
-    // with one head a thread, 35.5 with two, 25.7 with four).
+    // Few rows: one head a thread, so that the row is done by as many threads as it has. Many: accesses in
+    // flight count. Measured (us, with one head a thread and with four; device time):
+    //     rows                          64         400         608        1024        2048        5760
+    //     append, 12 + 24 heads of 64   2.6 3.8    2.9 3.9     3.1 4.0    3.8 4.0     5.7 4.6    12.0  9.5
+    //     append, 32 + 16 heads of 128  2.7 3.4    3.8 3.8     5.7 4.1    8.2 5.6    14.0 8.9    38.1 26.9
+    //     rotary, 24 heads of 64        1.7 2.2    1.8 2.3     2.1 2.4    2.5 2.4     3.0 3.1     5.6  4.8
+    //     rotary, 10 of 128 in fp32     1.9 2.3    2.0 2.3     2.2 2.4    2.9 3.0     3.7 4.0     7.3  6.9
+    // so that the border, 608 rows here, is late for wide rows and early for narrow ones, by 1.6 us at most.
     return p.N < 4 * p.sm_count ? start<T, V, INTER, 1>(p) : start<T, V, INTER, kRtHeads>(p);
 }
 
