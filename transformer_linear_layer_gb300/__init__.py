@@ -962,8 +962,11 @@ def _raw_stream(stream, index):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_MOST = 2 ** 31 - 1  # sizes are ints
+
+
 def _check_sizes(t, what):
-    if max(t.shape) > 2 ** 31 - 1:
+    if max(t.shape) > _MOST:
         raise ValueError(f"{what}: sizes are 32 bits, got {tuple(t.shape)}")
 
 
@@ -975,7 +978,8 @@ def _check_heads(t, dtype, what, index=None):
     if index is not None and t.get_device() != index:
         raise ValueError(f"{what} must be on cuda:{index}, got {t.device}")
     N, H, D = t.shape
-    _check_sizes(t, what)
+    if N > _MOST or H > _MOST or D > _MOST:
+        _check_sizes(t, what)
     s0, s1, s2 = t.stride()
     if (s2 != 1 and D > 1) or (s1 != D and H > 1):
         raise ValueError(f"{what}: a row must hold its heads one after the other")
@@ -1147,14 +1151,19 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     (:func:`cache_append`).
 
     q: tokens x query heads x width, bf16, rows any multiple of 8 elements apart; query heads a multiple
-    (at most 128) of the cache's. scale: of the scores, default (or 0) 1/sqrt(width). causal: each token sees the keys up to its own place; otherwise all of its
-    sequence's (a cross attention over an encoder's states). max_new: about how many new
-    tokens the longest sequence has (default: the average), which picks the kernel; any value is
-    right, but the average misjudges a long prompt among single tokens (63 of them and a prompt of 900, 12 heads of 64:
-    161 us instead of 138). Returns out (like q, contiguous), or (out, lse) with lse tokens x heads fp32 when ``with_lse`` or an lse
-    tensor is given. Rows that belong to no sequence are not written. workspace: a uint8 tensor of
-    :func:`paged_attention_workspace` bytes, for one call at a time. By default, calls on the default stream share one
-    that is kept for the device (up to 40 MB on a GB300), and any other call has its own from torch's allocator."""
+    (at most 128) of the cache's. scale: of the scores, default (or 0) 1/sqrt(width). causal: each token sees the keys up
+    to its own place; otherwise all of its sequence's (a cross attention over an encoder's states).
+
+    max_new: about how many new tokens the longest sequence has (default: the average), which picks the kernel; any
+    value is right, but the average misjudges a long prompt among single tokens (63 of them and a prompt of 900, 12
+    heads of 64: 161 us instead of 138).
+
+    Returns out (like q, contiguous), or (out, lse) with lse tokens x heads fp32 when ``with_lse`` or an lse tensor is
+    given. Rows that belong to no sequence are not written.
+
+    workspace: a uint8 tensor of :func:`paged_attention_workspace` bytes, for one call at a time. By default, calls on
+    the default stream share one that is kept for the device (up to 40 MB on a GB300), and any other call has its own
+    from torch's allocator."""
     import torch
 
     index = cache.index
@@ -1177,12 +1186,9 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     ctx = _context(index) if ctx is None else _on_device(ctx, index)
     hint = 0 if max_new is None else int(max_new)
     raw = _raw_stream(stream, index)
-
-    def enqueue(workspace, size):
-        return _loaded().lin_paged_attention(ctx._h, cache._ref, batch._ref(N), H, q.data_ptr(), ldq, out.data_ptr(), ldo,
-                                             _ptr(lse), int(bool(causal)), 0.0 if scale is None else float(scale), hint,
-                                             workspace.data_ptr(), size, raw)
-
+    call = _loaded().lin_paged_attention
+    args = (ctx._h, cache._ref, batch._ref(N), H, q.data_ptr(), ldq, out.data_ptr(), ldo, _ptr(lse), int(bool(causal)),
+            0.0 if scale is None else float(scale), hint)
     if workspace is None:
         # (the size goes by the device too, and all contexts of a cache are on its own)
         key = (H, hint, N if hint == 0 else 0, batch.sequences if hint == 0 else 0)
@@ -1200,14 +1206,15 @@ def paged_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
             with shared.turn:
                 if shared.workspace is None or shared.workspace.numel() < size:
                     shared.workspace = _scratch(cache.device, size, None)
-                rc = enqueue(shared.workspace, size)
+                rc = call(*args, shared.workspace.data_ptr(), size, raw)
         else:
-            rc = enqueue(_scratch(cache.device, size, stream), size)
+            workspace = _scratch(cache.device, size, stream)
+            rc = call(*args, workspace.data_ptr(), size, raw)
     else:
         _same_device(q, workspace)
         if not workspace.is_contiguous():
             raise ValueError("the workspace must be contiguous")
-        rc = enqueue(workspace, workspace.numel() * workspace.element_size())
+        rc = call(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
     if rc != OK:
         raise LinError(rc, "lin_paged_attention")
     return (out, lse) if lse is not None else out
