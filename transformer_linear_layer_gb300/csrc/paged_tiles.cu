@@ -22,16 +22,19 @@
 //               (bf16 keeps its relative precision; the argument of an exponential stays below 16, and its
 //               rounding below 2^-20). So nothing waits for a maximum and none is taken; in the
 //               rare case that the scores have risen, O is scaled and the 64 keys are exponentiated again.
+//               The price: the probability of a row's top key is rounded like the others and not 1 (error against
+//               64 bits 0.0023 of the norm where a maximum gives 0.0018; the output's rounding alone is 0.0017).
 // Keys past the last one that a row of the tile sees are not loaded where they fill a box, and their
 // values are set to zero in shared memory where they do not: a probability of 0 must not meet a
 // NaN in slots that were never written.
 // Every wait is bounded (about 1 s); a block that gives up sets the status word.
 //
-// Measured (GB300, with the joining kernel): 2 prompts of 4096 tokens, 16 heads of 128 on 2: 137 us, 1004
-// TF/s of the visible pairs' products (3100 cycles a block of 256 x 128, 2070 of them products when
-// nothing else is done); 4 chunks of 512 over 8704 keys, 12 heads of 64: 67 us, 790 TF/s (2500 cycles a
-// block, 1160 of products and 1250 of exponentials with two warps a scheduler). Tensor pipe 45 and 36 %,
-// DRAM 4 and 23 %: bound by a group's chain of scores, exponentials and products, and by the waits
+// Measured (GB300, with the joining kernel): 2 prompts of 4096 tokens, 16 heads of 128 on 2: 138 us, 992
+// TF/s of the visible pairs' products; 4 chunks of 512 over 8704 keys, 16 heads of 128 on 2: 114 us, 1240 TF/s
+// (3300 cycles a block of 256 x 128 in a long item, with stamps, 2070 of them products when
+// nothing else is done); the same chunks, 12 heads of 64: 68 us, 780 TF/s (2500 cycles a
+// block, 2700 with stamps, 1160 of products and 1250 of exponentials with two warps a scheduler). Tensor pipe 51 %
+// (prompts) and 35 % (heads of 64), DRAM 4 and 23 %: bound by a group's chain of scores, exponentials and products, and by the waits
 // between them, which queue behind the exponentials.
 #include <math.h>
 

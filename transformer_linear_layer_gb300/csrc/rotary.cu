@@ -22,7 +22,7 @@
 // first of the sizes below).
 // Measured (GB300): 8192 x 24 heads of 64, bf16, halves 7.9 us (6.4 TB/s); 2331 x 10 heads of 128, fp32,
 // half of each head, neighbours 3.9 us (6.2 TB/s); one row 1.4 us; append of 5757 rows of 32 + 16
-// heads of 128 25.7 us (5.5 TB/s), of 64 rows of 12 + 24 heads of 64 2.7 us.
+// heads of 128 26.0 us (5.4 TB/s), of 64 rows of 12 + 24 heads of 64 2.7 us.
 #include <limits.h>
 #include <math.h>
 
