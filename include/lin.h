@@ -700,7 +700,9 @@ LIN_API int lin_cache_append(lin_ctx* ctx, const lin_kv_cache* cache, const lin_
  * one rounding of the output. Sums are split by the lengths and the device alone: results repeat bit
  * for bit. A NaN or infinity in a key or value that some row of a sequence's new tokens sees may
  * reach all of that sequence's rows; slots that no row sees may hold anything. Reads and writes
- * only after the previous kernel on the stream has finished. */
+ * only after the previous kernel on the stream has finished. Waits inside the kernels end after about a second
+ * (lin_check_device then reports it): none lasts nearly as long, unless one block has more than 10^8 keys of one
+ * head and tile to itself. */
 LIN_API int lin_paged_attention(lin_ctx* ctx, const lin_kv_cache* cache, const lin_kv_batch* batch, int H, const void* q,
                                 long long ldq, void* out, long long ldo, float* lse, int causal, float scale,
                                 int max_new, void* workspace, size_t workspace_bytes, void* stream);

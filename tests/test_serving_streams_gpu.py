@@ -105,3 +105,34 @@ def test_results_are_memory_of_the_calls_stream(name):
     assert not held & {t.data_ptr() for t in again}
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(again, want))
+
+
+def test_the_legacy_streams_handle_is_the_default_stream():
+    cache, batch, q, N = setup()
+    want = tll.paged_attention(q, cache, batch)
+    torch.cuda.synchronize()
+    assert tll._torch_stream(1, q.device) == torch.cuda.default_stream()
+    out = tll.paged_attention(q, cache, batch, stream=1)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("name", ["forward", "rotary_forward", "cache_append", "paged_attention"])
+def test_calls_on_a_given_stream_in_a_capture(name):
+    """On the captured stream itself, and on one that is forked from it and joined: the results are the graph's memory."""
+    call = calls()[name]
+    want = [t.clone() for t in tensors(call(None))]
+    torch.cuda.synchronize()
+    s, side, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        first = tensors(call(s))
+        side.wait_stream(s)
+        second = tensors(call(side))
+        s.wait_stream(side)
+    for t in first + second:
+        t.fill_(0)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for got in (first, second):
+        assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))

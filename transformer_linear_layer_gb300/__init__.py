@@ -338,13 +338,14 @@ def _stream_ptr(stream, device):
 
 
 def _torch_stream(stream, device):
-    """torch's stream of a stream object or a raw handle (to torch, an external stream of handle 0 is any of its own)."""
+    """torch's stream of a stream object or a raw handle. 0 and 1 are the default stream's (to torch, external streams of
+    these handles are ones of its own)."""
     import torch
 
     if isinstance(stream, torch.cuda.Stream):
         return stream
     raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    return torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(raw, device=device) if raw > 1 else torch.cuda.default_stream(device)
 
 
 def _empty(shape, dtype, device, stream):
