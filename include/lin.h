@@ -695,7 +695,8 @@ LIN_API int lin_cache_append(lin_ctx* ctx, const lin_kv_cache* cache, const lin_
  *            of 64: 161 us instead of 138).
  *   workspace: DEVICE, 16-byte aligned, of lin_paged_attention_workspace's size for the same max_new: parts of
  *            items that several blocks share. NULL: the context's own (LIN_ERR_WORKSPACE when it is too
- *            small); calls that may run at the same time, captured ones included, need one each.
+ *            small); calls that may run at the same time, captured ones included, need one each, and so do calls that
+ *            several threads make at once, on one stream too (a call enqueues two kernels, one right after the other).
  * Arithmetic: bf16 products summed in fp32, softmax in fp32, probabilities rounded to bf16 for the product with V,
  * one rounding of the output. Sums are split by the lengths and the device alone: results repeat bit
  * for bit. A NaN or infinity in a key or value that some row of a sequence's new tokens sees may
